@@ -64,6 +64,7 @@ extern "C" {
 #define REPLAYSSM_DEVERR_CORRUPT 8         /* head/h/p out of range; sequence skipped     */
 #define REPLAYSSM_DEVERR_STALE 16          /* snapshot of a sequence with unfolded records */
 #define REPLAYSSM_DEVERR_INDEX 32          /* sequence index outside 0..B-1; skipped       */
+#define REPLAYSSM_DEVERR_RANGE 64          /* token table or length out of range; see calls */
 
 /* ---- configuration ------------------------------------------------------ */
 enum replayssm_kind {
@@ -408,6 +409,162 @@ int replayssm_conv_step(const replayssm_conv_config* cfg, const replayssm_conv_s
  * a outside 0..pend is clamped and flagged (REPLAYSSM_DEVERR_ACCEPT); pend = 0. */
 int replayssm_conv_accept(const replayssm_conv_config* cfg, const replayssm_conv_state* st,
                           const int32_t* accepted, void* stream);
+
+/* ==== the prompt side =====================================================
+ * A layer of the gated delta rule meets whole prompts before it decodes, and whole
+ * sequences when it is trained. The calls below serve both on a packed ragged batch: the
+ * tokens of all sequences one behind another, cu_tokens[i] .. cu_tokens[i + 1] - 1 those of
+ * sequence i. A prompt's last state goes to replayssm_restore (as [n][H][dv][dk] fp32,
+ * the layout it takes), and the decode path above continues from it; its alpha is e^g here.
+ * All pointers are 16-byte aligned device memory; rows of q, k and v may be column ranges
+ * of wider arrays (token strides in elements, multiples of 16 bytes). */
+enum replayssm_dtype { REPLAYSSM_F32 = 0, REPLAYSSM_BF16 = 1, REPLAYSSM_F16 = 2 };
+
+/* ---- tables of a packed batch --------------------------------------------
+ * Built on the GPU from the requests' lengths, so that nothing about a batch has to reach
+ * the host. n_seqs 1..REPLAYSSM_RAGGED_SEQS; max_tokens (room for packed tokens)
+ * 1..2^30; block (tokens per block; blocks never cross requests) 1..65536, and
+ * max_tokens / block + n_seqs < 2^30. */
+#define REPLAYSSM_RAGGED_SEQS 16384
+typedef struct replayssm_ragged_config {
+  int32_t n_seqs;
+  int32_t block;
+  int64_t max_tokens;
+} replayssm_ragged_config;
+
+/* Caller-owned arrays (int32, 16-byte aligned):
+ *  cu_tokens [n_seqs + 1]  packed offset of each request's first token, and the total
+ *  cu_blocks [n_seqs + 1]  the same in blocks, ceil(length / block) per request
+ *  token_seq [max_tokens]  request of each packed token; -1 behind the last token
+ *  token_pos [max_tokens]  its position, history + place in the request; -1 behind
+ *  block_seq [max_blocks]  request of each block; -1 behind the last block
+ *  err       [1]           sticky REPLAYSSM_DEVERR_* bits */
+typedef struct replayssm_ragged {
+  int32_t* cu_tokens;
+  int32_t* cu_blocks;
+  int32_t* token_seq;
+  int32_t* token_pos;
+  int32_t* block_seq;
+  int32_t* err;
+} replayssm_ragged;
+
+/* max_blocks = max_tokens / block + n_seqs, an upper bound of the batch's blocks. Host only. */
+int replayssm_ragged_sizes(const replayssm_ragged_config* cfg, int64_t* max_blocks);
+
+/* Fills every row of the five tables from lengths [n_seqs] and history [n_seqs] (tokens a
+ * request already has; NULL for none). A negative length counts as zero, and tokens beyond
+ * max_tokens are cut off; both set REPLAYSSM_DEVERR_RANGE. */
+int replayssm_ragged_maps(const replayssm_ragged_config* cfg, const replayssm_ragged* maps,
+                          const int32_t* lengths, const int32_t* history, void* stream);
+
+/* ---- queries and keys: norm per head and position rotation -----------------
+ * The step between the input projections and the delta rule or attention. For each token
+ * and head, with x the head's D channels (queries and keys alike):
+ *   r = (sum x^2 + eps)^(-1/2)  (NORM_L2)  or  (sum x^2 / D + eps)^(-1/2)  (NORM_RMS)
+ *   y = x * r * w               (w [D] fp32, shared by the heads; NULL: 1)
+ *   the first `rot` channels turn in pairs (a, b) by phi_i = positions[token] * inv_freq[i],
+ *   i < rot / 2: (a cos phi - b sin phi, b cos phi + a sin phi); pair i is channels
+ *   (i, i + rot / 2), or (2i, 2i + 1) with interleaved
+ *   queries are multiplied by q_scale; each head is written `rep` times in a row (heads
+ *   h * rep .. h * rep + rep - 1), as the decode path wants keys shared by value heads.
+ * Angles are formed in fp64 and everything else in fp32, rounded once at the end.
+ *   n_tokens 1..2^23, Hq, Hk >= 0 (not both 0), Hq + Hk <= 4096, D a multiple of 16 in
+ *   16..256, rep 1..64, rot even in 0..D (a multiple of 16 unless interleaved), eps >= 0;
+ *   q_stride, k_stride: elements between tokens, >= heads * D. */
+enum replayssm_norm { REPLAYSSM_NORM_L2 = 0, REPLAYSSM_NORM_RMS = 1 };
+typedef struct replayssm_qk_norm_config {
+  int32_t n_tokens;
+  int32_t Hq;
+  int32_t Hk;
+  int32_t D;
+  int32_t norm;        /* enum replayssm_norm                              */
+  int32_t rot;
+  int32_t interleaved; /* nonzero: pairs of neighbouring channels          */
+  int32_t rep;
+  int32_t dtype;       /* of q, k, dq, dk (enum replayssm_dtype)           */
+  int32_t out_dtype;   /* of q_out, k_out and their gradients              */
+  float eps;
+  float q_scale;
+  int64_t q_stride;
+  int64_t k_stride;
+} replayssm_qk_norm_config;
+
+/* Bytes of the backward call's workspace. Host only. */
+int replayssm_qk_norm_sizes(const replayssm_qk_norm_config* cfg, int64_t* backward_bytes);
+
+/* q [n_tokens][Hq][D] -> q_out [n_tokens][Hq * rep][D], k likewise (q and q_out unused with
+ * Hq = 0, k and k_out with Hk = 0). positions [n_tokens] int32 and inv_freq [rot / 2] fp32
+ * are read when rot > 0. */
+int replayssm_qk_norm(const replayssm_qk_norm_config* cfg, const void* q, const void* k, const float* wq,
+                      const float* wk, const int32_t* positions, const float* inv_freq, void* q_out,
+                      void* k_out, void* stream);
+
+/* Gradients: from dq_out, dk_out (laid out as q_out, k_out; a head's rep copies are summed)
+ * to dq [n_tokens][Hq][D], dk [n_tokens][Hk][D] and dwq, dwk [D] (either may be NULL: not
+ * wanted). workspace: replayssm_qk_norm_sizes bytes, used when dwq or dwk is wanted. The sums
+ * over rows have a fixed order: equal calls give equal bits. */
+int replayssm_qk_norm_backward(const replayssm_qk_norm_config* cfg, const void* q, const void* k,
+                               const float* wq, const float* wk, const int32_t* positions,
+                               const float* inv_freq, const void* dq_out, const void* dk_out, void* dq,
+                               void* dk, float* dwq, float* dwk, void* workspace, void* stream);
+
+/* ---- the gated delta rule over sequences -----------------------------------
+ * Per value head, with state S [dv][dk], log decay g and rate beta:
+ *   S_t = e^{g_t} S_{t-1} + u_t k_t^T,  u_t = beta_t (v_t - e^{g_t} S_{t-1} k_t),
+ *   o_t = scale S_t q_t
+ * (the recurrence of REPLAYSSM_GDN with alpha = e^g; g = -infinity closes the gate exactly).
+ *   q, k [n_tokens][Hk][dk], v, out [n_tokens][H][dv] in `dtype`; g, beta [n_tokens][H] fp32;
+ *   states [..][H][dv][dk] fp32, the logical layout of replayssm_restore.
+ * Value head h uses query and key head h / (H / Hk).
+ *   n_seqs 1..65535 (prompt calls: 1..REPLAYSSM_RAGGED_SEQS), n_tokens 1..2^30, H a multiple
+ *   of Hk, dk 16, 32, 64 or 128, dv a multiple of 16 in 16..256; token strides in elements,
+ *   >= the row, a multiple of 16 bytes; and H * dv / 16 * n_seqs <= 2^23 and
+ *   H * (n_tokens / 64 + n_seqs) <= 2^23.
+ * Sums and states are fp32. Rows of out of tokens that no sequence holds are left as they
+ * were. A non-finite input may reach every later token of its sequence, and in the
+ * prompt calls the earlier tokens of its block of 64 too; other sequences are not touched. */
+#define REPLAYSSM_DELTA_BLOCK 64
+typedef struct replayssm_delta_config {
+  int32_t n_seqs;
+  int32_t H;     /* value heads          */
+  int32_t Hk;    /* query and key heads  */
+  int32_t dk;
+  int32_t dv;
+  int32_t dtype; /* enum replayssm_dtype */
+  int64_t n_tokens;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  float scale;
+} replayssm_delta_config;
+
+/* Recurrent form, for the one or few new tokens of each sequence: sequence i's state is
+ * S_in[slots[i]], and S_out[slots[i]] receives the state after its tokens (S_out may be S_in;
+ * otherwise they must not overlap; a sequence without tokens has its state copied). slots
+ * [n_seqs] int32 within a pool of n_slots states, or NULL for slots[i] = i. A negative slot
+ * is a padded entry and skipped. A slot >= n_slots and every further sequence on a slot that an
+ * earlier one names are skipped and set REPLAYSSM_DEVERR_INDEX; offsets cu_tokens [n_seqs + 1]
+ * that fall or leave 0..n_tokens skip their sequence and set REPLAYSSM_DEVERR_RANGE. Slots
+ * that no sequence names are left as they were. */
+int replayssm_delta_step(const replayssm_delta_config* cfg, const int32_t* cu_tokens, const int32_t* slots,
+                         int n_slots, const void* q, const void* k, const void* v, const float* g,
+                         const float* beta, const float* S_in, float* S_out, void* out, int32_t* err,
+                         void* stream);
+
+/* Bytes of the prompt calls' workspaces (either pointer may be NULL). Host only. */
+int replayssm_delta_sizes(const replayssm_delta_config* cfg, int64_t* forward_bytes, int64_t* backward_bytes);
+
+/* Chunked form: every sequence of the batch from its state S0[i] ([n_seqs][H][dv][dk]; NULL:
+ * zero), however long or short. maps: the tables of this batch, built by
+ * replayssm_ragged_maps with block = REPLAYSSM_DELTA_BLOCK and max_tokens <= n_tokens (read:
+ * cu_tokens, cu_blocks, block_seq). out as above; S_out [n_seqs][H][dv][dk] receives
+ * the states after the last tokens (S0 for an empty sequence; NULL: not wanted; may be S0).
+ * workspace: forward_bytes of replayssm_delta_sizes, free again when the call's work is done. A
+ * sequence whose tables contradict each other or leave the arrays is skipped and
+ * REPLAYSSM_DEVERR_RANGE set in err. Results do not depend on what else is in the batch. */
+int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
+                           const void* k, const void* v, const float* g, const float* beta, const float* S0,
+                           void* out, float* S_out, void* workspace, int32_t* err, void* stream);
 
 /* ---- Kernel tiling (no effect on results) ----------------------------------------------
  * How the replay kernel (decode, verify, flush and the fused steps) maps the checkpoint onto

@@ -28,7 +28,14 @@ KINDS = {"mamba2": MAMBA2, "gdn": GDN, "kda": KDA}
 
 OK, EINVAL, ENOTSUP, EHIP = 0, -1, -2, -3
 TILES_AUTO, TILES_ONE, TILES_TWO = 0, 1, 2
-DEVERR_APPEND_OVERFLOW, DEVERR_PENDING, DEVERR_ACCEPT, DEVERR_CORRUPT, DEVERR_STALE, DEVERR_INDEX = 1, 2, 4, 8, 16, 32
+(DEVERR_APPEND_OVERFLOW, DEVERR_PENDING, DEVERR_ACCEPT, DEVERR_CORRUPT, DEVERR_STALE, DEVERR_INDEX, DEVERR_RANGE) = \
+    1, 2, 4, 8, 16, 32, 64
+F32, BF16, F16 = 0, 1, 2
+DTYPES = {"f32": F32, "bf16": BF16, "f16": F16}
+TORCH_DTYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+NORM_L2, NORM_RMS = 0, 1
+NORMS = {"l2": NORM_L2, "rms": NORM_RMS}
+DELTA_BLOCK = 64
 
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -59,6 +66,27 @@ class ConvConfig(ctypes.Structure):
 
 class ConvState(ctypes.Structure):
     _fields_ = [("ring", _vp), ("start", _vp), ("pend", _vp), ("arrive", _vp), ("err", _vp)]
+
+
+class RaggedConfig(ctypes.Structure):
+    _fields_ = [("n_seqs", _i32), ("block", _i32), ("max_tokens", _i64)]
+
+
+class Ragged(ctypes.Structure):
+    _fields_ = [("cu_tokens", _vp), ("cu_blocks", _vp), ("token_seq", _vp), ("token_pos", _vp), ("block_seq", _vp),
+                ("err", _vp)]
+
+
+class QkNormConfig(ctypes.Structure):
+    _fields_ = [("n_tokens", _i32), ("Hq", _i32), ("Hk", _i32), ("D", _i32), ("norm", _i32), ("rot", _i32),
+                ("interleaved", _i32), ("rep", _i32), ("dtype", _i32), ("out_dtype", _i32), ("eps", ctypes.c_float),
+                ("q_scale", ctypes.c_float), ("q_stride", _i64), ("k_stride", _i64)]
+
+
+class DeltaConfig(ctypes.Structure):
+    _fields_ = [("n_seqs", _i32), ("H", _i32), ("Hk", _i32), ("dk", _i32), ("dv", _i32), ("dtype", _i32),
+                ("n_tokens", _i64), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("scale", ctypes.c_float)]
 
 
 class ReplaySSMError(RuntimeError):
@@ -100,6 +128,14 @@ SIGNATURES = {
     "replayssm_flush_selected": [ctypes.POINTER(Config), ctypes.POINTER(State), _vp, _vp],
     "replayssm_snapshot": [ctypes.POINTER(Config), ctypes.POINTER(State), ctypes.c_int, _vp, _vp, _vp],
     "replayssm_restore": [ctypes.POINTER(Config), ctypes.POINTER(State), ctypes.c_int, _vp, _vp, _vp],
+    "replayssm_ragged_sizes": [ctypes.POINTER(RaggedConfig), ctypes.POINTER(_i64)],
+    "replayssm_ragged_maps": [ctypes.POINTER(RaggedConfig), ctypes.POINTER(Ragged), _vp, _vp, _vp],
+    "replayssm_qk_norm_sizes": [ctypes.POINTER(QkNormConfig), ctypes.POINTER(_i64)],
+    "replayssm_qk_norm": [ctypes.POINTER(QkNormConfig)] + [_vp] * 9,
+    "replayssm_qk_norm_backward": [ctypes.POINTER(QkNormConfig)] + [_vp] * 14,
+    "replayssm_delta_step": [ctypes.POINTER(DeltaConfig), _vp, _vp, ctypes.c_int] + [_vp] * 10,
+    "replayssm_delta_prompt": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(Ragged)] + [_vp] * 11,
+    "replayssm_delta_sizes": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(_i64), ctypes.POINTER(_i64)],
 }
 STRING_FUNCTIONS = {"replayssm_status_string": [ctypes.c_int], "replayssm_last_error": []}
 
@@ -379,3 +415,176 @@ class ConvLayer:
         self.err = torch.empty(4, dtype=torch.int32, device=device)
         self.struct = ConvState(*[t.data_ptr() for t in (self.ring, self.start, self.pend, self.arrive, self.err)])
         conv_init(cfg, self.struct, stream)
+
+
+# ---- the prompt side: ragged tables, query/key norm, the delta rule over sequences ----
+
+def _dev(t, dtype, shape=None, what="tensor"):
+    """Pointer of a contiguous tensor of the current GPU with this type (and shape); None stays None."""
+    if t is None:
+        return None
+    _on_current(t, what)
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} tensor expected, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on_current(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t, dtype, tokens, heads, dim, stride, what):
+    """Pointer of [tokens, heads, dim] rows whose heads lie together and whose tokens lie `stride` elements apart."""
+    _on_current(t, what)
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} tensor expected, got {t.dtype}")
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError(f"{what}: shape {(tokens, heads, dim)} expected, got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or (tokens > 1 and t.stride(0) != stride):
+        raise ValueError(f"{what}: strides ({stride}, {dim}, 1) expected, got {t.stride()}")
+    return t.data_ptr()
+
+
+def _workspace(t, need, what="workspace"):
+    if t is None:
+        return None
+    _on_current(t, what)
+    if not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"{what} must be contiguous and hold {need} bytes")
+    return t.data_ptr()
+
+
+def make_ragged_config(n_seqs, max_tokens, block=DELTA_BLOCK) -> RaggedConfig:
+    return RaggedConfig(int(n_seqs), int(block), int(max_tokens))
+
+
+def ragged_sizes(cfg: RaggedConfig) -> int:
+    n = _i64(0)
+    _check(lib().replayssm_ragged_sizes(ctypes.byref(cfg), ctypes.byref(n)), "ragged_sizes")
+    return int(n.value)
+
+
+def ragged_maps(cfg, maps, lengths, history=None, stream=None):
+    n = (cfg.n_seqs,)
+    _check(lib().replayssm_ragged_maps(ctypes.byref(cfg), ctypes.byref(maps),
+                                       _dev(lengths, torch.int32, n, "lengths"),
+                                       _dev(history, torch.int32, n, "history"), _s(stream)), "ragged_maps")
+
+
+class RaggedMaps:
+    """Device memory (torch tensors) for one packed batch's tables, plus the C struct. Filled by ragged_maps."""
+
+    def __init__(self, cfg: RaggedConfig, device="cuda"):
+        self.cfg = cfg
+        self.max_blocks = ragged_sizes(cfg)  # validates
+        i32 = torch.int32
+        self.cu_tokens = torch.zeros(cfg.n_seqs + 1, dtype=i32, device=device)
+        self.cu_blocks = torch.zeros(cfg.n_seqs + 1, dtype=i32, device=device)
+        self.token_seq = torch.full((cfg.max_tokens,), -1, dtype=i32, device=device)
+        self.token_pos = torch.full((cfg.max_tokens,), -1, dtype=i32, device=device)
+        self.block_seq = torch.full((self.max_blocks,), -1, dtype=i32, device=device)
+        self.err = torch.zeros(4, dtype=i32, device=device)
+        tensors = (self.cu_tokens, self.cu_blocks, self.token_seq, self.token_pos, self.block_seq, self.err)
+        self.struct = Ragged(*[t.data_ptr() for t in tensors])
+        self.struct.tensors = tensors  # the struct may outlive this object
+
+
+def make_qk_norm_config(n_tokens, Hq, Hk, D, norm="l2", rot=0, interleaved=False, rep=1, eps=1e-6, q_scale=1.0,
+                        dtype="bf16", out_dtype=None, q_stride=None, k_stride=None) -> QkNormConfig:
+    """Strides default to contiguous rows, out_dtype to dtype."""
+    out_dtype = dtype if out_dtype is None else out_dtype
+    return QkNormConfig(int(n_tokens), int(Hq), int(Hk), int(D), NORMS.get(norm, norm), int(rot),
+                        int(bool(interleaved)), int(rep), DTYPES.get(dtype, dtype), DTYPES.get(out_dtype, out_dtype),
+                        float(eps), float(q_scale), int(Hq * D if q_stride is None else q_stride),
+                        int(Hk * D if k_stride is None else k_stride))
+
+
+def qk_norm_sizes(cfg: QkNormConfig) -> int:
+    n = _i64(0)
+    _check(lib().replayssm_qk_norm_sizes(ctypes.byref(cfg), ctypes.byref(n)), "qk_norm_sizes")
+    return int(n.value)
+
+
+def _qk_inputs(cfg, q, k, wq, wk, positions, inv_freq):
+    t, n = TORCH_DTYPES[cfg.dtype], cfg.n_tokens
+    return (_rows(q, t, n, cfg.Hq, cfg.D, cfg.q_stride, "q") if cfg.Hq else None,
+            _rows(k, t, n, cfg.Hk, cfg.D, cfg.k_stride, "k") if cfg.Hk else None,
+            _dev(wq, torch.float32, (cfg.D,), "wq"), _dev(wk, torch.float32, (cfg.D,), "wk"),
+            _dev(positions, torch.int32, (n,), "positions") if cfg.rot else None,
+            _dev(inv_freq, torch.float32, (cfg.rot // 2,), "inv_freq") if cfg.rot else None)
+
+
+def qk_norm(cfg, q, k, wq, wk, positions, inv_freq, q_out, k_out, stream=None):
+    qk_norm_sizes(cfg)  # validates
+    o, n = TORCH_DTYPES[cfg.out_dtype], cfg.n_tokens
+    _check(lib().replayssm_qk_norm(
+        ctypes.byref(cfg), *_qk_inputs(cfg, q, k, wq, wk, positions, inv_freq),
+        _dev(q_out, o, (n, cfg.Hq * cfg.rep, cfg.D), "q_out") if cfg.Hq else None,
+        _dev(k_out, o, (n, cfg.Hk * cfg.rep, cfg.D), "k_out") if cfg.Hk else None, _s(stream)), "qk_norm")
+
+
+def qk_norm_backward(cfg, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq=None, dwk=None,
+                     workspace=None, stream=None):
+    need = qk_norm_sizes(cfg)
+    t, o, n = TORCH_DTYPES[cfg.dtype], TORCH_DTYPES[cfg.out_dtype], cfg.n_tokens
+    _check(lib().replayssm_qk_norm_backward(
+        ctypes.byref(cfg), *_qk_inputs(cfg, q, k, wq, wk, positions, inv_freq),
+        _dev(dq_out, o, (n, cfg.Hq * cfg.rep, cfg.D), "dq_out") if cfg.Hq else None,
+        _dev(dk_out, o, (n, cfg.Hk * cfg.rep, cfg.D), "dk_out") if cfg.Hk else None,
+        _dev(dq, t, (n, cfg.Hq, cfg.D), "dq") if cfg.Hq else None,
+        _dev(dk, t, (n, cfg.Hk, cfg.D), "dk") if cfg.Hk else None,
+        _dev(dwq, torch.float32, (cfg.D,), "dwq"), _dev(dwk, torch.float32, (cfg.D,), "dwk"),
+        _workspace(workspace, need if dwq is not None or dwk is not None else 0), _s(stream)), "qk_norm_backward")
+
+
+def make_delta_config(n_seqs, n_tokens, H, Hk, dk, dv, dtype="bf16", scale=1.0, q_stride=None, k_stride=None,
+                      v_stride=None) -> DeltaConfig:
+    """Strides default to contiguous rows."""
+    return DeltaConfig(int(n_seqs), int(H), int(Hk), int(dk), int(dv), DTYPES.get(dtype, dtype), int(n_tokens),
+                       int(Hk * dk if q_stride is None else q_stride), int(Hk * dk if k_stride is None else k_stride),
+                       int(H * dv if v_stride is None else v_stride), float(scale))
+
+
+def delta_sizes(cfg: DeltaConfig):
+    """(bytes of delta_prompt's workspace, bytes of delta_prompt_backward's)"""
+    f, b = _i64(0), _i64(0)
+    _check(lib().replayssm_delta_sizes(ctypes.byref(cfg), ctypes.byref(f), ctypes.byref(b)), "delta_sizes")
+    return int(f.value), int(b.value)
+
+
+def _delta_inputs(cfg, q, k, v, g, beta):
+    if cfg.dtype not in TORCH_DTYPES:
+        raise ReplaySSMError(EINVAL, "delta", f"dtype {cfg.dtype} unknown")
+    t, n = TORCH_DTYPES[cfg.dtype], cfg.n_tokens
+    return (_rows(q, t, n, cfg.Hk, cfg.dk, cfg.q_stride, "q"), _rows(k, t, n, cfg.Hk, cfg.dk, cfg.k_stride, "k"),
+            _rows(v, t, n, cfg.H, cfg.dv, cfg.v_stride, "v"), _dev(g, torch.float32, (n, cfg.H), "g"),
+            _dev(beta, torch.float32, (n, cfg.H), "beta"))
+
+
+def delta_step(cfg, cu_tokens, slots, n_slots, q, k, v, g, beta, S_in, S_out, out, err, stream=None):
+    inputs = _delta_inputs(cfg, q, k, v, g, beta)
+    pool = (n_slots, cfg.H, cfg.dv, cfg.dk)
+    _check(lib().replayssm_delta_step(
+        ctypes.byref(cfg), _dev(cu_tokens, torch.int32, (cfg.n_seqs + 1,), "cu_tokens"),
+        _dev(slots, torch.int32, (cfg.n_seqs,), "slots"), int(n_slots), *inputs,
+        _dev(S_in, torch.float32, pool, "S_in"), _dev(S_out, torch.float32, pool, "S_out"),
+        _dev(out, TORCH_DTYPES[cfg.dtype], (cfg.n_tokens, cfg.H, cfg.dv), "out"), _dev(err, torch.int32, None, "err"),
+        _s(stream)), "delta_step")
+
+
+def delta_prompt(cfg, maps, q, k, v, g, beta, S0, out, S_out, workspace, err, stream=None):
+    need = delta_sizes(cfg)[0]
+    inputs = _delta_inputs(cfg, q, k, v, g, beta)
+    states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
+    _check(lib().replayssm_delta_prompt(
+        ctypes.byref(cfg), ctypes.byref(maps), *inputs, _dev(S0, torch.float32, states, "S0"),
+        _dev(out, TORCH_DTYPES[cfg.dtype], (cfg.n_tokens, cfg.H, cfg.dv), "out"),
+        _dev(S_out, torch.float32, states, "S_out"), _workspace(workspace, need), _dev(err, torch.int32, None, "err"),
+        _s(stream)), "delta_prompt")

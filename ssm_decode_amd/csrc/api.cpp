@@ -10,6 +10,7 @@
 #include <string>
 
 #include "conv.hpp"
+#include "host.hpp"
 #include "internal.hpp"
 #include "replayssm.h"
 
@@ -17,7 +18,9 @@ namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int code, const char* fmt, ...) {
+}  // namespace
+
+int rs::fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -27,10 +30,9 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-int hip_result(hipError_t e, const char* what) {
-  if (e == hipSuccess) return REPLAYSSM_OK;
-  return fail(REPLAYSSM_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
+using namespace rs::host;
+
+namespace {
 
 bool exact_u(const replayssm_config* c);
 
@@ -47,15 +49,6 @@ int replay(const replayssm_config* cfg, int tmax, const rs::ReplayArgs& a, hipSt
                 what, lds.total * 4, max_lds);
   return hip_result(rs::launch_replay(cfg->kind, cfg->dk, tmax, a, s), what);
 }
-
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Pointer must be non-NULL and 16-byte aligned.
-#define NEED(ptr)                                                                   \
-  do {                                                                              \
-    if ((ptr) == nullptr) return fail(REPLAYSSM_EINVAL, "%s is NULL", #ptr);        \
-    if (!aligned(ptr)) return fail(REPLAYSSM_EINVAL, "%s is not 16-byte aligned", #ptr); \
-  } while (0)
 
 int tmax_bucket(int T) { return T <= 1 ? 1 : (T <= 4 ? 4 : 8); }
 
@@ -152,8 +145,6 @@ rs::ReplayArgs replay_args(const replayssm_config* c, const replayssm_state* s, 
   a.mode = mode;
   return a;
 }
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
 

@@ -1,0 +1,250 @@
+// Device pieces of the chunked gated delta rule: operands in bf16 parts, swizzled LDS tiles,
+// and matrix products on 16 x 16 x 32 MFMA whose results feed the next product from registers.
+//
+// Precision. The matrix cores take bf16; an fp32 value goes in as a sum of bf16 parts, each
+// the rounded remainder of the ones before it. Two parts keep 17 bits of it (relative error
+// at most 2^-18), three keep 24. A product of parts (i, j) is left out where i + j reaches the
+// larger part count, which is the size of the rounding already made. bf16 inputs are one
+// exact part and fp16 inputs two exact parts; what is computed on the way (states,
+// corrections, the inverse, decayed scores) takes two parts beside 16-bit inputs, which leaves
+// states and gradients within a few 1e-6 of 64-bit ones, and three beside fp32 inputs.
+//
+// Layout. In D = A B + C of v_mfma_f32_16x16x32_bf16 lane l (n = l & 15, g = l >> 4) holds
+// A[l & 15][8g .. 8g + 7], B[8g .. 8g + 7][n] and D[4g .. 4g + 3][n]. A result can be the next
+// product's B (or, transposed, its A) straight from registers if the rows of a pair of result
+// tiles are dealt out so that a lane's 4 + 4 values are eight consecutive indices:
+//     tile 2s, row 4q + r  <->  index 32s + 8q + r;   tile 2s + 1  <->  32s + 8q + 4 + r.
+// Only the order in which A's rows are read from LDS changes (`dealt`).
+#pragma once
+
+#include "element.hpp"
+#include "prompt.hpp"
+
+namespace rs {
+
+template <typename T>
+struct Parts;
+template <>
+struct Parts<__bf16> {
+  static constexpr int in = 1, mid = 2;
+};
+template <>
+struct Parts<_Float16> {
+  static constexpr int in = 2, mid = 2;
+};
+template <>
+struct Parts<float> {
+  static constexpr int in = 3, mid = 3;
+};
+
+template <int N>
+struct Split {
+  bf16x8 p[N];
+};
+
+template <int N>
+__device__ __forceinline__ Split<N> split8(const f32x8& x) {
+  Split<N> s;
+  s.p[0] = __builtin_convertvector(x, bf16x8);
+  f32x8 rest = x;
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    rest -= __builtin_convertvector(s.p[i - 1], f32x8);
+    s.p[i] = __builtin_convertvector(rest, bf16x8);
+  }
+  return s;
+}
+
+__device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) {
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// acc += A B over the kept products of parts, smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Split<NA>& a, const Split<NB>& b, f32x4 acc) {
+  constexpr int kOrder = NA > NB ? NA : NB;
+#pragma unroll
+  for (int o = kOrder - 1; o >= 0; --o)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (o - i >= 0 && o - i < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[o - i], acc, 0, 0, 0);
+  return acc;
+}
+
+// The index of row m of result tile `tile` (see above).
+__device__ __forceinline__ int dealt(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
+
+// The raw eight elements of a row as they come from memory, and their parts.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__bf16> {
+  bf16x8 x;
+  __device__ __forceinline__ void load(const __bf16* p) { x = *reinterpret_cast<const bf16x8*>(p); }
+  __device__ __forceinline__ void zero() { x = bf16x8{}; }
+  __device__ __forceinline__ Split<1> split() const {
+    Split<1> s;
+    s.p[0] = x;
+    return s;
+  }
+};
+template <>
+struct Raw8<_Float16> {
+  f16x8 x;
+  __device__ __forceinline__ void load(const _Float16* p) { x = *reinterpret_cast<const f16x8*>(p); }
+  __device__ __forceinline__ void zero() { x = f16x8{}; }
+  __device__ __forceinline__ Split<2> split() const { return split8<2>(__builtin_convertvector(x, f32x8)); }
+};
+template <>
+struct Raw8<float> {
+  f32x8 x;
+  __device__ __forceinline__ void load(const float* p) { x = load8(p); }
+  __device__ __forceinline__ void zero() { x = f32x8{}; }
+  __device__ __forceinline__ Split<3> split() const { return split8<3>(x); }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// ROWS rows of W columns in N bf16 planes in LDS (W a multiple of 32). The 16-byte chunks of a
+// row are exchanged by an exclusive-or with a key of the row, so that the eight lanes an LDS
+// cycle serves hit distinct banks when they read one chunk column of eight dealt rows, and the
+// transposing reads (four rows by four chunks per 16 lanes) meet at most in pairs, the least
+// their half-chunk reads allow.
+template <int W, int N, int ROWS = kBlock>
+struct Tile {
+  static constexpr int kRowBytes = W * 2;
+  static constexpr int kPlane = ROWS * kRowBytes;
+  static constexpr int kBytes = N * kPlane;
+  static constexpr int kChunks = W / 8;
+  char* base;
+  __device__ __forceinline__ explicit Tile(char* b) : base(b) {}
+
+  __device__ __forceinline__ static int key(int row) {
+    return (((row & 1) << 2) | (row & 2) | ((row >> 3) & 1)) & (kChunks - 1);
+  }
+  __device__ __forceinline__ static int at(int row, int chunk) { return row * kRowBytes + ((chunk ^ key(row)) << 4); }
+
+  __device__ __forceinline__ void put(int row, int chunk, const Split<N>& s) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8*>(base + i * kPlane + at(row, chunk)) = s.p[i];
+  }
+  // Eight consecutive columns 32 ks + 8 g of one row: an A or B operand whose row is the lane's.
+  __device__ __forceinline__ Split<N> row8(int row, int ks, int g) const {
+    Split<N> s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s.p[i] = *reinterpret_cast<const bf16x8*>(base + i * kPlane + at(row, 4 * ks + g));
+    return s;
+  }
+  // Eight consecutive rows 32 ks + 8 g + 0..7 of one column, transposed on the way out of LDS: the
+  // operand whose k index runs over rows. ds_read_b64_tr_b16 transposes a 4 x 16 block in each
+  // 16 lanes: lane i gives the address of four columns of row i >> 2 (the group i & 3 of them), and
+  // lane 4c + e receives column e of group c from all four rows. The columns are `dealt`
+  // (DEALT: column of lane n is dealt(tile, n)) or plain (16 tile + n).
+  template <bool DEALT>
+  __device__ __forceinline__ Split<N> col8(int tile, int ks, int lane) const {
+    const int g = lane >> 4, e = (lane >> 2) & 3, c = lane & 3;
+    const int col = DEALT ? 32 * (tile >> 1) + 8 * c + 4 * (tile & 1) : 16 * tile + 4 * c;
+    const int row = 32 * ks + 8 * g + e;
+    const int off0 = at(row, col >> 3) + (col & 4) * 2, off1 = at(row + 4, col >> 3) + (col & 4) * 2;
+    Split<N> s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(base + i * kPlane + off0));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(base + i * kPlane + off1));
+      s.p[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    return s;
+  }
+};
+
+constexpr int kChunkThreads = 256;
+
+// Rows of a block on their way from memory to a tile: loads early, stores (as parts) later.
+template <typename T, int DK, int ROWS = kBlock>
+struct RowStage {
+  static constexpr int kUnits = ROWS * DK / 8;
+  static constexpr int kPer = (kUnits + kChunkThreads - 1) / kChunkThreads;
+  Raw8<T> x[kPer];
+  // rows valid rows starting at p; the others are zero
+  __device__ __forceinline__ void load(const T* p, int64_t stride, int rows) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int unit = i * kChunkThreads + threadIdx.x;
+      const int row = unit / (DK / 8), c = unit % (DK / 8);
+      if (row < rows && unit < kUnits)
+        x[i].load(p + row * stride + c * 8);
+      else
+        x[i].zero();
+    }
+  }
+  template <int W>
+  __device__ __forceinline__ void store(const Tile<W, Parts<T>::in, ROWS>& tile) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int unit = i * kChunkThreads + threadIdx.x;
+      if (unit < kUnits) tile.put(unit / (DK / 8), unit % (DK / 8), x[i].split());
+    }
+  }
+};
+
+// Tiles are at least 32 columns wide; a head of 16 keeps its upper half zero.
+template <int DK>
+constexpr int kWide = DK < 32 ? 32 : DK;
+
+template <int W, int N, int ROWS>
+__device__ __forceinline__ void zero_tile(const Tile<W, N, ROWS>& t) {
+  for (int i = threadIdx.x * 16; i < Tile<W, N, ROWS>::kBytes; i += kChunkThreads * 16)
+    *reinterpret_cast<bf16x8*>(t.base + i) = bf16x8{};
+}
+
+// What the kernels pass to each other per (block, value head), in 16-byte units of a lane:
+// triangular 64 x 64 operands as 6 fragments (row tile t, 32-column step s; the two that are
+// zero are not kept) of `mid` parts, and the block's scalars.
+constexpr int kFrags = 6;
+__host__ __device__ constexpr int64_t frag_bytes(int mid) { return (int64_t)kFrags * mid * 1024; }
+// lower triangle: s <= t / 2; upper triangle: s >= t / 2
+__device__ __forceinline__ int lower_frag(int t, int s) { return t < 2 ? t : 2 + 2 * (t - 2) + s; }
+__device__ __forceinline__ int upper_frag(int t, int s) { return t < 2 ? 2 * t + s : 2 + t; }
+
+template <int N>
+__device__ __forceinline__ void put_frag(char* base, int frag, int lane, const Split<N>& s) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<bf16x8*>(base + ((frag * N + i) * 64 + lane) * 16) = s.p[i];
+}
+template <int N>
+__device__ __forceinline__ Split<N> get_frag(const char* base, int frag, int lane) {
+  Split<N> s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s.p[i] = *reinterpret_cast<const bf16x8*>(base + ((frag * N + i) * 64 + lane) * 16);
+  return s;
+}
+
+// The block's scalars per token: e^{G_i}, e^{G_end - G_i}, beta_i (G the running sum of g).
+struct BlockScalars {
+  float first[kBlock];
+  float last[kBlock];
+  float beta[kBlock];
+};
+
+// A sequence's place in the packed batch; ok = false where the tables contradict each other or
+// leave the arrays (nothing of the sequence is touched then).
+struct SeqRange {
+  int begin, end, block0, blocks;
+  bool ok;
+};
+__device__ __forceinline__ SeqRange seq_range(const DeltaArgs& a, int s) {
+  SeqRange r;
+  r.begin = a.cu_tokens[s];
+  r.end = a.cu_tokens[s + 1];
+  r.block0 = a.cu_blocks[s];
+  const int block1 = a.cu_blocks[s + 1];
+  r.ok = r.begin >= 0 && r.end >= r.begin && (int64_t)r.end <= a.n_tokens && r.block0 >= 0 && block1 >= r.block0 &&
+         block1 <= a.max_blocks;
+  r.blocks = r.ok ? block1 - r.block0 : 0;
+  if (r.ok && r.blocks != (int)(((int64_t)r.end - r.begin + kBlock - 1) / kBlock)) r.ok = false;
+  return r;
+}
+
+}  // namespace rs
