@@ -566,6 +566,19 @@ int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ra
                            const void* k, const void* v, const float* g, const float* beta, const float* S0,
                            void* out, float* S_out, void* workspace, int32_t* err, void* stream);
 
+/* Gradients of replayssm_delta_prompt: from dout [n_tokens][H][dv] (of out) and dS_out
+ * [n_seqs][H][dv][dk] (of S_out; NULL: zero) to dq, dk [n_tokens][Hk][dk] (summed over the value
+ * heads that share a key head), dv [n_tokens][H][dv], dg, dbeta [n_tokens][H] fp32, and dS0
+ * (of S0; NULL: not wanted; must not be dS_out). dq, dk and dv are contiguous, in `dtype`.
+ * The inputs, tables and S0 are those of the forward call; states are computed again, so nothing
+ * of the forward call's workspace is needed. workspace: backward_bytes of replayssm_delta_sizes.
+ * Sums have a fixed order: equal calls give equal bits. Rows of tokens that no sequence holds are
+ * left as they were; a sequence with bad tables is skipped and flagged as in the forward call. */
+int replayssm_delta_prompt_backward(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
+                                    const void* k, const void* v, const float* g, const float* beta, const float* S0,
+                                    const void* dout, const float* dS_out, void* dq, void* dk, void* dv, float* dg,
+                                    float* dbeta, float* dS0, void* workspace, int32_t* err, void* stream);
+
 /* ---- Kernel tiling (no effect on results) ----------------------------------------------
  * How the replay kernel (decode, verify, flush and the fused steps) maps the checkpoint onto
  * wavefronts when dk = 128, T_max <= 4 and dv is a multiple of 32: one 16-row tile

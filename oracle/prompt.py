@@ -94,3 +94,23 @@ def ragged_tables(lengths, history, block, max_tokens):
         cub.append(len(bseq))
     pad = lambda x, to: np.array(x + [-1] * (to - len(x)), np.int64)  # noqa: E731
     return np.array(cu), np.array(cub), pad(seq, max_tokens), pad(pos, max_tokens), pad(bseq, max_tokens // block + n)
+
+
+def delta_rule_backward_magnitudes(q, k, v, g, beta, S0, scale, dout, dS_last):
+    """Sizes of the terms of each gradient: delta_rule_backward's last products with absolute values."""
+    _, last, before = delta_rule(q, k, v, g, beta, S0, scale)
+    after = list(before[1:]) + [last]
+    dS, A = dS_last.astype(np.float64).copy(), np.abs
+    m = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape), np.zeros(len(g)), np.zeros(len(g))]
+    for t in reversed(range(len(g))):
+        a, S = np.exp(float(g[t])), before[t]
+        r = A(v[t]) + a * (A(S) @ A(k[t]))
+        m[0][t] = scale * (A(after[t]).T @ A(dout[t]))
+        dS = dS + scale * np.outer(dout[t], q[t])
+        du = A(dS) @ A(k[t])
+        m[4][t] = du @ r
+        m[2][t] = beta[t] * du
+        m[1][t] = A(dS).T @ (beta[t] * r) + a * (A(S).T @ m[2][t])
+        m[3][t] = a * ((A(dS) * A(S)).sum() + m[2][t] @ (A(S) @ A(k[t]))) + A(dout[t]) @ (A(after[t]) @ A(q[t])) * scale
+        dS = a * (dS - np.outer(beta[t] * (dS @ k[t]), k[t]))
+    return m

@@ -14,6 +14,6 @@ from ._lib import (  # noqa: F401
     TILES_AUTO, TILES_ONE, TILES_TWO, get_tiling, set_tiling,
     ConvConfig, ConvLayer, ConvState, conv_accept, conv_init, conv_sizes, conv_step, make_conv_config,
     BF16, DELTA_BLOCK, DEVERR_RANGE, DeltaConfig, F16, F32, NORM_L2, NORM_RMS, QkNormConfig, Ragged, RaggedConfig,
-    RaggedMaps, delta_prompt, delta_sizes, delta_step, make_delta_config, make_qk_norm_config, make_ragged_config, qk_norm, qk_norm_backward,
+    RaggedMaps, delta_prompt, delta_prompt_backward, delta_sizes, delta_step, make_delta_config, make_qk_norm_config, make_ragged_config, qk_norm, qk_norm_backward,
     qk_norm_sizes, ragged_maps, ragged_sizes,
 )

@@ -135,6 +135,7 @@ SIGNATURES = {
     "replayssm_qk_norm_backward": [ctypes.POINTER(QkNormConfig)] + [_vp] * 14,
     "replayssm_delta_step": [ctypes.POINTER(DeltaConfig), _vp, _vp, ctypes.c_int] + [_vp] * 10,
     "replayssm_delta_prompt": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(Ragged)] + [_vp] * 11,
+    "replayssm_delta_prompt_backward": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(Ragged)] + [_vp] * 17,
     "replayssm_delta_sizes": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(_i64), ctypes.POINTER(_i64)],
 }
 STRING_FUNCTIONS = {"replayssm_status_string": [ctypes.c_int], "replayssm_last_error": []}
@@ -588,3 +589,18 @@ def delta_prompt(cfg, maps, q, k, v, g, beta, S0, out, S_out, workspace, err, st
         _dev(out, TORCH_DTYPES[cfg.dtype], (cfg.n_tokens, cfg.H, cfg.dv), "out"),
         _dev(S_out, torch.float32, states, "S_out"), _workspace(workspace, need), _dev(err, torch.int32, None, "err"),
         _s(stream)), "delta_prompt")
+
+
+def delta_prompt_backward(cfg, maps, q, k, v, g, beta, S0, dout, dS_out, dq, dk, dv, dg, dbeta, dS0, workspace, err,
+                          stream=None):
+    need = delta_sizes(cfg)[1]
+    inputs = _delta_inputs(cfg, q, k, v, g, beta)
+    t, n, f32 = TORCH_DTYPES[cfg.dtype], cfg.n_tokens, torch.float32
+    states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
+    _check(lib().replayssm_delta_prompt_backward(
+        ctypes.byref(cfg), ctypes.byref(maps), *inputs, _dev(S0, f32, states, "S0"),
+        _dev(dout, t, (n, cfg.H, cfg.dv), "dout"), _dev(dS_out, f32, states, "dS_out"),
+        _dev(dq, t, (n, cfg.Hk, cfg.dk), "dq"), _dev(dk, t, (n, cfg.Hk, cfg.dk), "dk"),
+        _dev(dv, t, (n, cfg.H, cfg.dv), "dv"), _dev(dg, f32, (n, cfg.H), "dg"),
+        _dev(dbeta, f32, (n, cfg.H), "dbeta"), _dev(dS0, f32, states, "dS0"), _workspace(workspace, need),
+        _dev(err, torch.int32, None, "err"), _s(stream)), "delta_prompt_backward")

@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libreplayssm.so")
 SOURCES = ["replay.hip", "ring.hip", "eager.hip", "probe.hip", "conv.hip", "ragged.hip", "qknorm.hip",
-           "delta_step.hip", "delta_prompt.hip", "api.cpp", "api_prompt.cpp"]
+           "delta_step.hip", "delta_prompt.hip", "delta_backward.hip", "api.cpp", "api_prompt.cpp"]
 ARCH = "gfx950"
 
 

@@ -317,4 +317,38 @@ int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ra
   return hip_result(rs::launch_delta_prompt(a, as_stream(stream)), "delta_prompt");
 }
 
+int replayssm_delta_prompt_backward(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
+                                    const void* k, const void* v, const float* g, const float* beta, const float* S0,
+                                    const void* dout, const float* dS_out, void* dq, void* dk, void* dv, float* dg,
+                                    float* dbeta, float* dS0, void* workspace, int32_t* err, void* stream) {
+  if (int r = check_delta(cfg, REPLAYSSM_RAGGED_SEQS)) return r;
+  if (int r = check_delta_maps(maps)) return r;
+  if (int r = check_delta_inputs(q, k, v, g, beta, err)) return r;
+  if (S0 && !aligned(S0)) return fail(REPLAYSSM_EINVAL, "S0 is not 16-byte aligned");
+  if (dS_out && !aligned(dS_out)) return fail(REPLAYSSM_EINVAL, "dS_out is not 16-byte aligned");
+  if (dS0 && !aligned(dS0)) return fail(REPLAYSSM_EINVAL, "dS0 is not 16-byte aligned");
+  NEED(dout);
+  NEED(dq);
+  NEED(dk);
+  NEED(dv);
+  NEED(dg);
+  NEED(dbeta);
+  NEED(workspace);
+  rs::DeltaArgs a = delta_args(cfg, q, k, v, g, beta, err);
+  a.cu_tokens = maps->cu_tokens;
+  a.cu_blocks = maps->cu_blocks;
+  a.block_seq = maps->block_seq;
+  a.S0 = S0;
+  a.dout = dout;
+  a.dS_out = dS_out;
+  a.dq = dq;
+  a.dk_ = dk;
+  a.dv_ = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.dS0 = dS0;
+  a.ws = workspace;
+  return hip_result(rs::launch_delta_prompt_backward(a, as_stream(stream)), "delta_prompt_backward");
+}
+
 }  // extern "C"
