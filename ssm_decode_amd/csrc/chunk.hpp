@@ -161,31 +161,107 @@ struct Tile {
 
 constexpr int kChunkThreads = 256;
 
-// Rows of a block on their way from memory to a tile: loads early, stores (as parts) later.
-template <typename T, int DK, int ROWS = kBlock>
+// Rows of a block (W columns of each) on their way from memory to LDS: loads early, stores (as parts)
+// later. A thread's units lie whole row steps apart, so that per block only the uniform base
+// changes. Every lane loads on every path, from the nearest row and column that exist: a register
+// that some lanes load and others clear would make the clearing wait for the load. Rows past the
+// block's end are zeroed on their way into LDS; columns past the last are only read into lanes whose
+// results nothing uses.
+template <typename T, int W, int ROWS = kBlock>
 struct RowStage {
-  static constexpr int kUnits = ROWS * DK / 8;
+  static constexpr int kUnits = ROWS * W / 8;
   static constexpr int kPer = (kUnits + kChunkThreads - 1) / kChunkThreads;
+  static constexpr int kRowStep = kChunkThreads / (W / 8);  // rows between a thread's units
   Raw8<T> x[kPer];
-  // rows valid rows starting at p; the others are zero
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int rows) {
+  int64_t offset;  // of the thread's first unit
+  int row, chunk, column;
+  int rows;  // of the block on its way (uniform)
+  // columns: how many of the W exist (a multiple of 8)
+  __device__ __forceinline__ RowStage(int64_t stride, int columns = W) {
+    const int unit = (int)threadIdx.x < kUnits ? threadIdx.x : kUnits - 1;
+    row = unit / (W / 8);
+    chunk = unit % (W / 8);
+    column = chunk * 8 < columns ? chunk * 8 : columns - 8;
+    offset = row * stride + column;
+    rows = ROWS;
+  }
+  // n valid rows (at least one) starting at p (uniform)
+  __device__ __forceinline__ void load(const T* p, int64_t stride, int n) {
+    rows = n;
+    if (n == ROWS) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int unit = i * kChunkThreads + threadIdx.x;
-      const int row = unit / (DK / 8), c = unit % (DK / 8);
-      if (row < rows && unit < kUnits)
-        x[i].load(p + row * stride + c * 8);
-      else
-        x[i].zero();
+      for (int i = 0; i < kPer; ++i) x[i].load(p + i * kRowStep * stride + offset);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = row + i * kRowStep < n ? row + i * kRowStep : n - 1;
+        x[i].load(p + r * stride + column);
+      }
     }
   }
-  template <int W>
-  __device__ __forceinline__ void store(const Tile<W, Parts<T>::in, ROWS>& tile) const {
+  // Zeroes what was loaded for rows past the end.
+  __device__ __forceinline__ void clip() {
+    if (rows != ROWS) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int unit = i * kChunkThreads + threadIdx.x;
-      if (unit < kUnits) tile.put(unit / (DK / 8), unit % (DK / 8), x[i].split());
+      for (int i = 0; i < kPer; ++i)
+        if (row + i * kRowStep >= rows) x[i].zero();
     }
+  }
+  __device__ __forceinline__ bool mine() const { return kUnits % kChunkThreads == 0 || (int)threadIdx.x < kUnits; }
+  template <int TW>
+  __device__ __forceinline__ void store(const Tile<TW, Parts<T>::in, ROWS>& tile) {
+    clip();
+    if (mine()) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) tile.put(row + i * kRowStep, chunk, x[i].split());
+    }
+  }
+};
+
+// The same rows kept in their own type, to be read back a column at a time, eight rows
+// 32 p + 8 g .. + 7 per lane: 16-bit types through the transposing read, fp32 one by one from
+// rows padded by 16 bytes.
+template <typename T, int W>
+struct ColumnTile {
+  static constexpr int kBytes = kBlock * W * 2;
+  Tile<W, 1> tile;
+  __device__ __forceinline__ explicit ColumnTile(char* b) : tile(b) {}
+  __device__ __forceinline__ void put(RowStage<T, W>& s) const {
+    s.clip();
+#pragma unroll
+    for (int i = 0; i < RowStage<T, W>::kPer; ++i)
+      *reinterpret_cast<bf16x8*>(tile.base + tile.at(s.row + i * s.kRowStep, s.chunk)) =
+          __builtin_bit_cast(bf16x8, s.x[i].x);
+  }
+  __device__ __forceinline__ void zero_row(int row, int chunk) const {
+    *reinterpret_cast<bf16x8*>(tile.base + tile.at(row, chunk)) = bf16x8{};
+  }
+  template <bool DEALT>
+  __device__ __forceinline__ f32x8 read(int t, int p, int lane) const {
+    typedef T vec __attribute__((ext_vector_type(8)));
+    return __builtin_convertvector(__builtin_bit_cast(vec, tile.template col8<DEALT>(t, p, lane).p[0]), f32x8);
+  }
+};
+template <int W>
+struct ColumnTile<float, W> {
+  static constexpr int kLdRow = W + 4;
+  static constexpr int kBytes = kBlock * kLdRow * 4;
+  float* base;
+  __device__ __forceinline__ explicit ColumnTile(char* b) : base(reinterpret_cast<float*>(b)) {}
+  __device__ __forceinline__ void put(RowStage<float, W>& s) const {
+    s.clip();
+#pragma unroll
+    for (int i = 0; i < RowStage<float, W>::kPer; ++i)
+      store8(base + (s.row + i * s.kRowStep) * kLdRow + s.chunk * 8, s.x[i].x);
+  }
+  template <bool DEALT>
+  __device__ __forceinline__ f32x8 read(int t, int p, int lane) const {
+    const int n = lane & 15, g = lane >> 4;
+    const float* c = base + (32 * p + 8 * g) * kLdRow + (DEALT ? dealt(t, n) : 16 * t + n);
+    f32x8 x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = c[e * kLdRow];
+    return x;
   }
 };
 
@@ -221,11 +297,13 @@ __device__ __forceinline__ Split<N> get_frag(const char* base, int frag, int lan
   return s;
 }
 
-// The block's scalars per token: e^{G_i}, e^{G_end - G_i}, beta_i (G the running sum of g).
+// The block's scalars per token: e^{G_i}, e^{G_end - G_i}, beta_i (G the running sum of g). Padded
+// to the fragments' 1 KiB.
 struct BlockScalars {
   float first[kBlock];
   float last[kBlock];
   float beta[kBlock];
+  float unused[kBlock];
 };
 
 // A sequence's place in the packed batch; ok = false where the tables contradict each other or

@@ -33,21 +33,15 @@ struct BackwardBlock {
   static constexpr int64_t reverse_bytes = bytes - scalars;   // and the reverse scan, from the scalars
 };
 
-template <typename T, int DK>
-struct ReverseLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
-  using Rows = Tile<kWide<DK>, in>;
-  static constexpr int k = 0, q = k + Rows::kBytes, ops = q + Rows::kBytes,
-                       total = ops + (int)BackwardBlock<mid>::reverse_bytes;
-};
+template <typename T, int DK, int NT>
+using ReverseLayout = FeedLayout<T, DK, 64 * NT, (int)BackwardBlock<Parts<T>::mid>::reverse_bytes, true>;
 
 template <typename T, int DK, int NT>
 __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
-  using L = ReverseLds<T, DK>;
-  using Rows = typename L::Rows;
+  using L = ReverseLayout<T, DK, NT>;
   using Ops = BackwardBlock<mid>;
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + kCols - 1) / kCols;
@@ -55,168 +49,176 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
   const int s = item / a.H, h = item - s * a.H;
   const SeqRange seq = seq_range(a, s);
   if (!seq.ok) return;  // (flagged by the scan)
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int hk = h / (a.H / a.Hk);
-  const int col = slice * kCols + wave * 16 * NT + n;
+  const int v0 = slice * kCols;
+  int col[NT];
   bool live[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) live[nt] = col + 16 * nt < a.dv;
-  const int64_t state = ((int64_t)s * a.H + h) * a.dv;
-
-  f32x4 dS[NT][kTiles];  // transposed, as S in the scan
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-      f32x8 x = {};
-      if (a.dS_out != nullptr && live[nt] && 32 * ks + 8 * g < DK)
-        x = load8(a.dS_out + (state + col + 16 * nt) * DK + 32 * ks + 8 * g);
-      dS[nt][2 * ks] = f32x4{x[0], x[1], x[2], x[3]};
-      dS[nt][2 * ks + 1] = f32x4{x[4], x[5], x[6], x[7]};
-    }
-
-  const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
-  const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
-  const int64_t do_stride = (int64_t)a.H * a.dv;
-  const T* dop = static_cast<const T*>(a.dout) + (int64_t)h * a.dv + col;
-  const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes + Ops::scalars;
-  const int64_t ws_step = (int64_t)a.H * Ops::bytes;
-  const Rows K(lds + L::k), Q(lds + L::q);
-  char* ops = lds + L::ops;
-  const BlockScalars& sc = *reinterpret_cast<const BlockScalars*>(ops);
-  const char* tt = ops + (Ops::tt - Ops::scalars);
-  const char* pt = ops + (Ops::pt - Ops::scalars);
-  if (DK < 32) {
-    zero_tile(K);
-    zero_tile(Q);
+  for (int nt = 0; nt < NT; ++nt) {
+    col[nt] = v0 + 16 * NT * wave + 16 * nt + n;
+    live[nt] = col[nt] < a.dv;
   }
+  const bool idle = v0 + 16 * NT * wave >= a.dv;
+  const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
+  StateTiles<DK, NT> dS;
+  dS.load(a.dS_out == nullptr ? nullptr : a.dS_out + state, col, live, g);
 
-  RowStage<T, DK> kst, qst;
-  OperandStage<Ops::reverse_bytes> ost;
-  T d[NT][4][4];
-  const auto fetch = [&](int c) {
-    const int64_t t0 = (int64_t)seq.begin + (int64_t)c * kBlock;
-    const int rows = seq.end - t0 < kBlock ? (int)(seq.end - t0) : kBlock;
-    kst.load(kp + t0 * a.k_stride, a.k_stride, rows);
-    qst.load(qp + t0 * a.q_stride, a.q_stride, rows);
-    ost.load(ws + c * ws_step);
-    load_cols<T, NT>(dop + t0 * do_stride, do_stride, rows, g, live, d);
-  };
-  if (seq.blocks > 0) fetch(seq.blocks - 1);
+  FeedSource<T> src;
+  src.k = static_cast<const T*>(a.k) + (int64_t)hk * DK;
+  src.q = static_cast<const T*>(a.q) + (int64_t)hk * DK;
+  src.v = static_cast<const T*>(a.dout) + (int64_t)h * a.dv + v0;
+  src.ops = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes + Ops::scalars;
+  src.k_stride = a.k_stride;
+  src.q_stride = a.q_stride;
+  src.v_stride = (int64_t)a.H * a.dv;
+  src.ops_step = (int64_t)a.H * Ops::bytes;
+  src.columns = a.dv - v0 < kCols ? a.dv - v0 : kCols;
+  src.begin = seq.begin;
+  src.end = seq.end;
+  Feed<T, DK, kCols, (int)Ops::reverse_bytes, true, L::kAsync> feed(src, lds);
+  if (seq.blocks > 0) {
+#pragma unroll
+    for (int part = 0; part < 4; ++part) feed.request(part, seq.blocks - 1);
+  }
   for (int c = seq.blocks - 1; c >= 0; --c) {
-    __syncthreads();  // (the block after has been read)
-    kst.store(K);
-    qst.store(Q);
-    ost.store(ops);
-    f32x8 dr[NT][2];  // dO as it came: rows 32 p + 8 g + 0..7 of the lane's column
+    feed.arrive(c);
+    const bool more = c > 0;
+    if (idle) {
+#pragma unroll
+      for (int part = 0; part < 4; ++part)
+        if (more) feed.request(part, c - 1);
+      continue;
+    }
+    const auto K = feed.K();
+    const auto Q = feed.Q();
+    const auto D = feed.V();
+    const char* ops = feed.ops();
+    const BlockScalars& sc = *reinterpret_cast<const BlockScalars*>(ops);
+    const char* tt = ops + (Ops::tt - Ops::scalars);
+    const char* pt = ops + (Ops::pt - Ops::scalars);
+    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
+    dS.store(kept.dS + place * a.dv * DK, col, live, g);
+
+    const auto scal8 = [&](const float* p, int h) { return load8(p + 32 * h + 8 * g); };
+    f32x4 y[NT][4], w[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) y[nt][t] = w[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x8 d[NT][2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) d[nt][p] = D.template read<false>(NT * wave + nt, p, lane);
+    {  // (operands are requested a step ahead, as in the scan)
+      Split<in> kf[2][4];
+      const auto request = [&](int ks) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) kf[ks & 1][t] = K.row8(dealt(t, n), ks, g);
+      };
+      request(0);
+      if (more) feed.request(0, c - 1);
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        if (ks + 1 < kSteps) request(ks + 1);
+        if (ks == kSteps / 2 && more) feed.request(1, c - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        Split<mid> bs[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) bs[nt] = dS.template operand<mid>(nt, ks);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) y[nt][t] = mma(kf[ks & 1][t], bs[nt], y[nt][t]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    Split<mid> bu[NT][2], tf[kFrags];
+    {
+      Split<mid> pf[kFrags];
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(pt, i, lane);
+      if (more) feed.request(2, c - 1);
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(tt, i, lane);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dr[nt][p][e] = (float)d[nt][2 * p + (e >> 2)][e & 3];
-    __syncthreads();
-    if (c > 0) fetch(c - 1);
-    if (!live[0]) continue;
-    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
+        for (int nt = 0; nt < NT; ++nt) {
+          const Split<in> bd = split8<in>(d[nt][p]);  // exact
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks)
-        if (live[nt] && 32 * ks + 8 * g < DK)
-          store8(kept.dS + (place * a.dv + col + 16 * nt) * DK + 32 * ks + 8 * g, join(dS[nt][2 * ks], dS[nt][2 * ks + 1]));
-
-    const auto scal = [&](const float* p, int t) { return ld4(p + 32 * (t >> 1) + 8 * g + 4 * (t & 1)); };
-    f32x4 dU[NT][4];
-    {
-      Split<mid> bs[NT][kSteps];
-      Split<in> bd[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) bs[nt][ks] = split8<mid>(join(dS[nt][2 * ks], dS[nt][2 * ks + 1]));
-#pragma unroll
-        for (int p = 0; p < 2; ++p) bd[nt][p] = split8<in>(dr[nt][p]);  // exact
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        f32x4 y[NT], w[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) y[nt] = w[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          const Split<in> kf = K.row8(dealt(t, n), ks, g);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) y[nt] = mma<in, mid>(kf, bs[nt][ks], y[nt]);
+          for (int t = 0; t <= 2 * p + 1; ++t) w[nt][t] = mma(pf[upper_frag(t, p)], bd, w[nt][t]);
         }
-#pragma unroll
-        for (int p = t / 2; p < 2; ++p) {
-          const Split<mid> pf = get_frag<mid>(pt, upper_frag(t, p), lane);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) w[nt] = mma<mid, in>(pf, bd[nt][p], w[nt]);
-        }
-        const f32x4 last = scal(sc.last, t);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) dU[nt][t] = last * y[nt] + a.scale * w[nt];
-      }
     }
-    f32x4 dX[NT][4];
-    {
-      Split<mid> bu[NT][2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const f32x8 last = scal8(sc.last, p);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) bu[nt][p] = split8<mid>(join(dU[nt][2 * p], dU[nt][2 * p + 1]));
+        bu[nt][p] = split8<mid>(last * join(y[nt][2 * p], y[nt][2 * p + 1]) + a.scale * join(w[nt][2 * p], w[nt][2 * p + 1]));
+    }
+    f32x8 x[NT][2];
+    {
+      f32x4 dX[NT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) dX[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = t / 2; p < 2; ++p) {
-          const Split<mid> tf = get_frag<mid>(tt, upper_frag(t, p), lane);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) dX[nt][t] = mma<mid, mid>(tf, bu[nt][p], dX[nt][t]);
+          for (int nt = 0; nt < NT; ++nt) dX[nt][t] = mma(tf[upper_frag(t, p)], bu[nt][p], dX[nt][t]);
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) x[nt][p] = join(dX[nt][2 * p], dX[nt][2 * p + 1]);
     }
-    store_cols<NT>(kept.dX + place * kBlock * a.dv + col, a.dv, g, live, dX);
+    store_cols<NT>(kept.dX + place * kBlock * a.dv + col[0], a.dv, g, live, x);
     {
       Split<mid> bd[NT][2], bx[NT][2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const f32x8 first = join(scal(sc.first, 2 * p), scal(sc.first, 2 * p + 1));
-        const f32x8 rate = first * join(scal(sc.beta, 2 * p), scal(sc.beta, 2 * p + 1));
+        const f32x8 first = scal8(sc.first, p), rate = -first * scal8(sc.beta, p);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          bd[nt][p] = split8<mid>(dr[nt][p] * first * a.scale);
-          bx[nt][p] = split8<mid>(-rate * join(dX[nt][2 * p], dX[nt][2 * p + 1]));
+          bd[nt][p] = split8<mid>(d[nt][p] * first * a.scale);
+          bx[nt][p] = split8<mid>(rate * x[nt][p]);
         }
       }
       const float whole = sc.first[kBlock - 1];
-#pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) dS[nt][tl] *= whole;
+      Split<in> qc[2][2], kc[2][2];
+      const auto request = [&](int tl) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const Split<in> qf = Q.template col8<true>(tl, p, lane), kf = K.template col8<true>(tl, p, lane);
+          qc[tl & 1][p] = Q.template col8<true>(tl, p, lane);
+          kc[tl & 1][p] = K.template col8<true>(tl, p, lane);
+        }
+      };
+      request(0);
+      if (more) feed.request(3, c - 1);
+#pragma unroll
+      for (int tl = 0; tl < kTiles; ++tl) {
+        if (tl + 1 < kTiles) request(tl + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) dS.x[nt][tl] *= whole;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            dS[nt][tl] = mma<in, mid>(qf, bd[nt][p], dS[nt][tl]);
-            dS[nt][tl] = mma<in, mid>(kf, bx[nt][p], dS[nt][tl]);
+            dS.x[nt][tl] = mma(qc[tl & 1][p], bd[nt][p], dS.x[nt][tl]);
+            dS.x[nt][tl] = mma(kc[tl & 1][p], bx[nt][p], dS.x[nt][tl]);
           }
-        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
-  if (a.dS0 == nullptr) return;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-      if (live[nt] && 32 * ks + 8 * g < DK)
-        store8(a.dS0 + (state + col + 16 * nt) * DK + 32 * ks + 8 * g, join(dS[nt][2 * ks], dS[nt][2 * ks + 1]));
+  if (a.dS0 != nullptr) dS.store(a.dS0 + state, col, live, g);
 }
 
 // The gradients kernel walks the state rows in slices of 32 (one MFMA step over dv), then needs
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_gradients_kernel(const De
     }
     __syncthreads();  // (the slices have been read)
     {
-      RowStage<T, DK> ks, qs;
+      RowStage<T, DK> ks(a.k_stride), qs(a.q_stride);
       ks.load(static_cast<const T*>(a.k) + t0 * a.k_stride + (int64_t)hk * DK, a.k_stride, rows);
       qs.load(static_cast<const T*>(a.q) + t0 * a.q_stride + (int64_t)hk * DK, a.q_stride, rows);
       if (DK < 32) {
@@ -552,7 +554,7 @@ struct BackwardSizes {
 
 template <typename T, int DK, int NT>
 hipError_t launch_reverse(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ReverseLds<T, DK>;
+  using L = ReverseLayout<T, DK, NT>;
   auto kernel = delta_reverse_kernel<T, DK, NT>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::total);
   if (e != hipSuccess) return e;
@@ -576,9 +578,12 @@ hipError_t launch_backward(const DeltaArgs& a, hipStream_t s) {
   e = launch_scan<T, DK, BackwardBlock<mid>, true>(a, kept, s);
   if (e != hipSuccess) return e;
   bool two = false;
-  e = wide_tiles(a, &two);
+  e = wide_tiles<T>(a, &two);
   if (e != hipSuccess) return e;
-  e = two ? launch_reverse<T, DK, 2>(a, kept, s) : launch_reverse<T, DK, 1>(a, kept, s);
+  if constexpr (sizeof(T) == 2)
+    e = two ? launch_reverse<T, DK, 2>(a, kept, s) : launch_reverse<T, DK, 1>(a, kept, s);
+  else
+    e = launch_reverse<T, DK, 1>(a, kept, s);
   if (e != hipSuccess) return e;
   using L = GradLds<T, DK>;
   auto kernel = delta_gradients_kernel<T, DK>;

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, g = lane >> 4;
 
-  RowStage<T, DK> ks, qs;
+  RowStage<T, DK> ks(a.k_stride), qs(a.q_stride);
   ks.load(static_cast<const T*>(a.k) + t0 * a.k_stride + (int64_t)hk * DK, a.k_stride, rows);
   qs.load(static_cast<const T*>(a.q) + t0 * a.q_stride + (int64_t)hk * DK, a.q_stride, rows);
   const Rows K(lds + L::k), Q(lds + L::q);
@@ -210,42 +210,6 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
       put_frag<mid>(out + Out::tt, upper_frag(wave, si), lane, split8<mid>(x));
     }
   }
-}
-
-// The operands of one block (16-byte units), from the workspace to LDS.
-template <int64_t BYTES>
-struct OperandStage {
-  static constexpr int kUnits = (int)(BYTES / 16);
-  static constexpr int kPer = (kUnits + kChunkThreads - 1) / kChunkThreads;
-  f32x4 x[kPer];
-  __device__ __forceinline__ void load(const char* p) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int unit = i * kChunkThreads + threadIdx.x;
-      if (unit < kUnits) x[i] = *reinterpret_cast<const f32x4*>(p + unit * 16);
-    }
-  }
-  __device__ __forceinline__ void store(char* dst) const {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int unit = i * kChunkThreads + threadIdx.x;
-      if (unit < kUnits) *reinterpret_cast<f32x4*>(dst + unit * 16) = x[i];
-    }
-  }
-};
-
-// A wavefront's columns of a [token][H][dv] array, in the order of the result tiles.
-template <typename T, int NT>
-__device__ __forceinline__ void load_cols(const T* p, int64_t stride, int rows, int g, const bool (&live)[NT],
-                                          T (&x)[NT][4][4]) {
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][t][r] = (row < rows && live[nt]) ? p[row * stride + 16 * nt] : (T)0.f;
-    }
 }
 
 // Lets `kernel` use `bytes` of dynamic LDS (past 64 KiB it has to be asked for).

@@ -2,6 +2,7 @@
 // recomputation of states.
 #pragma once
 
+#include "feed.hpp"
 #include "prepare.hpp"
 
 namespace rs {
@@ -17,35 +18,65 @@ struct Kept {
   float* dX;
 };
 
-// A wavefront's result tiles to its columns of a [64][dv] fp32 array.
+// A wavefront's result tiles (two of one column joined: rows 32 p + 8 g .. + 7) to a [64][dv] fp32 array.
 template <int NT>
-__device__ __forceinline__ void store_cols(float* p, int dv, int g, const bool (&live)[NT], const f32x4 (&x)[NT][4]) {
+__device__ __forceinline__ void store_cols(float* p, int dv, int g, const bool (&live)[NT], const f32x8 (&x)[NT][2]) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int e = 0; e < 8; ++e)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        if (live[nt]) p[(32 * (t >> 1) + 8 * g + 4 * (t & 1) + r) * dv + 16 * nt] = x[nt][t][r];
+        if (live[nt]) p[(32 * h + 8 * g + e) * dv + 16 * nt] = x[nt][h][e];
 }
 
-template <typename T, int DK, typename Ops, bool KEEP>
-struct ScanLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
-  using Rows = Tile<kWide<DK>, in>;
-  static constexpr int k = 0, q = k + Rows::kBytes, ops = q + (KEEP ? 0 : Rows::kBytes),
-                       total = ops + (int)Ops::scan_bytes;
+// State rows of a wavefront, transposed: tiles 2ks and 2ks + 1 hold channels 32 ks + 8 g + 0..3 and + 4..7 of
+// the lane's row.
+template <int DK, int NT>
+struct StateTiles {
+  static constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
+  f32x4 x[NT][kTiles];
+  // rows: the lane's row of each tile in an array of [..][DK]; NULL reads as zero
+  __device__ __forceinline__ void load(const float* p, const int (&row)[NT], const bool (&live)[NT], int g) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        f32x8 v = {};
+        if (p != nullptr && live[nt] && 32 * ks + 8 * g < DK) v = load8(p + row[nt] * DK + 32 * ks + 8 * g);
+        x[nt][2 * ks] = f32x4{v[0], v[1], v[2], v[3]};
+        x[nt][2 * ks + 1] = f32x4{v[4], v[5], v[6], v[7]};
+      }
+  }
+  __device__ __forceinline__ void store(float* p, const int (&row)[NT], const bool (&live)[NT], int g) const {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+        if (live[nt] && 32 * ks + 8 * g < DK)
+          store8(p + row[nt] * DK + 32 * ks + 8 * g, join(x[nt][2 * ks], x[nt][2 * ks + 1]));
+  }
+  template <int N>
+  __device__ __forceinline__ Split<N> operand(int nt, int ks) const {
+    return split8<N>(join(x[nt][2 * ks], x[nt][2 * ks + 1]));
+  }
 };
+
+template <typename T, int DK, int NT, typename Ops, bool KEEP>
+using ScanLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::scan_bytes, !KEEP>;
 
 // NT result tiles of 16 state rows per wavefront. With KEEP (the backward pass) it writes the state
 // before each block and the block's corrections in place of outputs.
+//
+// Outputs are computed transposed (state rows by tokens): the operands of a product can change places,
+// and a lane then holds 4 NT neighbouring state rows of one token, which it stores in one piece.
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
-  using L = ScanLds<T, DK, Ops, KEEP>;
-  using Rows = typename L::Rows;
+  constexpr bool kDealt = NT == 2 && !KEEP;  // a lane's output rows of both tiles are neighbours
+  using L = ScanLayout<T, DK, NT, Ops, KEEP>;
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + kCols - 1) / kCols;
   const int slice = blockIdx.x % slices, item = blockIdx.x / slices;
@@ -55,158 +86,178 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
     if (threadIdx.x == 0 && slice == 0 && h == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int hk = h / (a.H / a.Hk);
-  const int col = slice * kCols + wave * 16 * NT + n;  // of the first tile
+  const int v0 = slice * kCols;
+  int col[NT];  // of the head's dv, per tile
   bool live[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) live[nt] = col + 16 * nt < a.dv;
-  const int64_t state = ((int64_t)s * a.H + h) * a.dv;
-
-  // S^T: tiles 2ks and 2ks + 1 hold channels 32 ks + 8 g + 0..3 and + 4..7 of state row col
-  f32x4 S[NT][kTiles];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-      f32x8 x = {};
-      if (a.S0 != nullptr && live[nt] && 32 * ks + 8 * g < DK)
-        x = load8(a.S0 + (state + col + 16 * nt) * DK + 32 * ks + 8 * g);
-      S[nt][2 * ks] = f32x4{x[0], x[1], x[2], x[3]};
-      S[nt][2 * ks + 1] = f32x4{x[4], x[5], x[6], x[7]};
-    }
-
-  const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
-  const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
-  const T* vp = static_cast<const T*>(a.v) + (int64_t)h * a.dv + col;
-  T* op = static_cast<T*>(a.out) + (int64_t)h * a.dv + col;
-  const int64_t out_stride = (int64_t)a.H * a.dv;
-  const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
-  const int64_t ws_step = (int64_t)a.H * Ops::bytes;
-  const Rows K(lds + L::k), Q(lds + L::q);
-  char* ops = lds + L::ops;
-  const BlockScalars& sc = *reinterpret_cast<const BlockScalars*>(ops + Ops::scalars);
-  if (DK < 32) {
-    zero_tile(K);
-    if (!KEEP) zero_tile(Q);
+  for (int nt = 0; nt < NT; ++nt) {
+    col[nt] = v0 + 16 * NT * wave + (kDealt ? dealt(nt, n) : 16 * nt + n);
+    live[nt] = col[nt] < a.dv;
   }
+  const bool idle = v0 + 16 * NT * wave >= a.dv;  // the whole wavefront
+  const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
+  StateTiles<DK, NT> S;
+  S.load(a.S0 == nullptr ? nullptr : a.S0 + state, col, live, g);
 
-  RowStage<T, DK> kst, qst;
-  OperandStage<Ops::scan_bytes> ost;
-  T v[NT][4][4];
-  const auto fetch = [&](int c) {
-    const int64_t t0 = (int64_t)seq.begin + (int64_t)c * kBlock;
-    const int rows = seq.end - t0 < kBlock ? (int)(seq.end - t0) : kBlock;
-    kst.load(kp + t0 * a.k_stride, a.k_stride, rows);
-    if (!KEEP) qst.load(qp + t0 * a.q_stride, a.q_stride, rows);
-    ost.load(ws + c * ws_step);
-    load_cols<T, NT>(vp + t0 * a.v_stride, a.v_stride, rows, g, live, v);
-  };
-  if (seq.blocks > 0) fetch(0);
+  const int64_t out_stride = (int64_t)a.H * a.dv;
+  // the first of the lane's 4 NT neighbouring output rows
+  const int out_col = v0 + 16 * NT * wave + 4 * NT * g;
+  T* op = static_cast<T*>(a.out) + (int64_t)h * a.dv + out_col;
+  FeedSource<T> src;
+  src.k = static_cast<const T*>(a.k) + (int64_t)hk * DK;
+  src.q = static_cast<const T*>(a.q) + (int64_t)hk * DK;
+  src.v = static_cast<const T*>(a.v) + (int64_t)h * a.dv + v0;
+  src.ops = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
+  src.k_stride = a.k_stride;
+  src.q_stride = a.q_stride;
+  src.v_stride = a.v_stride;
+  src.ops_step = (int64_t)a.H * Ops::bytes;
+  src.columns = a.dv - v0 < kCols ? a.dv - v0 : kCols;
+  src.begin = seq.begin;
+  src.end = seq.end;
+  Feed<T, DK, kCols, (int)Ops::scan_bytes, !KEEP, L::kAsync> feed(src, lds);
+  if (seq.blocks > 0) {
+#pragma unroll
+    for (int part = 0; part < 4; ++part) feed.request(part, 0);
+  }
   for (int c = 0; c < seq.blocks; ++c) {
-    const int64_t t0 = (int64_t)seq.begin + (int64_t)c * kBlock;
-    const int rows = seq.end - t0 < kBlock ? (int)(seq.end - t0) : kBlock;
-    __syncthreads();  // (the block before has been read)
-    kst.store(K);
-    if (!KEEP) qst.store(Q);
-    ost.store(ops);
-    f32x4 X[NT][4];
+    feed.arrive(c);
+    const bool more = c + 1 < seq.blocks;
+    if (idle) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) X[nt][t][r] = (float)v[nt][t][r];
-    __syncthreads();
-    if (c + 1 < seq.blocks) fetch(c + 1);
-    if (!live[0]) continue;
-    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    if constexpr (KEEP) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks)
-          if (live[nt] && 32 * ks + 8 * g < DK)
-            store8(kept.S + (place * a.dv + col + 16 * nt) * DK + 32 * ks + 8 * g, join(S[nt][2 * ks], S[nt][2 * ks + 1]));
+      for (int part = 0; part < 4; ++part)
+        if (more) feed.request(part, c + 1);
+      continue;
     }
+    const int rows = feed.rows(c);
+    const int64_t t0 = feed.token(c);
+    const auto K = feed.K();
+    const auto Q = feed.Q();
+    const auto V = feed.V();
+    const char* ops = feed.ops();
+    const BlockScalars& sc = *reinterpret_cast<const BlockScalars*>(ops + Ops::scalars);
+    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
+    if constexpr (KEEP) S.store(kept.S + place * a.dv * DK, col, live, g);
 
-    Split<mid> bs[NT][kSteps];
+    f32x8 v[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) bs[nt][ks] = split8<mid>(join(S[nt][2 * ks], S[nt][2 * ks + 1]));
-    const auto scal = [&](const float* p, int t) { return ld4(p + 32 * (t >> 1) + 8 * g + 4 * (t & 1)); };
+      for (int p = 0; p < 2; ++p) v[nt][p] = V.template read<kDealt>(NT * wave + nt, p, lane);
+    f32x4 y[NT][4], o[NT][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 y[NT];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) y[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < 4; ++t) y[nt][t] = o[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    {
+      // Operands of one step are requested before the step in front of them is computed, and the
+      // compiler is kept from moving the requests back to their uses: a wavefront has its SIMD
+      // to itself here, so nothing else would cover an LDS read's latency.
+      Split<in> kf[2][4], qf[2][4];
+      const auto request = [&](int ks) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          kf[ks & 1][t] = K.row8(dealt(t, n), ks, g);
+          if constexpr (!KEEP) qf[ks & 1][t] = Q.row8(dealt(t, n), ks, g);
+        }
+      };
+      request(0);
+      // the next block is asked for in parts between the steps: asked for at once, it would hold up
+      // the wavefront until the memory pipeline has taken it all
+      if (more) feed.request(0, c + 1);
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
-        const Split<in> kf = K.row8(dealt(t, n), ks, g);
+        if (ks + 1 < kSteps) request(ks + 1);
+        if (ks == kSteps / 2 && more) feed.request(1, c + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        Split<mid> bs[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) y[nt] = mma<in, mid>(kf, bs[nt][ks], y[nt]);
+        for (int nt = 0; nt < NT; ++nt) bs[nt] = S.template operand<mid>(nt, ks);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            y[nt][t] = mma(kf[ks & 1][t], bs[nt], y[nt][t]);
+            if constexpr (!KEEP) o[nt][t] = mma(bs[nt], qf[ks & 1][t], o[nt][t]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const f32x4 first = scal(sc.first, t), beta = scal(sc.beta, t);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) X[nt][t] = beta * (X[nt][t] - first * y[nt]);
     }
-    f32x4 U[NT][4];
+    const auto scal8 = [&](const float* p, int h) { return load8(p + 32 * h + 8 * g); };
+    f32x8 u[NT][2];
     {
-      Split<mid> bx[NT][2];
+      Split<mid> bx[NT][2], tf[kFrags];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(ops + Ops::t, i, lane);
+      if (more) feed.request(2, c + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) bx[nt][p] = split8<mid>(join(X[nt][2 * p], X[nt][2 * p + 1]));
+      for (int p = 0; p < 2; ++p) {
+        const f32x8 first = scal8(sc.first, p), beta = scal8(sc.beta, p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          bx[nt][p] = split8<mid>(beta * (v[nt][p] - first * join(y[nt][2 * p], y[nt][2 * p + 1])));
+      }
+      f32x4 U[NT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) U[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p <= t / 2; ++p) {
-          const Split<mid> tf = get_frag<mid>(ops + Ops::t, lower_frag(t, p), lane);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) U[nt][t] = mma<mid, mid>(tf, bx[nt][p], U[nt][t]);
+          for (int nt = 0; nt < NT; ++nt) U[nt][t] = mma(tf[lower_frag(t, p)], bx[nt][p], U[nt][t]);
         }
       }
-    }
-    if constexpr (KEEP) {
-      store_cols<NT>(kept.U + place * kBlock * a.dv + col, a.dv, g, live, U);
-    } else {  // outputs
-      Split<mid> bu[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) bu[nt][p] = split8<mid>(join(U[nt][2 * p], U[nt][2 * p + 1]));
+        for (int p = 0; p < 2; ++p) u[nt][p] = join(U[nt][2 * p], U[nt][2 * p + 1]);
+    }
+    if constexpr (KEEP) {
+      store_cols<NT>(kept.U + place * kBlock * a.dv + col[0], a.dv, g, live, u);
+    } else {
+      Split<mid> bu[NT][2], pf[kFrags];
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(ops + Ops::p, i, lane);
+      float first[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) first[t] = sc.first[dealt(t, n)];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) bu[nt][p] = split8<mid>(u[nt][p]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        f32x4 o[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          const Split<in> qf = Q.row8(dealt(t, n), ks, g);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) o[nt] = mma<in, mid>(qf, bs[nt][ks], o[nt]);
-        }
-        const f32x4 first = scal(sc.first, t);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[nt] *= first;
+        for (int nt = 0; nt < NT; ++nt) o[nt][t] *= first[t];
 #pragma unroll
         for (int p = 0; p <= t / 2; ++p) {
-          const Split<mid> pf = get_frag<mid>(ops + Ops::p, lower_frag(t, p), lane);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) o[nt] = mma<mid, mid>(pf, bu[nt][p], o[nt]);
+          for (int nt = 0; nt < NT; ++nt) o[nt][t] = mma(bu[nt][p], pf[lower_frag(t, p)], o[nt][t]);
         }
+      }
+      const auto put = [&](int t) {
+        T* dst = op + (t0 + dealt(t, n)) * out_stride;
+        if constexpr (NT == 2) {
+          store8(dst, join(o[0][t], o[1][t]) * a.scale);
+        } else {
+          typedef T vec __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<vec*>(dst) = __builtin_convertvector(o[0][t] * a.scale, vec);
+        }
+      };
+      if (out_col < a.dv) {
+        if (rows == kBlock) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r;
-          if (row < rows) {
+          for (int t = 0; t < 4; ++t) put(t);
+        } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              if (live[nt]) op[(t0 + row) * out_stride + 16 * nt] = (T)(o[nt][r] * a.scale);
-          }
+          for (int t = 0; t < 4; ++t)
+            if (dealt(t, n) < rows) put(t);
         }
       }
     }
@@ -214,36 +265,39 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
       Split<mid> bl[NT][2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const f32x4 l0 = scal(sc.last, 2 * p), l1 = scal(sc.last, 2 * p + 1);
+        const f32x8 last = scal8(sc.last, p);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) bl[nt][p] = split8<mid>(join(l0 * U[nt][2 * p], l1 * U[nt][2 * p + 1]));
+        for (int nt = 0; nt < NT; ++nt) bl[nt][p] = split8<mid>(last * u[nt][p]);
       }
       const float whole = sc.first[kBlock - 1];
+      Split<in> kc[2][2];
+      const auto request = [&](int tl) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) kc[tl & 1][p] = K.template col8<true>(tl, p, lane);
+      };
+      request(0);
+      if (more) feed.request(3, c + 1);
 #pragma unroll
       for (int tl = 0; tl < kTiles; ++tl) {
+        if (tl + 1 < kTiles) request(tl + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[nt][tl] *= whole;
+        for (int nt = 0; nt < NT; ++nt) S.x[nt][tl] *= whole;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const Split<in> kf = K.template col8<true>(tl, p, lane);
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) S[nt][tl] = mma<in, mid>(kf, bl[nt][p], S[nt][tl]);
-        }
+          for (int nt = 0; nt < NT; ++nt) S.x[nt][tl] = mma(kc[tl & 1][p], bl[nt][p], S.x[nt][tl]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
-  if (a.S_out == nullptr) return;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-      if (live[nt] && 32 * ks + 8 * g < DK)
-        store8(a.S_out + (state + col + 16 * nt) * DK + 32 * ks + 8 * g, join(S[nt][2 * ks], S[nt][2 * ks + 1]));
+  if (a.S_out == nullptr || KEEP) return;
+  S.store(a.S_out + state, col, live, g);
 }
 
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 hipError_t launch_scan_tiles(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ScanLds<T, DK, Ops, KEEP>;
+  using L = ScanLayout<T, DK, NT, Ops, KEEP>;
   auto kernel = delta_scan_kernel<T, DK, NT, Ops, KEEP>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::total);
   if (e != hipSuccess) return e;
@@ -253,20 +307,25 @@ hipError_t launch_scan_tiles(const DeltaArgs& a, const Kept& kept, hipStream_t s
 }
 
 // Two tiles per wavefront read each operand from LDS once for 32 state rows; one tile gives
-// twice the workgroups where there are fewer than the chip has compute units.
-inline hipError_t wide_tiles(const DeltaArgs& a, bool* two) {
+// twice the workgroups where there are fewer than the chip has compute units. fp32 inputs, whose three
+// parts fill the LDS and the registers, keep one.
+template <typename T>
+hipError_t wide_tiles(const DeltaArgs& a, bool* two) {
   int cus = 0;
   const hipError_t e = device_cus(&cus);
-  *two = e == hipSuccess && a.dv > 64 && (int64_t)a.n_seqs * a.H * ((a.dv + 127) / 128) >= cus;
+  *two = e == hipSuccess && sizeof(T) == 2 && a.dv > 64 && (int64_t)a.n_seqs * a.H * ((a.dv + 127) / 128) >= cus;
   return e;
 }
 
 template <typename T, int DK, typename Ops, bool KEEP>
 hipError_t launch_scan(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
   bool two = false;
-  const hipError_t e = wide_tiles(a, &two);
+  const hipError_t e = wide_tiles<T>(a, &two);
   if (e != hipSuccess) return e;
-  return two ? launch_scan_tiles<T, DK, 2, Ops, KEEP>(a, kept, s) : launch_scan_tiles<T, DK, 1, Ops, KEEP>(a, kept, s);
+  if constexpr (sizeof(T) == 2) {
+    if (two) return launch_scan_tiles<T, DK, 2, Ops, KEEP>(a, kept, s);
+  }
+  return launch_scan_tiles<T, DK, 1, Ops, KEEP>(a, kept, s);
 }
 
 }  // namespace
