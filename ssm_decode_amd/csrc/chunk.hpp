@@ -59,15 +59,26 @@ __device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) {
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// acc += A B over the kept products of parts, smallest first.
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 mma(const Split<NA>& a, const Split<NB>& b, f32x4 acc) {
+// The kept products of parts, smallest first: f(i, j) for part i of A and part j of B.
+template <int NA, int NB, typename F>
+__device__ __forceinline__ void products(const F& f) {
   constexpr int kOrder = NA > NB ? NA : NB;
 #pragma unroll
   for (int o = kOrder - 1; o >= 0; --o)
 #pragma unroll
     for (int i = 0; i < NA; ++i)
-      if (o - i >= 0 && o - i < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[o - i], acc, 0, 0, 0);
+      if (o - i >= 0 && o - i < NB) f(i, o - i);
+}
+
+__device__ __forceinline__ f32x4 mfma(const bf16x8& a, const bf16x8& b, const f32x4& acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+}
+
+// acc += A B. (Its products wait for each other; where several results are built at once, `products`
+// around the loop over them keeps the matrix pipe full.)
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Split<NA>& a, const Split<NB>& b, f32x4 acc) {
+  products<NA, NB>([&](int i, int j) { acc = mfma(a.p[i], b.p[j], acc); });
   return acc;
 }
 

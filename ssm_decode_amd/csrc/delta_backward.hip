@@ -128,10 +128,12 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
         Split<mid> bs[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) bs[nt] = dS.template operand<mid>(nt, ks);
+        products<in, mid>([&](int i, int j) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) y[nt][t] = mma(kf[ks & 1][t], bs[nt], y[nt][t]);
+            for (int nt = 0; nt < NT; ++nt) y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
+        });
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -149,8 +151,10 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const Split<in> bd = split8<in>(d[nt][p]);  // exact
+          products<mid, in>([&](int i, int j) {
 #pragma unroll
-          for (int t = 0; t <= 2 * p + 1; ++t) w[nt][t] = mma(pf[upper_frag(t, p)], bd, w[nt][t]);
+            for (int t = 0; t <= 2 * p + 1; ++t) w[nt][t] = mfma(pf[upper_frag(t, p)].p[i], bd.p[j], w[nt][t]);
+          });
         }
     }
 #pragma unroll
@@ -164,15 +168,17 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
     {
       f32x4 dX[NT][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) dX[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int p = t / 2; p < 2; ++p) {
+      for (int p = 0; p < 2; ++p)
+        products<mid, mid>([&](int i, int j) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) dX[nt][t] = mma(tf[upper_frag(t, p)], bu[nt][p], dX[nt][t]);
-        }
-      }
+          for (int t = 0; t <= 2 * p + 1; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) dX[nt][t] = mfma(tf[upper_frag(t, p)].p[i], bu[nt][p].p[j], dX[nt][t]);
+        });
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -191,29 +197,41 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
         }
       }
       const float whole = sc.first[kBlock - 1];
-      Split<in> qc[2][2], kc[2][2];
-      const auto request = [&](int tl) {
+      constexpr int kGroup = in == 3 ? 1 : 2;
+      Split<in> qc[2][kGroup][2], kc[2][kGroup][2];
+      const auto request = [&](int group) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          qc[tl & 1][p] = Q.template col8<true>(tl, p, lane);
-          kc[tl & 1][p] = K.template col8<true>(tl, p, lane);
-        }
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            qc[group & 1][i][p] = Q.template col8<true>(group * kGroup + i, p, lane);
+            kc[group & 1][i][p] = K.template col8<true>(group * kGroup + i, p, lane);
+          }
       };
       request(0);
       if (more) feed.request(3, c - 1);
 #pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) {
-        if (tl + 1 < kTiles) request(tl + 1);
+      for (int group = 0; group < kTiles / kGroup; ++group) {
+        if (group + 1 < kTiles / kGroup) request(group + 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) dS.x[nt][tl] *= whole;
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) dS.x[nt][group * kGroup + i] *= whole;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
+          products<in, mid>([&](int x, int y) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            dS.x[nt][tl] = mma(qc[tl & 1][p], bd[nt][p], dS.x[nt][tl]);
-            dS.x[nt][tl] = mma(kc[tl & 1][p], bx[nt][p], dS.x[nt][tl]);
-          }
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+              for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  f32x4& acc = dS.x[nt][group * kGroup + i];
+                  acc = z == 0 ? mfma(qc[group & 1][i][p].p[x], bd[nt][p].p[y], acc)
+                               : mfma(kc[group & 1][i][p].p[x], bx[nt][p].p[y], acc);
+                }
+          });
         __builtin_amdgcn_sched_barrier(0);
       }
     }

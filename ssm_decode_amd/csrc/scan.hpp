@@ -176,71 +176,125 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
         Split<mid> bs[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) bs[nt] = S.template operand<mid>(nt, ks);
+        products<in, mid>([&](int i, int j) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            y[nt][t] = mma(kf[ks & 1][t], bs[nt], y[nt][t]);
-            if constexpr (!KEEP) o[nt][t] = mma(bs[nt], qf[ks & 1][t], o[nt][t]);
-          }
+            for (int nt = 0; nt < NT; ++nt) {
+              y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
+              if constexpr (!KEEP) o[nt][t] = mfma(bs[nt].p[j], qf[ks & 1][t].p[i], o[nt][t]);
+            }
+        });
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     const auto scal8 = [&](const float* p, int h) { return load8(p + 32 * h + 8 * g); };
     f32x8 u[NT][2];
+    Split<mid> pf[kFrags];
+    float first_t[4];
     {
       Split<mid> bx[NT][2], tf[kFrags];
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(ops + Ops::t, i, lane);
+      const f32x8 first[2] = {scal8(sc.first, 0), scal8(sc.first, 1)}, beta[2] = {scal8(sc.beta, 0), scal8(sc.beta, 1)};
       if (more) feed.request(2, c + 1);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const f32x8 first = scal8(sc.first, p), beta = scal8(sc.beta, p);
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          bx[nt][p] = split8<mid>(beta * (v[nt][p] - first * join(y[nt][2 * p], y[nt][2 * p + 1])));
+          bx[nt][p] = split8<mid>(beta[p] * (v[nt][p] - first[p] * join(y[nt][2 * p], y[nt][2 * p + 1])));
+      if constexpr (!KEEP) {
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(ops + Ops::p, i, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) first_t[t] = sc.first[dealt(t, n)];
       }
+      __builtin_amdgcn_sched_barrier(0);
       f32x4 U[NT][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) U[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int p = 0; p <= t / 2; ++p) {
+      for (int p = 0; p < 2; ++p)
+        products<mid, mid>([&](int i, int j) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) U[nt][t] = mma(tf[lower_frag(t, p)], bx[nt][p], U[nt][t]);
-        }
-      }
+          for (int t = 2 * p; t < 4; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) U[nt][t] = mfma(tf[lower_frag(t, p)].p[i], bx[nt][p].p[j], U[nt][t]);
+        });
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int p = 0; p < 2; ++p) u[nt][p] = join(U[nt][2 * p], U[nt][2 * p + 1]);
     }
+    // The state's operands come through LDS transposed, a group of tiles ahead of their products.
+    constexpr int kGroup = in == 1 ? 4 : 2;
+    static_assert(kTiles % 2 == 0, "groups are whole");
+    constexpr int kTileGroup = kTiles < kGroup ? kTiles : kGroup;
+    Split<in> kc[2][kTileGroup][2];
+    const auto request_state = [&](int group) {
+#pragma unroll
+      for (int i = 0; i < kTileGroup; ++i)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) kc[group & 1][i][p] = K.template col8<true>(group * kTileGroup + i, p, lane);
+    };
+    request_state(0);
+    const f32x8 last[2] = {scal8(sc.last, 0), scal8(sc.last, 1)};
+    const float whole = sc.first[kBlock - 1];
+    if (more) feed.request(3, c + 1);
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (KEEP) {
       store_cols<NT>(kept.U + place * kBlock * a.dv + col[0], a.dv, g, live, u);
-    } else {
-      Split<mid> bu[NT][2], pf[kFrags];
-#pragma unroll
-      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(ops + Ops::p, i, lane);
-      float first[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) first[t] = sc.first[dealt(t, n)];
-      __builtin_amdgcn_sched_barrier(0);
+    } else {  // outputs
+      Split<mid> bu[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int p = 0; p < 2; ++p) bu[nt][p] = split8<mid>(u[nt][p]);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[nt][t] *= first[t];
+        for (int nt = 0; nt < NT; ++nt) o[nt][t] *= first_t[t];
 #pragma unroll
-        for (int p = 0; p <= t / 2; ++p) {
+      for (int p = 0; p < 2; ++p)
+        products<mid, mid>([&](int i, int j) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) o[nt][t] = mma(bu[nt][p], pf[lower_frag(t, p)], o[nt][t]);
-        }
+          for (int t = 2 * p; t < 4; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) o[nt][t] = mfma(bu[nt][p].p[i], pf[lower_frag(t, p)].p[j], o[nt][t]);
+        });
+    }
+    {  // state
+      Split<mid> bl[NT][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) bl[nt][p] = split8<mid>(last[p] * u[nt][p]);
+#pragma unroll
+      for (int group = 0; group < kTiles / kTileGroup; ++group) {
+        if (group + 1 < kTiles / kTileGroup) request_state(group + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kTileGroup; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) S.x[nt][group * kTileGroup + i] *= whole;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          products<in, mid>([&](int x, int y) {
+#pragma unroll
+            for (int i = 0; i < kTileGroup; ++i)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                f32x4& acc = S.x[nt][group * kTileGroup + i];
+                acc = mfma(kc[group & 1][i][p].p[x], bl[nt][p].p[y], acc);
+              }
+          });
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    if constexpr (!KEEP) {
       const auto put = [&](int t) {
         T* dst = op + (t0 + dealt(t, n)) * out_stride;
         if constexpr (NT == 2) {
@@ -259,35 +313,6 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
           for (int t = 0; t < 4; ++t)
             if (dealt(t, n) < rows) put(t);
         }
-      }
-    }
-    {  // state
-      Split<mid> bl[NT][2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const f32x8 last = scal8(sc.last, p);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) bl[nt][p] = split8<mid>(last * u[nt][p]);
-      }
-      const float whole = sc.first[kBlock - 1];
-      Split<in> kc[2][2];
-      const auto request = [&](int tl) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) kc[tl & 1][p] = K.template col8<true>(tl, p, lane);
-      };
-      request(0);
-      if (more) feed.request(3, c + 1);
-#pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) {
-        if (tl + 1 < kTiles) request(tl + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S.x[nt][tl] *= whole;
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) S.x[nt][tl] = mma(kc[tl & 1][p], bl[nt][p], S.x[nt][tl]);
-        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
