@@ -420,46 +420,68 @@ class ConvLayer:
 
 # ---- the prompt side: ragged tables, query/key norm, the delta rule over sequences ----
 
-def _dev(t, dtype, shape=None, what="tensor"):
-    """Pointer of a contiguous tensor of the current GPU with this type (and shape); None stays None."""
+# These calls may be a few microseconds of GPU work, so the checks read each tensor attribute once.
+
+def _device_and_stream(stream):
+    """The current GPU and the stream a call goes to."""
+    try:
+        dev = torch.cuda.current_device()
+    except RuntimeError as e:
+        raise ValueError(f"tensors must be on the GPU: {e}") from e
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _off_device(t, dev, what):
+    if not t.is_cuda:
+        return ValueError(f"{what} must be on the GPU")
+    return ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _dev(t, dev, dtype, shape, what):
+    """Pointer of a contiguous tensor of GPU `dev` with this type and shape (None: any); None stays None."""
     if t is None:
         return None
-    _on_current(t, what)
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise _off_device(t, dev, what)
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: {dtype} tensor expected, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _on_current(t, what):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _rows(t, dtype, tokens, heads, dim, stride, what):
+def _rows(t, dev, dtype, shape, stride, what):
     """Pointer of [tokens, heads, dim] rows whose heads lie together and whose tokens lie `stride` elements apart."""
-    _on_current(t, what)
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise _off_device(t, dev, what)
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: {dtype} tensor expected, got {t.dtype}")
-    if tuple(t.shape) != (tokens, heads, dim):
-        raise ValueError(f"{what}: shape {(tokens, heads, dim)} expected, got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim) or (tokens > 1 and t.stride(0) != stride):
-        raise ValueError(f"{what}: strides ({stride}, {dim}, 1) expected, got {t.stride()}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {shape} expected, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != shape[2] and shape[1] > 1) or (s[0] != stride and shape[0] > 1):
+        raise ValueError(f"{what}: strides ({stride}, {shape[2]}, 1) expected, got {s}")
     return t.data_ptr()
 
 
-def _workspace(t, need, what="workspace"):
+def _workspace(t, dev, need):
     if t is None:
         return None
-    _on_current(t, what)
-    if not t.is_contiguous() or t.numel() * t.element_size() < need:
-        raise ValueError(f"{what} must be contiguous and hold {need} bytes")
+    if t.get_device() != dev:
+        raise _off_device(t, dev, "workspace")
+    if t.numel() * t.element_size() < need or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and hold {need} bytes")
     return t.data_ptr()
+
+
+def _torch_dtype(value, where):
+    if value not in TORCH_DTYPES:
+        raise ReplaySSMError(EINVAL, where, f"dtype {value} unknown")
+    return TORCH_DTYPES[value]
 
 
 def make_ragged_config(n_seqs, max_tokens, block=DELTA_BLOCK) -> RaggedConfig:
@@ -474,9 +496,10 @@ def ragged_sizes(cfg: RaggedConfig) -> int:
 
 def ragged_maps(cfg, maps, lengths, history=None, stream=None):
     n = (cfg.n_seqs,)
+    dev, s = _device_and_stream(stream)
     _check(lib().replayssm_ragged_maps(ctypes.byref(cfg), ctypes.byref(maps),
-                                       _dev(lengths, torch.int32, n, "lengths"),
-                                       _dev(history, torch.int32, n, "history"), _s(stream)), "ragged_maps")
+                                       _dev(lengths, dev, torch.int32, n, "lengths"),
+                                       _dev(history, dev, torch.int32, n, "history"), s), "ragged_maps")
 
 
 class RaggedMaps:
@@ -513,36 +536,41 @@ def qk_norm_sizes(cfg: QkNormConfig) -> int:
     return int(n.value)
 
 
-def _qk_inputs(cfg, q, k, wq, wk, positions, inv_freq):
-    t, n = TORCH_DTYPES[cfg.dtype], cfg.n_tokens
-    return (_rows(q, t, n, cfg.Hq, cfg.D, cfg.q_stride, "q") if cfg.Hq else None,
-            _rows(k, t, n, cfg.Hk, cfg.D, cfg.k_stride, "k") if cfg.Hk else None,
-            _dev(wq, torch.float32, (cfg.D,), "wq"), _dev(wk, torch.float32, (cfg.D,), "wk"),
-            _dev(positions, torch.int32, (n,), "positions") if cfg.rot else None,
-            _dev(inv_freq, torch.float32, (cfg.rot // 2,), "inv_freq") if cfg.rot else None)
+def _qk_inputs(cfg, dev, q, k, wq, wk, positions, inv_freq):
+    t, n, D, rot, f32 = _torch_dtype(cfg.dtype, "qk_norm"), cfg.n_tokens, cfg.D, cfg.rot, torch.float32
+    try:
+        return (_rows(q, dev, t, (n, cfg.Hq, D), cfg.q_stride, "q") if cfg.Hq else None,
+                _rows(k, dev, t, (n, cfg.Hk, D), cfg.k_stride, "k") if cfg.Hk else None,
+                _dev(wq, dev, f32, (D,), "wq"), _dev(wk, dev, f32, (D,), "wk"),
+                _dev(positions, dev, torch.int32, (n,), "positions") if rot else None,
+                _dev(inv_freq, dev, f32, (rot // 2,), "inv_freq") if rot else None)
+    except (TypeError, ValueError):
+        qk_norm_sizes(cfg)  # a configuration that the library refuses is named first
+        raise
 
 
 def qk_norm(cfg, q, k, wq, wk, positions, inv_freq, q_out, k_out, stream=None):
-    qk_norm_sizes(cfg)  # validates
-    o, n = TORCH_DTYPES[cfg.out_dtype], cfg.n_tokens
+    dev, s = _device_and_stream(stream)
+    o, n = _torch_dtype(cfg.out_dtype, "qk_norm"), cfg.n_tokens
     _check(lib().replayssm_qk_norm(
-        ctypes.byref(cfg), *_qk_inputs(cfg, q, k, wq, wk, positions, inv_freq),
-        _dev(q_out, o, (n, cfg.Hq * cfg.rep, cfg.D), "q_out") if cfg.Hq else None,
-        _dev(k_out, o, (n, cfg.Hk * cfg.rep, cfg.D), "k_out") if cfg.Hk else None, _s(stream)), "qk_norm")
+        ctypes.byref(cfg), *_qk_inputs(cfg, dev, q, k, wq, wk, positions, inv_freq),
+        _dev(q_out, dev, o, (n, cfg.Hq * cfg.rep, cfg.D), "q_out") if cfg.Hq else None,
+        _dev(k_out, dev, o, (n, cfg.Hk * cfg.rep, cfg.D), "k_out") if cfg.Hk else None, s), "qk_norm")
 
 
 def qk_norm_backward(cfg, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq=None, dwk=None,
                      workspace=None, stream=None):
-    need = qk_norm_sizes(cfg)
-    t, o, n = TORCH_DTYPES[cfg.dtype], TORCH_DTYPES[cfg.out_dtype], cfg.n_tokens
+    dev, s = _device_and_stream(stream)
+    need = qk_norm_sizes(cfg) if dwq is not None or dwk is not None else 0
+    t, o, n, D = _torch_dtype(cfg.dtype, "qk_norm"), _torch_dtype(cfg.out_dtype, "qk_norm"), cfg.n_tokens, cfg.D
     _check(lib().replayssm_qk_norm_backward(
-        ctypes.byref(cfg), *_qk_inputs(cfg, q, k, wq, wk, positions, inv_freq),
-        _dev(dq_out, o, (n, cfg.Hq * cfg.rep, cfg.D), "dq_out") if cfg.Hq else None,
-        _dev(dk_out, o, (n, cfg.Hk * cfg.rep, cfg.D), "dk_out") if cfg.Hk else None,
-        _dev(dq, t, (n, cfg.Hq, cfg.D), "dq") if cfg.Hq else None,
-        _dev(dk, t, (n, cfg.Hk, cfg.D), "dk") if cfg.Hk else None,
-        _dev(dwq, torch.float32, (cfg.D,), "dwq"), _dev(dwk, torch.float32, (cfg.D,), "dwk"),
-        _workspace(workspace, need if dwq is not None or dwk is not None else 0), _s(stream)), "qk_norm_backward")
+        ctypes.byref(cfg), *_qk_inputs(cfg, dev, q, k, wq, wk, positions, inv_freq),
+        _dev(dq_out, dev, o, (n, cfg.Hq * cfg.rep, D), "dq_out") if cfg.Hq else None,
+        _dev(dk_out, dev, o, (n, cfg.Hk * cfg.rep, D), "dk_out") if cfg.Hk else None,
+        _dev(dq, dev, t, (n, cfg.Hq, D), "dq") if cfg.Hq else None,
+        _dev(dk, dev, t, (n, cfg.Hk, D), "dk") if cfg.Hk else None,
+        _dev(dwq, dev, torch.float32, (D,), "dwq"), _dev(dwk, dev, torch.float32, (D,), "dwk"),
+        _workspace(workspace, dev, need), s), "qk_norm_backward")
 
 
 def make_delta_config(n_seqs, n_tokens, H, Hk, dk, dv, dtype="bf16", scale=1.0, q_stride=None, k_stride=None,
@@ -560,47 +588,47 @@ def delta_sizes(cfg: DeltaConfig):
     return int(f.value), int(b.value)
 
 
-def _delta_inputs(cfg, q, k, v, g, beta):
-    if cfg.dtype not in TORCH_DTYPES:
-        raise ReplaySSMError(EINVAL, "delta", f"dtype {cfg.dtype} unknown")
-    t, n = TORCH_DTYPES[cfg.dtype], cfg.n_tokens
-    return (_rows(q, t, n, cfg.Hk, cfg.dk, cfg.q_stride, "q"), _rows(k, t, n, cfg.Hk, cfg.dk, cfg.k_stride, "k"),
-            _rows(v, t, n, cfg.H, cfg.dv, cfg.v_stride, "v"), _dev(g, torch.float32, (n, cfg.H), "g"),
-            _dev(beta, torch.float32, (n, cfg.H), "beta"))
+def _delta_inputs(cfg, dev, t, q, k, v, g, beta):
+    n, f32 = cfg.n_tokens, torch.float32
+    return (_rows(q, dev, t, (n, cfg.Hk, cfg.dk), cfg.q_stride, "q"),
+            _rows(k, dev, t, (n, cfg.Hk, cfg.dk), cfg.k_stride, "k"),
+            _rows(v, dev, t, (n, cfg.H, cfg.dv), cfg.v_stride, "v"), _dev(g, dev, f32, (n, cfg.H), "g"),
+            _dev(beta, dev, f32, (n, cfg.H), "beta"))
 
 
 def delta_step(cfg, cu_tokens, slots, n_slots, q, k, v, g, beta, S_in, S_out, out, err, stream=None):
-    inputs = _delta_inputs(cfg, q, k, v, g, beta)
+    dev, s = _device_and_stream(stream)
+    t, i32, n = _torch_dtype(cfg.dtype, "delta_step"), torch.int32, cfg.n_seqs
     pool = (n_slots, cfg.H, cfg.dv, cfg.dk)
     _check(lib().replayssm_delta_step(
-        ctypes.byref(cfg), _dev(cu_tokens, torch.int32, (cfg.n_seqs + 1,), "cu_tokens"),
-        _dev(slots, torch.int32, (cfg.n_seqs,), "slots"), int(n_slots), *inputs,
-        _dev(S_in, torch.float32, pool, "S_in"), _dev(S_out, torch.float32, pool, "S_out"),
-        _dev(out, TORCH_DTYPES[cfg.dtype], (cfg.n_tokens, cfg.H, cfg.dv), "out"), _dev(err, torch.int32, None, "err"),
-        _s(stream)), "delta_step")
+        ctypes.byref(cfg), _dev(cu_tokens, dev, i32, (n + 1,), "cu_tokens"), _dev(slots, dev, i32, (n,), "slots"),
+        int(n_slots), *_delta_inputs(cfg, dev, t, q, k, v, g, beta), _dev(S_in, dev, torch.float32, pool, "S_in"),
+        _dev(S_out, dev, torch.float32, pool, "S_out"), _dev(out, dev, t, (cfg.n_tokens, cfg.H, cfg.dv), "out"),
+        _dev(err, dev, i32, None, "err"), s), "delta_step")
 
 
 def delta_prompt(cfg, maps, q, k, v, g, beta, S0, out, S_out, workspace, err, stream=None):
+    dev, s = _device_and_stream(stream)
     need = delta_sizes(cfg)[0]
-    inputs = _delta_inputs(cfg, q, k, v, g, beta)
+    t, f32 = _torch_dtype(cfg.dtype, "delta_prompt"), torch.float32
     states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
     _check(lib().replayssm_delta_prompt(
-        ctypes.byref(cfg), ctypes.byref(maps), *inputs, _dev(S0, torch.float32, states, "S0"),
-        _dev(out, TORCH_DTYPES[cfg.dtype], (cfg.n_tokens, cfg.H, cfg.dv), "out"),
-        _dev(S_out, torch.float32, states, "S_out"), _workspace(workspace, need), _dev(err, torch.int32, None, "err"),
-        _s(stream)), "delta_prompt")
+        ctypes.byref(cfg), ctypes.byref(maps), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
+        _dev(S0, dev, f32, states, "S0"), _dev(out, dev, t, (cfg.n_tokens, cfg.H, cfg.dv), "out"),
+        _dev(S_out, dev, f32, states, "S_out"), _workspace(workspace, dev, need),
+        _dev(err, dev, torch.int32, None, "err"), s), "delta_prompt")
 
 
 def delta_prompt_backward(cfg, maps, q, k, v, g, beta, S0, dout, dS_out, dq, dk, dv, dg, dbeta, dS0, workspace, err,
                           stream=None):
+    dev, s = _device_and_stream(stream)
     need = delta_sizes(cfg)[1]
-    inputs = _delta_inputs(cfg, q, k, v, g, beta)
-    t, n, f32 = TORCH_DTYPES[cfg.dtype], cfg.n_tokens, torch.float32
-    states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
+    t, n, f32 = _torch_dtype(cfg.dtype, "delta_prompt_backward"), cfg.n_tokens, torch.float32
+    states, keys, values = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk), (n, cfg.Hk, cfg.dk), (n, cfg.H, cfg.dv)
     _check(lib().replayssm_delta_prompt_backward(
-        ctypes.byref(cfg), ctypes.byref(maps), *inputs, _dev(S0, f32, states, "S0"),
-        _dev(dout, t, (n, cfg.H, cfg.dv), "dout"), _dev(dS_out, f32, states, "dS_out"),
-        _dev(dq, t, (n, cfg.Hk, cfg.dk), "dq"), _dev(dk, t, (n, cfg.Hk, cfg.dk), "dk"),
-        _dev(dv, t, (n, cfg.H, cfg.dv), "dv"), _dev(dg, f32, (n, cfg.H), "dg"),
-        _dev(dbeta, f32, (n, cfg.H), "dbeta"), _dev(dS0, f32, states, "dS0"), _workspace(workspace, need),
-        _dev(err, torch.int32, None, "err"), _s(stream)), "delta_prompt_backward")
+        ctypes.byref(cfg), ctypes.byref(maps), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
+        _dev(S0, dev, f32, states, "S0"), _dev(dout, dev, t, values, "dout"),
+        _dev(dS_out, dev, f32, states, "dS_out"), _dev(dq, dev, t, keys, "dq"), _dev(dk, dev, t, keys, "dk"),
+        _dev(dv, dev, t, values, "dv"), _dev(dg, dev, f32, (n, cfg.H), "dg"),
+        _dev(dbeta, dev, f32, (n, cfg.H), "dbeta"), _dev(dS0, dev, f32, states, "dS0"),
+        _workspace(workspace, dev, need), _dev(err, dev, torch.int32, None, "err"), s), "delta_prompt_backward")

@@ -573,8 +573,8 @@ struct BackwardSizes {
 template <typename T, int DK, int NT>
 hipError_t launch_reverse(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
   using L = ReverseLayout<T, DK, NT>;
-  auto kernel = delta_reverse_kernel<T, DK, NT>;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::total);
+  constexpr auto kernel = delta_reverse_kernel<T, DK, NT>;
+  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
   const int slices = (a.dv + 64 * NT - 1) / (64 * NT);
   kernel<<<dim3((unsigned)((int64_t)a.n_seqs * a.H * slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
@@ -604,8 +604,8 @@ hipError_t launch_backward(const DeltaArgs& a, hipStream_t s) {
     e = launch_reverse<T, DK, 1>(a, kept, s);
   if (e != hipSuccess) return e;
   using L = GradLds<T, DK>;
-  auto kernel = delta_gradients_kernel<T, DK>;
-  e = allow_lds(reinterpret_cast<const void*>(kernel), L::total);
+  constexpr auto kernel = delta_gradients_kernel<T, DK>;
+  e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)((int64_t)a.max_blocks * a.Hk)), dim3(kChunkThreads), L::total, s>>>(a, kept);
   return hipGetLastError();

@@ -2,6 +2,8 @@
 // inverse T of the block's corrections and the decayed scores P, as matrix operands.
 #pragma once
 
+#include <atomic>
+
 #include "chunk.hpp"
 
 namespace rs {
@@ -212,17 +214,26 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
   }
 }
 
-// Lets `kernel` use `bytes` of dynamic LDS (past 64 KiB it has to be asked for).
-hipError_t allow_lds(const void* kernel, int bytes) {
+// Lets KERNEL use `bytes` of dynamic LDS (past 64 KiB it has to be asked for, once per device).
+template <typename K, K KERNEL>
+hipError_t allow_lds(int bytes) {
   if (bytes <= 64 * 1024) return hipSuccess;
-  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> done{0};  // a bit per device
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <typename T, int DK, typename Out>
 hipError_t launch_prepare(const DeltaArgs& a, hipStream_t s) {
   using L = PrepareLds<T, DK>;
-  auto kernel = delta_prepare_kernel<T, DK, Out>;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::total);
+  constexpr auto kernel = delta_prepare_kernel<T, DK, Out>;
+  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)((int64_t)a.max_blocks * a.H)), dim3(kChunkThreads), L::total, s>>>(a);
   return hipGetLastError();

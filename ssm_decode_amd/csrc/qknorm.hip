@@ -25,9 +25,13 @@ constexpr int kQkRows = 128;    // rows a workgroup aims at, tokens times heads
 constexpr int kQkTokens = 16;   // at most; the angles' LDS is kQkTokens * rot floats
 constexpr int kMaxD = 256;
 constexpr int kQkPartials = 1024;
+constexpr int kQkEnough = 1024;  // workgroups that fill the chip
 
-__host__ __device__ inline int tokens_per_group(int heads) {
-  const int t = kQkRows / heads;
+// Tokens a workgroup takes: as many as make kQkRows rows, fewer where that would leave compute
+// units without a workgroup.
+__host__ __device__ inline int tokens_per_group(int n_tokens, int heads) {
+  int t = kQkRows / heads;
+  if (t > n_tokens / kQkEnough) t = n_tokens / kQkEnough;
   return t < 1 ? 1 : t > kQkTokens ? kQkTokens : t;
 }
 
@@ -111,20 +115,21 @@ template <typename IN, typename OUT, int LPR>
 __global__ void __launch_bounds__(kQkThreads) qk_norm_kernel(const QkNormArgs a) {
   __shared__ __align__(16) float table[kQkTokens * kMaxD];
   const int heads = a.Hq + a.Hk;
-  const int tpg = tokens_per_group(heads);
+  const int tpg = tokens_per_group(a.n_tokens, heads);
+  constexpr int kRowsAtOnce = kQkThreads / LPR;
+  // a token of its own may be shared by gridDim.y workgroups, kRowsAtOnce heads at a time each
   const int t0 = blockIdx.x * tpg;
   const int tokens = a.n_tokens - t0 < tpg ? a.n_tokens - t0 : tpg;
   if (a.rot > 0) {
     fill_angles(a, t0, tokens, table);
     __syncthreads();
   }
-  constexpr int kRowsAtOnce = kQkThreads / LPR;
   const int sub = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const int c = sub * 8;
   const bool in = c < a.D;
   const f32x8 wq = weights(a.wq, c, in), wk = weights(a.wk, c, in);
   const int rows = tokens * heads;
-  for (int base = 0; base < rows; base += kRowsAtOnce) {
+  for (int base = blockIdx.y * kRowsAtOnce; base < rows; base += kRowsAtOnce * gridDim.y) {
     const int row = base + group;
     const bool live = row < rows;
     const int t = live ? row / heads : 0, h = live ? row - t * heads : 0;
@@ -154,7 +159,7 @@ template <typename IN, typename OUT, int LPR>
 __global__ void __launch_bounds__(kQkThreads) qk_norm_backward_kernel(const QkNormArgs a) {
   __shared__ __align__(16) float table[kQkTokens * kMaxD];
   const int heads = a.Hq + a.Hk;
-  const int tpg = tokens_per_group(heads);
+  const int tpg = tokens_per_group(a.n_tokens, heads);
   constexpr int kRowsAtOnce = kQkThreads / LPR;
   const int sub = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const int c = sub * 8;
@@ -232,7 +237,15 @@ __global__ void __launch_bounds__(256) qk_weights_kernel(const float* partial, i
   const int which = blockIdx.y;
   const int ch = blockIdx.x * 16 + (threadIdx.x & 15), lane = threadIdx.x >> 4;
   float s = 0.f;
-  for (int r = lane; r < rows; r += 16) s += partial[((int64_t)r * 2 + which) * D + ch];
+  int r = lane;
+  for (; r + 7 * 16 < rows; r += 8 * 16) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = partial[((int64_t)(r + i * 16) * 2 + which) * D + ch];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += x[i];
+  }
+  for (; r < rows; r += 16) s += partial[((int64_t)r * 2 + which) * D + ch];
   part[lane][threadIdx.x & 15] = s;
   __syncthreads();
   if (lane == 0) {
@@ -245,10 +258,16 @@ __global__ void __launch_bounds__(256) qk_weights_kernel(const float* partial, i
 
 template <typename IN, typename OUT, int LPR>
 hipError_t launch_lpr(const QkNormArgs& a, bool backward, hipStream_t s) {
-  const int tpg = tokens_per_group(a.Hq + a.Hk);
+  const int heads = a.Hq + a.Hk;
+  const int tpg = tokens_per_group(a.n_tokens, heads);
   const int groups = (a.n_tokens + tpg - 1) / tpg;
   if (!backward) {
-    qk_norm_kernel<IN, OUT, LPR><<<dim3(groups), dim3(kQkThreads), 0, s>>>(a);
+    int split = 1;
+    if (tpg == 1 && groups < kQkEnough) {
+      const int passes = (heads + kQkThreads / LPR - 1) / (kQkThreads / LPR);
+      split = kQkEnough / groups < passes ? kQkEnough / groups : passes;
+    }
+    qk_norm_kernel<IN, OUT, LPR><<<dim3(groups, split), dim3(kQkThreads), 0, s>>>(a);
     return hipGetLastError();
   }
   const int grid = qk_norm_partials(a.n_tokens, a.Hq, a.Hk, a.D);
@@ -289,7 +308,7 @@ hipError_t launch_in(const QkNormArgs& a, bool backward, hipStream_t s) {
 }  // namespace
 
 int qk_norm_partials(int n_tokens, int Hq, int Hk, int D) {
-  const int tpg = tokens_per_group(Hq + Hk);
+  const int tpg = tokens_per_group(n_tokens, Hq + Hk);
   const int groups = (n_tokens + tpg - 1) / tpg;
   return groups < kQkPartials ? groups : kQkPartials;
 }

@@ -323,8 +323,8 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 hipError_t launch_scan_tiles(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
   using L = ScanLayout<T, DK, NT, Ops, KEEP>;
-  auto kernel = delta_scan_kernel<T, DK, NT, Ops, KEEP>;
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), L::total);
+  constexpr auto kernel = delta_scan_kernel<T, DK, NT, Ops, KEEP>;
+  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
   const int slices = (a.dv + 64 * NT - 1) / (64 * NT);
   kernel<<<dim3((unsigned)((int64_t)a.n_seqs * a.H * slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
