@@ -44,13 +44,22 @@ struct Split {
 
 template <int N>
 __device__ __forceinline__ Split<N> split8(const f32x8& x) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   Split<N> s;
-  s.p[0] = __builtin_convertvector(x, bf16x8);
   f32x8 rest = x;
 #pragma unroll
-  for (int i = 1; i < N; ++i) {
-    rest -= __builtin_convertvector(s.p[i - 1], f32x8);
-    s.p[i] = __builtin_convertvector(rest, bf16x8);
+  for (int i = 0; i < N; ++i) {
+    u32x4 packed;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // pair by pair, so that one conversion serves the part and the remainder
+      const bf16x2 pair = __builtin_convertvector((f32x2{rest[2 * e], rest[2 * e + 1]}), bf16x2);
+      packed[e] = __builtin_bit_cast(uint32_t, pair);
+      rest[2 * e] -= bf16_lo(packed[e]);
+      rest[2 * e + 1] -= bf16_hi(packed[e]);
+    }
+    s.p[i] = __builtin_bit_cast(bf16x8, packed);
   }
   return s;
 }
@@ -59,7 +68,9 @@ __device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) {
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// The kept products of parts, smallest first: f(i, j) for part i of A and part j of B.
+// How many products of parts are kept, and the products, smallest first: f(i, j) for part i of A and part j of B.
+template <int NA, int NB>
+constexpr int kProducts = NA * NB - (NA < NB ? NA * (NA - 1) / 2 : NB * (NB - 1) / 2);
 template <int NA, int NB, typename F>
 __device__ __forceinline__ void products(const F& f) {
   constexpr int kOrder = NA > NB ? NA : NB;
@@ -93,6 +104,7 @@ struct Raw8<__bf16> {
   bf16x8 x;
   __device__ __forceinline__ void load(const __bf16* p) { x = *reinterpret_cast<const bf16x8*>(p); }
   __device__ __forceinline__ void zero() { x = bf16x8{}; }
+  __device__ __forceinline__ f32x8 f32() const { return __builtin_convertvector(x, f32x8); }
   __device__ __forceinline__ Split<1> split() const {
     Split<1> s;
     s.p[0] = x;
@@ -104,6 +116,7 @@ struct Raw8<_Float16> {
   f16x8 x;
   __device__ __forceinline__ void load(const _Float16* p) { x = *reinterpret_cast<const f16x8*>(p); }
   __device__ __forceinline__ void zero() { x = f16x8{}; }
+  __device__ __forceinline__ f32x8 f32() const { return __builtin_convertvector(x, f32x8); }
   __device__ __forceinline__ Split<2> split() const { return split8<2>(__builtin_convertvector(x, f32x8)); }
 };
 template <>
@@ -111,17 +124,21 @@ struct Raw8<float> {
   f32x8 x;
   __device__ __forceinline__ void load(const float* p) { x = load8(p); }
   __device__ __forceinline__ void zero() { x = f32x8{}; }
+  __device__ __forceinline__ f32x8 f32() const { return __builtin_convertvector(x, f32x8); }
   __device__ __forceinline__ Split<3> split() const { return split8<3>(x); }
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-// ROWS rows of W columns in N bf16 planes in LDS (W a multiple of 32). The 16-byte chunks of a
-// row are exchanged by an exclusive-or with a key of the row, so that the eight lanes an LDS
-// cycle serves hit distinct banks when they read one chunk column of eight dealt rows, and the
-// transposing reads (four rows by four chunks per 16 lanes) meet at most in pairs, the least
-// their half-chunk reads allow.
+// ROWS rows of W columns in N bf16 planes in LDS (W a multiple of 32). LDS serves 256 bytes a cycle
+// (16 lanes of 16-byte reads) when those lanes' 16-byte slots differ modulo 256 bytes. The chunks of a
+// row are exchanged by an exclusive-or with a key of the row such that they do for 16 dealt rows and for 16
+// consecutive rows read at one chunk column (every one of row bits 0, 1, 3 and 2 or 4 reaches the slot), and
+// for the four rows by four chunks that 16 lanes of a transposing read take (bits 0 and 1 reach the
+// slot above the chunks' two). Measured, four wavefronts reading 1 KiB each: 16 cycles for rows, 32 for
+// transposing reads, whose 8 bytes per lane are served at half the rate; a key that leaves pairs of rows on
+// a slot doubles both.
 template <int W, int N, int ROWS = kBlock>
 struct Tile {
   static constexpr int kRowBytes = W * 2;
@@ -132,7 +149,11 @@ struct Tile {
   __device__ __forceinline__ explicit Tile(char* b) : base(b) {}
 
   __device__ __forceinline__ static int key(int row) {
-    return (((row & 1) << 2) | (row & 2) | ((row >> 3) & 1)) & (kChunks - 1);
+    const int q0 = (row >> 3) & 1, q1 = ((row >> 2) ^ (row >> 4)) & 1;
+    const int low = q1 | ((q0 ^ q1) << 1);
+    if (W >= 128) return low | ((row & 3) << 2);
+    if (W == 64) return low | ((row & 2) << 1);  // bit 0 is the slot's bit 3 already
+    return low;
   }
   __device__ __forceinline__ static int at(int row, int chunk) { return row * kRowBytes + ((chunk ^ key(row)) << 4); }
 
@@ -248,9 +269,11 @@ struct ColumnTile {
     *reinterpret_cast<bf16x8*>(tile.base + tile.at(row, chunk)) = bf16x8{};
   }
   template <bool DEALT>
-  __device__ __forceinline__ f32x8 read(int t, int p, int lane) const {
+  __device__ __forceinline__ Raw8<T> read(int t, int p, int lane) const {
     typedef T vec __attribute__((ext_vector_type(8)));
-    return __builtin_convertvector(__builtin_bit_cast(vec, tile.template col8<DEALT>(t, p, lane).p[0]), f32x8);
+    Raw8<T> r;
+    r.x = __builtin_bit_cast(vec, tile.template col8<DEALT>(t, p, lane).p[0]);
+    return r;
   }
 };
 template <int W>
@@ -266,13 +289,13 @@ struct ColumnTile<float, W> {
       store8(base + (s.row + i * s.kRowStep) * kLdRow + s.chunk * 8, s.x[i].x);
   }
   template <bool DEALT>
-  __device__ __forceinline__ f32x8 read(int t, int p, int lane) const {
+  __device__ __forceinline__ Raw8<float> read(int t, int p, int lane) const {
     const int n = lane & 15, g = lane >> 4;
     const float* c = base + (32 * p + 8 * g) * kLdRow + (DEALT ? dealt(t, n) : 16 * t + n);
-    f32x8 x;
+    Raw8<float> r;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c[e * kLdRow];
-    return x;
+    for (int e = 0; e < 8; ++e) r.x[e] = c[e * kLdRow];
+    return r;
   }
 };
 

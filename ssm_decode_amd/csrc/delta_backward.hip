@@ -37,7 +37,8 @@ template <typename T, int DK, int NT>
 using ReverseLayout = FeedLayout<T, DK, 64 * NT, (int)BackwardBlock<Parts<T>::mid>::reverse_bytes, true>;
 
 template <typename T, int DK, int NT>
-__global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const DeltaArgs a, const Kept kept) {
+__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 2 : 1)
+    delta_reverse_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + kCols - 1) / kCols;
   const int slice = blockIdx.x % slices, item = blockIdx.x / slices;
-  const int s = item / a.H, h = item - s * a.H;
+  const int h = item % a.H, s = by_length(a, item / a.H);
   const SeqRange seq = seq_range(a, s);
   if (!seq.ok) return;  // (flagged by the scan)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -77,18 +78,20 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
   src.columns = a.dv - v0 < kCols ? a.dv - v0 : kCols;
   src.begin = seq.begin;
   src.end = seq.end;
-  Feed<T, DK, kCols, (int)Ops::reverse_bytes, true, L::kAsync> feed(src, lds);
+  src.n_tokens = a.n_tokens;
+  using F = Feed<T, DK, kCols, (int)Ops::reverse_bytes, true, L::kAsync>;
+  F feed(src, lds);
   if (seq.blocks > 0) {
+    feed.start(seq.blocks - 1);
 #pragma unroll
-    for (int part = 0; part < 4; ++part) feed.request(part, seq.blocks - 1);
+    for (int u = 0; u < F::kUnits; ++u) feed.unit(u);
   }
   for (int c = seq.blocks - 1; c >= 0; --c) {
     feed.arrive(c);
-    const bool more = c > 0;
+    feed.start(c - 1);
     if (idle) {
 #pragma unroll
-      for (int part = 0; part < 4; ++part)
-        if (more) feed.request(part, c - 1);
+      for (int u = 0; u < F::kUnits; ++u) feed.unit(u);
       continue;
     }
     const auto K = feed.K();
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int t = 0; t < 4; ++t) y[nt][t] = w[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    f32x8 d[NT][2];
+    Raw8<T> d[NT][2];  // (before the next block is asked for, as in the scan)
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -118,21 +121,25 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
 #pragma unroll
         for (int t = 0; t < 4; ++t) kf[ks & 1][t] = K.row8(dealt(t, n), ks, g);
       };
+      constexpr int kSlots = kSteps * kProducts<in, mid> * 4;
+      int slot = 0;
       request(0);
-      if (more) feed.request(0, c - 1);
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
         if (ks + 1 < kSteps) request(ks + 1);
-        if (ks == kSteps / 2 && more) feed.request(1, c - 1);
         __builtin_amdgcn_sched_barrier(0);
         Split<mid> bs[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) bs[nt] = dS.template operand<mid>(nt, ks);
         products<in, mid>([&](int i, int j) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 4; ++t) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
+#pragma unroll
+            for (int u = slot * F::kUnits / kSlots; u < (slot + 1) * F::kUnits / kSlots; ++u) feed.unit(u);
+            ++slot;
+          }
         });
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -142,15 +149,11 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
       Split<mid> pf[kFrags];
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(pt, i, lane);
-      if (more) feed.request(2, c - 1);
-#pragma unroll
-      for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(tt, i, lane);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const Split<in> bd = split8<in>(d[nt][p]);  // exact
+          const Split<in> bd = d[nt][p].split();  // exact
           products<mid, in>([&](int i, int j) {
 #pragma unroll
             for (int t = 0; t <= 2 * p + 1; ++t) w[nt][t] = mfma(pf[upper_frag(t, p)].p[i], bd.p[j], w[nt][t]);
@@ -166,6 +169,8 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
     }
     f32x8 x[NT][2];
     {
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(tt, i, lane);
       f32x4 dX[NT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -192,12 +197,12 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
         const f32x8 first = scal8(sc.first, p), rate = -first * scal8(sc.beta, p);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          bd[nt][p] = split8<mid>(d[nt][p] * first * a.scale);
+          bd[nt][p] = split8<mid>(d[nt][p].f32() * first * a.scale);
           bx[nt][p] = split8<mid>(rate * x[nt][p]);
         }
       }
       const float whole = sc.first[kBlock - 1];
-      constexpr int kGroup = in == 3 ? 1 : 2;
+      constexpr int kGroup = in == 1 ? 2 : 1;
       Split<in> qc[2][kGroup][2], kc[2][kGroup][2];
       const auto request = [&](int group) {
 #pragma unroll
@@ -209,7 +214,6 @@ __global__ void __launch_bounds__(kChunkThreads) delta_reverse_kernel(const Delt
           }
       };
       request(0);
-      if (more) feed.request(3, c - 1);
 #pragma unroll
       for (int group = 0; group < kTiles / kGroup; ++group) {
         if (group + 1 < kTiles / kGroup) request(group + 1);

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = 32 * sj + 8 * g + 4 * p + r;
-          acc[p][r] = j <= i ? acc[p][r] * expf((float)(G[i] - G[j])) : 0.f;
+          acc[p][r] = j <= i ? a.scale * acc[p][r] * expf((float)(G[i] - G[j])) : 0.f;
         }
       put_frag<mid>(out + Out::p, lower_frag(wave, sj), lane, split8<mid>(join(acc[0], acc[1])));
     }
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
   invert(A, Tm);
   for (int sj = 0; sj <= wave / 2; ++sj) {
     const float* row = Tm + dealt(wave, n) * kLd + 32 * sj + 8 * g;
-    put_frag<mid>(out + Out::t, lower_frag(wave, sj), lane, split8<mid>(join(ld4(row), ld4(row + 4))));
+    put_frag<mid>(out + Out::t, lower_frag(wave, sj), lane, split8<mid>(load8(row) * load8(beta + 32 * sj + 8 * g)));
   }
   if constexpr (Out::backward) {  // T^T as the left operand of T^T dU
     for (int si = wave / 2; si < 2; ++si) {

@@ -62,6 +62,21 @@ struct StateTiles {
   }
 };
 
+// The place-th longest sequence. Workgroups start in index order, and a long sequence that starts last is
+// finished last; with over 64 sequences the heads of many are in flight and short ones fill the gaps,
+// so those keep their order.
+__device__ __forceinline__ int by_length(const DeltaArgs& a, int place) {
+  if (a.n_seqs > 64) return place;
+  const int lane = threadIdx.x & 63;
+  const int len = lane < a.n_seqs ? a.cu_blocks[lane + 1] - a.cu_blocks[lane] : INT32_MIN;
+  int rank = 0;
+  for (int i = 0; i < a.n_seqs; ++i) {
+    const int other = __builtin_amdgcn_readlane(len, i);
+    rank += other > len || (other == len && i < lane);
+  }
+  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.n_seqs && rank == place));
+}
+
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 using ScanLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::scan_bytes, !KEEP>;
 
@@ -71,7 +86,8 @@ using ScanLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::scan_bytes, !KEEP>;
 // Outputs are computed transposed (state rows by tokens): the operands of a product can change places,
 // and a lane then holds 4 NT neighbouring state rows of one token, which it stores in one piece.
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
-__global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaArgs a, const Kept kept) {
+__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 2 : 1)
+    delta_scan_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
@@ -80,7 +96,8 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + kCols - 1) / kCols;
   const int slice = blockIdx.x % slices, item = blockIdx.x / slices;
-  const int s = item / a.H, h = item - s * a.H;
+  const int place_in_order = item / a.H, h = item - place_in_order * a.H;
+  const int s = by_length(a, place_in_order);
   const SeqRange seq = seq_range(a, s);
   if (!seq.ok) {
     if (threadIdx.x == 0 && slice == 0 && h == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
@@ -118,18 +135,20 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
   src.columns = a.dv - v0 < kCols ? a.dv - v0 : kCols;
   src.begin = seq.begin;
   src.end = seq.end;
-  Feed<T, DK, kCols, (int)Ops::scan_bytes, !KEEP, L::kAsync> feed(src, lds);
+  src.n_tokens = a.n_tokens;
+  using F = Feed<T, DK, kCols, (int)Ops::scan_bytes, !KEEP, L::kAsync>;
+  F feed(src, lds);
   if (seq.blocks > 0) {
+    feed.start(0);
 #pragma unroll
-    for (int part = 0; part < 4; ++part) feed.request(part, 0);
+    for (int u = 0; u < F::kUnits; ++u) feed.unit(u);
   }
   for (int c = 0; c < seq.blocks; ++c) {
     feed.arrive(c);
-    const bool more = c + 1 < seq.blocks;
+    feed.start(c + 1 < seq.blocks ? c + 1 : -1);
     if (idle) {
 #pragma unroll
-      for (int part = 0; part < 4; ++part)
-        if (more) feed.request(part, c + 1);
+      for (int u = 0; u < F::kUnits; ++u) feed.unit(u);
       continue;
     }
     const int rows = feed.rows(c);
@@ -142,7 +161,9 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
     const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
     if constexpr (KEEP) S.store(kept.S + place * a.dv * DK, col, live, g);
 
-    f32x8 v[NT][2];
+    // The compiler lets a transposing read wait for every copy into LDS that is under way, so the next
+    // block is asked for between this one's two groups of them: v's here and the state's at the end.
+    Raw8<T> v[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -164,51 +185,46 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
           if constexpr (!KEEP) qf[ks & 1][t] = Q.row8(dealt(t, n), ks, g);
         }
       };
+      constexpr int kSlots = kSteps * kProducts<in, mid> * 4;
+      int slot = 0;
       request(0);
-      // the next block is asked for in parts between the steps: asked for at once, it would hold up
-      // the wavefront until the memory pipeline has taken it all
-      if (more) feed.request(0, c + 1);
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
         if (ks + 1 < kSteps) request(ks + 1);
-        if (ks == kSteps / 2 && more) feed.request(1, c + 1);
         __builtin_amdgcn_sched_barrier(0);
         Split<mid> bs[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) bs[nt] = S.template operand<mid>(nt, ks);
         products<in, mid>([&](int i, int j) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 4; ++t) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
               if constexpr (!KEEP) o[nt][t] = mfma(bs[nt].p[j], qf[ks & 1][t].p[i], o[nt][t]);
             }
+            // a share of the next block's pieces
+#pragma unroll
+            for (int u = slot * F::kUnits / kSlots; u < (slot + 1) * F::kUnits / kSlots; ++u) feed.unit(u);
+            ++slot;
+          }
         });
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     const auto scal8 = [&](const float* p, int h) { return load8(p + 32 * h + 8 * g); };
     f32x8 u[NT][2];
-    Split<mid> pf[kFrags];
-    float first_t[4];
     {
+      // (beta is in T's columns)
       Split<mid> bx[NT][2], tf[kFrags];
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(ops + Ops::t, i, lane);
-      const f32x8 first[2] = {scal8(sc.first, 0), scal8(sc.first, 1)}, beta[2] = {scal8(sc.beta, 0), scal8(sc.beta, 1)};
-      if (more) feed.request(2, c + 1);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < 2; ++p) {
+        const f32x8 first = scal8(sc.first, p);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          bx[nt][p] = split8<mid>(beta[p] * (v[nt][p] - first[p] * join(y[nt][2 * p], y[nt][2 * p + 1])));
-      if constexpr (!KEEP) {
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(ops + Ops::p, i, lane);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) first_t[t] = sc.first[dealt(t, n)];
+          bx[nt][p] = split8<mid>(v[nt][p].f32() - first * join(y[nt][2 * p], y[nt][2 * p + 1]));
       }
       __builtin_amdgcn_sched_barrier(0);
       f32x4 U[NT][4];
@@ -229,34 +245,24 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
 #pragma unroll
         for (int p = 0; p < 2; ++p) u[nt][p] = join(U[nt][2 * p], U[nt][2 * p + 1]);
     }
-    // The state's operands come through LDS transposed, a group of tiles ahead of their products.
-    constexpr int kGroup = in == 1 ? 4 : 2;
-    static_assert(kTiles % 2 == 0, "groups are whole");
-    constexpr int kTileGroup = kTiles < kGroup ? kTiles : kGroup;
-    Split<in> kc[2][kTileGroup][2];
-    const auto request_state = [&](int group) {
-#pragma unroll
-      for (int i = 0; i < kTileGroup; ++i)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) kc[group & 1][i][p] = K.template col8<true>(group * kTileGroup + i, p, lane);
-    };
-    request_state(0);
-    const f32x8 last[2] = {scal8(sc.last, 0), scal8(sc.last, 1)};
-    const float whole = sc.first[kBlock - 1];
-    if (more) feed.request(3, c + 1);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (KEEP) {
       store_cols<NT>(kept.U + place * kBlock * a.dv + col[0], a.dv, g, live, u);
-    } else {  // outputs
-      Split<mid> bu[NT][2];
+    } else {  // outputs (scale is in P)
+      Split<mid> bu[NT][2], pf[kFrags];
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(ops + Ops::p, i, lane);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int p = 0; p < 2; ++p) bu[nt][p] = split8<mid>(u[nt][p]);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t) {
+        const float first = a.scale * sc.first[dealt(t, n)];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[nt][t] *= first_t[t];
+        for (int nt = 0; nt < NT; ++nt) o[nt][t] *= first;
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
         products<mid, mid>([&](int i, int j) {
@@ -265,13 +271,43 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[nt][t] = mfma(bu[nt][p].p[i], pf[lower_frag(t, p)].p[j], o[nt][t]);
         });
+      const auto put = [&](int t) {
+        T* dst = op + (t0 + dealt(t, n)) * out_stride;
+        if constexpr (NT == 2) {
+          store8(dst, join(o[0][t], o[1][t]));
+        } else {
+          typedef T vec __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<vec*>(dst) = __builtin_convertvector(o[0][t], vec);
+        }
+      };
+      if (out_col < a.dv) {
+        if (rows == kBlock) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) put(t);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (dealt(t, n) < rows) put(t);
+        }
+      }
     }
+    // The state's operands come through LDS transposed, a group of tiles ahead of their products.
+    constexpr int kTileGroup = 2;
+    Split<in> kc[2][kTileGroup][2];
+    const auto request_state = [&](int group) {
+#pragma unroll
+      for (int i = 0; i < kTileGroup; ++i)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) kc[group & 1][i][p] = K.template col8<true>(group * kTileGroup + i, p, lane);
+    };
+    request_state(0);
+    const float whole = sc.first[kBlock - 1];
     {  // state
       Split<mid> bl[NT][2];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) bl[nt][p] = split8<mid>(last[p] * u[nt][p]);
+        for (int nt = 0; nt < NT; ++nt) bl[nt][p] = split8<mid>(scal8(sc.last, p) * u[nt][p]);
 #pragma unroll
       for (int group = 0; group < kTiles / kTileGroup; ++group) {
         if (group + 1 < kTiles / kTileGroup) request_state(group + 1);
@@ -292,27 +328,6 @@ __global__ void __launch_bounds__(kChunkThreads) delta_scan_kernel(const DeltaAr
               }
           });
         __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    if constexpr (!KEEP) {
-      const auto put = [&](int t) {
-        T* dst = op + (t0 + dealt(t, n)) * out_stride;
-        if constexpr (NT == 2) {
-          store8(dst, join(o[0][t], o[1][t]) * a.scale);
-        } else {
-          typedef T vec __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<vec*>(dst) = __builtin_convertvector(o[0][t] * a.scale, vec);
-        }
-      };
-      if (out_col < a.dv) {
-        if (rows == kBlock) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) put(t);
-        } else {
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (dealt(t, n) < rows) put(t);
-        }
       }
     }
   }
