@@ -37,7 +37,7 @@ template <typename T, int DK, int NT>
 using ReverseLayout = FeedLayout<T, DK, 64 * NT, (int)BackwardBlock<Parts<T>::mid>::reverse_bytes, true>;
 
 template <typename T, int DK, int NT>
-__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kChunkThreads)
     delta_reverse_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;

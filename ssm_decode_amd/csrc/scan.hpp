@@ -86,7 +86,7 @@ using ScanLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::scan_bytes, !KEEP>;
 // Outputs are computed transposed (state rows by tokens): the operands of a product can change places,
 // and a lane then holds 4 NT neighbouring state rows of one token, which it stores in one piece.
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
-__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kChunkThreads)
     delta_scan_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
@@ -161,13 +161,27 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 
     const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
     if constexpr (KEEP) S.store(kept.S + place * a.dv * DK, col, live, g);
 
-    // The compiler lets a transposing read wait for every copy into LDS that is under way, so the next
-    // block is asked for between this one's two groups of them: v's here and the state's at the end.
+    // The compiler lets a transposing read wait for every copy into LDS that is under way. Where the next
+    // block comes that way, this one's are all done before it is asked for: v's here, and the state
+    // update's operands (64 registers) during the first half of the next loop.
     Raw8<T> v[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int p = 0; p < 2; ++p) v[nt][p] = V.template read<kDealt>(NT * wave + nt, p, lane);
+    constexpr bool kHold = L::kAsync;
+    constexpr int kHoldSteps = kSteps > 1 ? kSteps / 2 : 1;
+    constexpr int kTileGroup = kHold ? kTiles : 2;
+    Split<in> kc[kHold ? 1 : 2][kTileGroup][2];
+    // The next block's pieces, an equal share at each of the places that call this.
+    constexpr int kFirstPiece = kSteps > 1 ? kSteps / 2 : 0;
+    constexpr int kSlots = (kSteps - kFirstPiece) * kProducts<in, mid> * 4 + 6 * kProducts<mid, mid> * (KEEP ? 1 : 2);
+    int slot = 0;
+    const auto piece = [&]() {
+#pragma unroll
+      for (int u = slot * F::kUnits / kSlots; u < (slot + 1) * F::kUnits / kSlots; ++u) feed.unit(u);
+      ++slot;
+    };
     f32x4 y[NT][4], o[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -185,12 +199,16 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 
           if constexpr (!KEEP) qf[ks & 1][t] = Q.row8(dealt(t, n), ks, g);
         }
       };
-      constexpr int kSlots = kSteps * kProducts<in, mid> * 4;
-      int slot = 0;
       request(0);
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks) {
         if (ks + 1 < kSteps) request(ks + 1);
+        if (kHold && ks < kHoldSteps) {
+#pragma unroll
+          for (int i = ks * kTiles / kHoldSteps; i < (ks + 1) * kTiles / kHoldSteps; ++i)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) kc[0][i][p] = K.template col8<true>(i, p, lane);
+        }
         __builtin_amdgcn_sched_barrier(0);
         Split<mid> bs[NT];
 #pragma unroll
@@ -203,10 +221,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 
               y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
               if constexpr (!KEEP) o[nt][t] = mfma(bs[nt].p[j], qf[ks & 1][t].p[i], o[nt][t]);
             }
-            // a share of the next block's pieces
-#pragma unroll
-            for (int u = slot * F::kUnits / kSlots; u < (slot + 1) * F::kUnits / kSlots; ++u) feed.unit(u);
-            ++slot;
+            if (ks >= kFirstPiece) piece();
           }
         });
         __builtin_amdgcn_sched_barrier(0);
@@ -236,9 +251,11 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 
       for (int p = 0; p < 2; ++p)
         products<mid, mid>([&](int i, int j) {
 #pragma unroll
-          for (int t = 2 * p; t < 4; ++t)
+          for (int t = 2 * p; t < 4; ++t) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) U[nt][t] = mfma(tf[lower_frag(t, p)].p[i], bx[nt][p].p[j], U[nt][t]);
+            piece();
+          }
         });
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -267,9 +284,11 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 
       for (int p = 0; p < 2; ++p)
         products<mid, mid>([&](int i, int j) {
 #pragma unroll
-          for (int t = 2 * p; t < 4; ++t)
+          for (int t = 2 * p; t < 4; ++t) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[nt][t] = mfma(bu[nt][p].p[i], pf[lower_frag(t, p)].p[j], o[nt][t]);
+            piece();
+          }
         });
       const auto put = [&](int t) {
         T* dst = op + (t0 + dealt(t, n)) * out_stride;
@@ -291,16 +310,14 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 && NT == 1 ? 
         }
       }
     }
-    // The state's operands come through LDS transposed, a group of tiles ahead of their products.
-    constexpr int kTileGroup = 2;
-    Split<in> kc[2][kTileGroup][2];
+    // Without the copies the state's operands come a group of tiles ahead of their products.
     const auto request_state = [&](int group) {
 #pragma unroll
       for (int i = 0; i < kTileGroup; ++i)
 #pragma unroll
         for (int p = 0; p < 2; ++p) kc[group & 1][i][p] = K.template col8<true>(group * kTileGroup + i, p, lane);
     };
-    request_state(0);
+    if (!kHold) request_state(0);
     const float whole = sc.first[kBlock - 1];
     {  // state
       Split<mid> bl[NT][2];
