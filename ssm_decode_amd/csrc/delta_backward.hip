@@ -34,213 +34,236 @@ struct BackwardBlock {
 };
 
 template <typename T, int DK, int NT>
-using ReverseLayout = FeedLayout<T, DK, 64 * NT, (int)BackwardBlock<Parts<T>::mid>::reverse_bytes, true>;
+struct ReverseLds {
+  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid, kSteps = kWide<DK> / 32;
+  // dS; dO; e^G d; dU; -e^G beta dX
+  static constexpr int s = 0, d = s + NT * kSteps * kStepBytes<mid>, df = d + NT * 2 * kStepBytes<in>,
+                       u = df + NT * 2 * kStepBytes<mid>, x = u + NT * 2 * kStepBytes<mid>,
+                       k = x + NT * 2 * kStepBytes<mid>, q = k + 4 * Tile<32, in>::kBytes,
+                       total = q + 4 * Tile<32, in>::kBytes;
+};
 
+// The scan's division of labour, from the last block to the first.
 template <typename T, int DK, int NT>
-__global__ void __launch_bounds__(kChunkThreads)
+__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_reverse_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
-  constexpr int kCols = 64 * NT;
-  using L = ReverseLayout<T, DK, NT>;
+  constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;
+  using L = ReverseLds<T, DK, NT>;
   using Ops = BackwardBlock<mid>;
   extern __shared__ __align__(16) char lds[];
-  const int slices = (a.dv + kCols - 1) / kCols;
-  const int slice = blockIdx.x % slices, item = blockIdx.x / slices;
+  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
+  int item, slice;
+  item_slice(slices, &item, &slice);
+  if (item >= a.n_seqs * a.H) return;
   const int h = item % a.H, s = by_length(a, item / a.H);
   const SeqRange seq = seq_range(a, s);
   if (!seq.ok) return;  // (flagged by the scan)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int hk = h / (a.H / a.Hk);
-  const int v0 = slice * kCols;
   int col[NT];
   bool live[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    col[nt] = v0 + 16 * NT * wave + 16 * nt + n;
+    col[nt] = 16 * NT * slice + 16 * nt + n;
     live[nt] = col[nt] < a.dv;
   }
-  const bool idle = v0 + 16 * NT * wave >= a.dv;
   const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
-  StateTiles<DK, NT> dS;
-  dS.load(a.dS_out == nullptr ? nullptr : a.dS_out + state, col, live, g);
-
-  FeedSource<T> src;
-  src.k = static_cast<const T*>(a.k) + (int64_t)hk * DK;
-  src.q = static_cast<const T*>(a.q) + (int64_t)hk * DK;
-  src.v = static_cast<const T*>(a.dout) + (int64_t)h * a.dv + v0;
-  src.ops = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes + Ops::scalars;
-  src.k_stride = a.k_stride;
-  src.q_stride = a.q_stride;
-  src.v_stride = (int64_t)a.H * a.dv;
-  src.ops_step = (int64_t)a.H * Ops::bytes;
-  src.columns = a.dv - v0 < kCols ? a.dv - v0 : kCols;
-  src.begin = seq.begin;
-  src.end = seq.end;
-  src.n_tokens = a.n_tokens;
-  using F = Feed<T, DK, kCols, (int)Ops::reverse_bytes, true, L::kAsync>;
-  F feed(src, lds);
-  if (seq.blocks > 0) {
-    feed.start(seq.blocks - 1);
+  const int tile0 = wave * kOwn;
+  const bool owner = tile0 < kTiles;
+  const auto channel = [&](int tl) { return 32 * (tl >> 1) + 8 * g + 4 * (tl & 1); };
+  const auto s_frags = [&](int nt) { return lds + L::s + nt * kSteps * kStepBytes<mid>; };
+  f32x4 dS[NT][kOwn];  // transposed, as S in the scan
 #pragma unroll
-    for (int u = 0; u < F::kUnits; ++u) feed.unit(u);
-  }
-  for (int c = seq.blocks - 1; c >= 0; --c) {
-    feed.arrive(c);
-    feed.start(c - 1);
-    if (idle) {
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int u = 0; u < F::kUnits; ++u) feed.unit(u);
-      continue;
+    for (int i = 0; i < kOwn; ++i) {
+      dS[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int c = channel(tile0 + i);
+      if (owner && a.dS_out != nullptr && live[nt] && c < DK)
+        dS[nt][i] = ld4(a.dS_out + state + (int64_t)col[nt] * DK + c);
+      if (owner) put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
     }
-    const auto K = feed.K();
-    const auto Q = feed.Q();
-    const auto D = feed.V();
-    const char* ops = feed.ops();
-    const BlockScalars& sc = *reinterpret_cast<const BlockScalars*>(ops);
-    const char* tt = ops + (Ops::tt - Ops::scalars);
-    const char* pt = ops + (Ops::pt - Ops::scalars);
-    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    dS.store(kept.dS + place * a.dv * DK, col, live, g);
 
-    const auto scal8 = [&](const float* p, int h) { return load8(p + 32 * h + 8 * g); };
-    f32x4 y[NT][4], w[NT][4];
+  const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
+  const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
+  const int64_t do_stride = (int64_t)a.H * a.dv;
+  const T* dop = static_cast<const T*>(a.dout) + (int64_t)h * a.dv;
+  const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
+  const int64_t ws_step = (int64_t)a.H * Ops::bytes;
+  const int ks_own = owner ? tile0 >> 1 : 0;
+  RowOperand<T, DK> K(wave);
+  ColumnStage<T, DK> Kc(a.k_stride, ks_own), Qc(a.q_stride, ks_own);
+  using Columns = typename ColumnStage<T, DK>::Columns;
+  const Columns Kt(lds + L::k + wave * Columns::kBytes), Qt(lds + L::q + wave * Columns::kBytes);
+  Split<mid> tf[2], pf[2];
+  T d[NT][4];
+  f32x4 first4, last4, beta4;
+  float whole;
+  const int row4 = dealt(wave, 4 * g);
+  const auto token = [&](int c) { return (int64_t)seq.begin + (int64_t)c * kBlock; };
+  const auto rows_of = [&](int c) {
+    const int64_t left = seq.end - token(c);
+    return left < kBlock ? (int)left : kBlock;
+  };
+  const auto ask_values = [&](int c) {
+    const int rows = rows_of(c);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int r = 0; r < 4; ++r) {
+      const T* p = dop + (token(c) + (row4 + r < rows ? row4 + r : rows - 1)) * do_stride;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) y[nt][t] = w[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Raw8<T> d[NT][2];  // (before the next block is asked for, as in the scan)
+      for (int nt = 0; nt < NT; ++nt) d[nt][r] = p[live[nt] ? col[nt] : 0];
+    }
+    const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
+    first4 = ld4(sc->first + row4);
+    last4 = ld4(sc->last + row4);
+    beta4 = ld4(sc->beta + row4);
+    whole = sc->first[kBlock - 1];
+  };
+  const auto ask_columns = [&](int c) {
+    Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
+    Qc.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
+  };
+  const auto ask_p = [&](int c) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
+      pf[p] = get_frag<mid>(ws + c * ws_step + Ops::pt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
+  };
+  const auto ask_t = [&](int c) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) d[nt][p] = D.template read<false>(NT * wave + nt, p, lane);
-    {  // (operands are requested a step ahead, as in the scan)
-      Split<in> kf[2][4];
-      const auto request = [&](int ks) {
+    for (int p = 0; p < 2; ++p)
+      tf[p] = get_frag<mid>(ws + c * ws_step + Ops::tt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
+  };
+  const auto d_frags = [&](int nt) { return lds + L::d + nt * 2 * kStepBytes<in>; };
+  // dO of the block that was asked for, as an operand
+  const auto put_values = [&](int c) {
+    const int rows = rows_of(c);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) kf[ks & 1][t] = K.row8(dealt(t, n), ks, g);
-      };
-      constexpr int kSlots = kSteps * kProducts<in, mid> * 4;
-      int slot = 0;
-      request(0);
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 x;
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {
-        if (ks + 1 < kSteps) request(ks + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        Split<mid> bs[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) bs[nt] = dS.template operand<mid>(nt, ks);
-        products<in, mid>([&](int i, int j) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
-#pragma unroll
-            for (int u = slot * F::kUnits / kSlots; u < (slot + 1) * F::kUnits / kSlots; ++u) feed.unit(u);
-            ++slot;
-          }
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      for (int r = 0; r < 4; ++r) x[r] = row4 + r < rows && live[nt] ? (float)d[nt][r] : 0.f;
+      put_half<in>(d_frags(nt), wave >> 1, wave & 1, lane, x);  // exact
     }
-    Split<mid> bu[NT][2], tf[kFrags];
-    {
-      Split<mid> pf[kFrags];
+  };
+  if (seq.blocks > 0) {
+    const int c = seq.blocks - 1;
+    ask_values(c);
+    K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
+    ask_p(c);
+    ask_t(c);
+    ask_columns(c);
+    put_values(c);
+  }
+  for (int c = seq.blocks - 1; c >= 0; --c) {
+    const int rows = rows_of(c);
+    const int next = c > 0 ? c - 1 : 0;  // (loads under no condition, as in the scan)
+    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
+    const f32x4 first_b = first4, beta_b = beta4;
+    const float whole_b = whole;
+    __syncthreads();  // dS and dO are there
+    f32x4 y[NT], w[NT];
 #pragma unroll
-      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(pt, i, lane);
+    for (int nt = 0; nt < NT; ++nt) {
+      y[nt] = w[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      Split<mid> bs[kSteps];
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) bs[ks] = get_frag<mid>(s_frags(nt), ks, lane);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
+        if (p >= wave / 2) w[nt] = mma(pf[p], get_frag<in>(d_frags(nt), p, lane), w[nt]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Split<in> bd = d[nt][p].split();  // exact
-          products<mid, in>([&](int i, int j) {
-#pragma unroll
-            for (int t = 0; t <= 2 * p + 1; ++t) w[nt][t] = mfma(pf[upper_frag(t, p)].p[i], bd.p[j], w[nt][t]);
-          });
-        }
+      for (int ks = 0; ks < kSteps; ++ks) y[nt] = mma(K.get(ks), bs[ks], y[nt]);
     }
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const f32x8 last = scal8(sc.last, p);
+    for (int nt = 0; nt < NT; ++nt) {
+      put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4 * y[nt] + a.scale * w[nt]);
+      f32x4 x;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        bu[nt][p] = split8<mid>(last * join(y[nt][2 * p], y[nt][2 * p + 1]) + a.scale * join(w[nt][2 * p], w[nt][2 * p + 1]));
+      for (int r = 0; r < 4; ++r)
+        x[r] = row4 + r < rows && live[nt] ? a.scale * first_b[r] * (float)d[nt][r] : 0.f;
+      put_half<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);
     }
-    f32x8 x[NT][2];
-    {
-#pragma unroll
-      for (int i = 0; i < kFrags; ++i) tf[i] = get_frag<mid>(tt, i, lane);
-      f32x4 dX[NT][4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) dX[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        products<mid, mid>([&](int i, int j) {
-#pragma unroll
-          for (int t = 0; t <= 2 * p + 1; ++t)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) dX[nt][t] = mfma(tf[upper_frag(t, p)].p[i], bu[nt][p].p[j], dX[nt][t]);
-        });
+    if (owner) {
+      Kc.store(Kt, rows);
+      Qc.store(Qt, rows);
+    }
+    ask_values(next);
+    K.load(kp + token(next) * a.k_stride, a.k_stride, rows_of(next));
+    ask_p(next);
+    // the gradient of the state after the block
+    if (owner) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) x[nt][p] = join(dX[nt][2 * p], dX[nt][2 * p + 1]);
+        for (int i = 0; i < kOwn; ++i)
+          if (live[nt] && channel(tile0 + i) < DK)
+            st4(kept.dS + (place * a.dv + col[nt]) * DK + channel(tile0 + i), dS[nt][i]);
     }
-    store_cols<NT>(kept.dX + place * kBlock * a.dv + col[0], a.dv, g, live, x);
-    {
-      Split<mid> bd[NT][2], bx[NT][2];
+    __syncthreads();  // dU and e^G d are there
+    f32x4 dX[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      dX[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (p >= wave / 2) dX[nt] = mma(tf[p], get_frag<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, p, lane), dX[nt]);
+      put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, -first_b * beta_b * dX[nt]);
+    }
+    ask_t(next);
+    ask_columns(next);
+    // (Q's part of the update fills the time of the exchange)
+    Split<in> kc[kOwn][2];
+    if (owner) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) dS[nt][i] *= whole_b;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const f32x8 first = scal8(sc.first, p), rate = -first * scal8(sc.beta, p);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          bd[nt][p] = split8<mid>(d[nt][p].f32() * first * a.scale);
-          bx[nt][p] = split8<mid>(rate * x[nt][p]);
+        for (int i = 0; i < kOwn; ++i) {
+          const Split<in> qc = Qt.template col8<true>((tile0 + i) & 1, p, lane);
+          kc[i][p] = Kt.template col8<true>((tile0 + i) & 1, p, lane);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            dS[nt][i] = mma(qc, get_frag<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, p, lane), dS[nt][i]);
         }
       }
-      const float whole = sc.first[kBlock - 1];
-      constexpr int kGroup = in == 1 ? 2 : 1;
-      Split<in> qc[2][kGroup][2], kc[2][kGroup][2];
-      const auto request = [&](int group) {
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            qc[group & 1][i][p] = Q.template col8<true>(group * kGroup + i, p, lane);
-            kc[group & 1][i][p] = K.template col8<true>(group * kGroup + i, p, lane);
-          }
-      };
-      request(0);
-#pragma unroll
-      for (int group = 0; group < kTiles / kGroup; ++group) {
-        if (group + 1 < kTiles / kGroup) request(group + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) dS.x[nt][group * kGroup + i] *= whole;
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          products<in, mid>([&](int x, int y) {
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-#pragma unroll
-              for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  f32x4& acc = dS.x[nt][group * kGroup + i];
-                  acc = z == 0 ? mfma(qc[group & 1][i][p].p[x], bd[nt][p].p[y], acc)
-                               : mfma(kc[group & 1][i][p].p[x], bx[nt][p].p[y], acc);
-                }
-          });
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (live[nt]) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) kept.dX[(place * kBlock + row4 + r) * a.dv + col[nt]] = dX[nt][r];
+      }
+    __syncthreads();  // dX is there
+    if (owner) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const Split<mid> bx = get_frag<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, p, lane);
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) dS[nt][i] = mma(kc[i][p], bx, dS[nt][i]);
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+          put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
+    }
+    put_values(next);
   }
-  if (a.dS0 != nullptr) dS.store(a.dS0 + state, col, live, g);
+  if (a.dS0 == nullptr || !owner) return;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (live[nt] && channel(tile0 + i) < DK)
+        st4(a.dS0 + state + (int64_t)col[nt] * DK + channel(tile0 + i), dS[nt][i]);
 }
 
 // The gradients kernel walks the state rows in slices of 32 (one MFMA step over dv), then needs
@@ -611,12 +634,12 @@ struct BackwardSizes {
 
 template <typename T, int DK, int NT>
 hipError_t launch_reverse(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ReverseLayout<T, DK, NT>;
+  using L = ReverseLds<T, DK, NT>;
   constexpr auto kernel = delta_reverse_kernel<T, DK, NT>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
-  const int slices = (a.dv + 64 * NT - 1) / (64 * NT);
-  kernel<<<dim3((unsigned)((int64_t)a.n_seqs * a.H * slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
+  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
+  kernel<<<dim3((unsigned)item_grid((int64_t)a.n_seqs * a.H, slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
   return hipGetLastError();
 }
 
@@ -635,12 +658,9 @@ hipError_t launch_backward(const DeltaArgs& a, hipStream_t s) {
   e = launch_scan<T, DK, BackwardBlock<mid>, true>(a, kept, s);
   if (e != hipSuccess) return e;
   bool two = false;
-  e = wide_tiles<T>(a, &two);
+  e = wide_tiles(a, &two);
   if (e != hipSuccess) return e;
-  if constexpr (sizeof(T) == 2)
-    e = two ? launch_reverse<T, DK, 2>(a, kept, s) : launch_reverse<T, DK, 1>(a, kept, s);
-  else
-    e = launch_reverse<T, DK, 1>(a, kept, s);
+  e = two ? launch_reverse<T, DK, 2>(a, kept, s) : launch_reverse<T, DK, 1>(a, kept, s);
   if (e != hipSuccess) return e;
   using L = GradLds<T, DK>;
   constexpr auto kernel = delta_gradients_kernel<T, DK>;
