@@ -100,15 +100,15 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const Columns Kt(lds + L::k + wave * Columns::kBytes), Qt(lds + L::q + wave * Columns::kBytes);
   Split<mid> tf[2], pf[2];
   T d[NT][4];
-  f32x4 first4, last4, beta4;
-  float whole;
+  f32x4 first4[2], last4[2], beta4[2];  // two sets, as in the scan
+  float whole[2];
   const int row4 = dealt(wave, 4 * g);
   const auto token = [&](int c) { return (int64_t)seq.begin + (int64_t)c * kBlock; };
   const auto rows_of = [&](int c) {
     const int64_t left = seq.end - token(c);
     return left < kBlock ? (int)left : kBlock;
   };
-  const auto ask_values = [&](int c) {
+  const auto ask_values = [&](int c, int set) {
     const int rows = rows_of(c);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       for (int nt = 0; nt < NT; ++nt) d[nt][r] = p[live[nt] ? col[nt] : 0];
     }
     const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
-    first4 = ld4(sc->first + row4);
-    last4 = ld4(sc->last + row4);
-    beta4 = ld4(sc->beta + row4);
-    whole = sc->first[kBlock - 1];
+    first4[set] = ld4(sc->first + row4);
+    last4[set] = ld4(sc->last + row4);
+    beta4[set] = ld4(sc->beta + row4);
+    whole[set] = sc->first[kBlock - 1];
   };
   const auto ask_columns = [&](int c) {
     Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
@@ -150,19 +150,17 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   };
   if (seq.blocks > 0) {
     const int c = seq.blocks - 1;
-    ask_values(c);
+    ask_values(c, 0);
     K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
     ask_p(c);
     ask_t(c);
     ask_columns(c);
     put_values(c);
   }
-  for (int c = seq.blocks - 1; c >= 0; --c) {
+  const auto block = [&](int c, int set) {
     const int rows = rows_of(c);
     const int next = c > 0 ? c - 1 : 0;  // (loads under no condition, as in the scan)
     const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    const f32x4 first_b = first4, beta_b = beta4;
-    const float whole_b = whole;
     __syncthreads();  // dS and dO are there
     f32x4 y[NT], w[NT];
 #pragma unroll
@@ -179,18 +177,18 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4 * y[nt] + a.scale * w[nt]);
+      put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * y[nt] + a.scale * w[nt]);
       f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        x[r] = row4 + r < rows && live[nt] ? a.scale * first_b[r] * (float)d[nt][r] : 0.f;
+        x[r] = row4 + r < rows && live[nt] ? a.scale * first4[set][r] * (float)d[nt][r] : 0.f;
       put_half<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);
     }
     if (owner) {
       Kc.store(Kt, rows);
       Qc.store(Qt, rows);
     }
-    ask_values(next);
+    ask_values(next, set ^ 1);
     K.load(kp + token(next) * a.k_stride, a.k_stride, rows_of(next));
     ask_p(next);
     // the gradient of the state after the block
@@ -210,7 +208,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
         if (p >= wave / 2) dX[nt] = mma(tf[p], get_frag<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, p, lane), dX[nt]);
-      put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, -first_b * beta_b * dX[nt]);
+      put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, -first4[set] * beta4[set] * dX[nt]);
     }
     ask_t(next);
     ask_columns(next);
@@ -220,7 +218,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) dS[nt][i] *= whole_b;
+        for (int i = 0; i < kOwn; ++i) dS[nt][i] *= whole[set];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
 #pragma unroll
@@ -256,6 +254,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
           put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
     }
     put_values(next);
+  };
+  for (int c = seq.blocks - 1; c >= 0; c -= 2) {
+    block(c, 0);
+    if (c > 0) block(c - 1, 1);
   }
   if (a.dS0 == nullptr || !owner) return;
 #pragma unroll

@@ -201,8 +201,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const typename ColumnStage<T, DK>::Columns Kt(lds + L::k + wave * Tile<32, in>::kBytes);
   Split<mid> tf[2], pf[2];
   T v[NT][4];
-  f32x4 first4, last4;  // of the lane's four tokens (rows of a result tile)
-  float first1, whole;  // of token dealt(wave, n), and of the block
+  // A block's scalars: of the lane's four tokens (rows of a result tile), of token dealt(wave, n), and of the block.
+  // Two sets, of even and odd blocks: one is still in use when the next is asked for.
+  f32x4 first4[2], last4[2];
+  float first1[2], whole[2];
   const int row4 = dealt(wave, 4 * g);
   const auto token = [&](int c) { return (int64_t)seq.begin + (int64_t)c * kBlock; };
   const auto rows_of = [&](int c) {
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const auto ask_columns = [&](int c) {
     Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
   };
-  const auto ask_values = [&](int c) {
+  const auto ask_values = [&](int c, int set) {
     const int rows = rows_of(c);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -225,10 +227,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       for (int nt = 0; nt < NT; ++nt) v[nt][r] = p[live[nt] ? col[nt] : 0];
     }
     const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
-    first4 = ld4(sc->first + row4);
-    last4 = ld4(sc->last + row4);
-    first1 = sc->first[dealt(wave, n)];
-    whole = sc->first[kBlock - 1];
+    first4[set] = ld4(sc->first + row4);
+    last4[set] = ld4(sc->last + row4);
+    first1[set] = sc->first[dealt(wave, n)];
+    whole[set] = sc->first[kBlock - 1];
   };
   const auto ask_t = [&](int c) {
 #pragma unroll
@@ -244,12 +246,12 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   };
   if (seq.blocks > 0) {
     ask_rows(0);
-    ask_values(0);
+    ask_values(0, 0);
     ask_t(0);
     ask_columns(0);
     ask_p(0);
   }
-  for (int c = 0; c < seq.blocks; ++c) {
+  const auto block = [&](int c, int set) {
     const int rows = rows_of(c);
     const int64_t t0 = token(c);
     // (The last block asks for itself again. Loads under a condition would join their registers with the old ones
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       for (int nt = 0; nt < NT; ++nt) {
         f32x4 x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = (row4 + r < rows && live[nt] ? (float)v[nt][r] : 0.f) - first4[r] * y[nt][r];
+        for (int r = 0; r < 4; ++r) x[r] = (row4 + r < rows && live[nt] ? (float)v[nt][r] : 0.f) - first4[set][r] * y[nt][r];
         put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);  // (beta is in T's columns)
       }
       if constexpr (!KEEP) {
@@ -291,10 +293,8 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       }
     }
     if (owner) Kc.store(Kt, rows);
-    const float first_t = first1, whole_b = whole;
-    const f32x4 last_b = last4;
     ask_rows(next);
-    ask_values(next);
+    ask_values(next, set ^ 1);
     __syncthreads();  // X is there
     f32x4 U[NT];
 #pragma unroll
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      put_half<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last_b * U[nt]);
+      put_half<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * U[nt]);
       if constexpr (!KEEP) put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, U[nt]);
     }
     // the update's left operands, transposed
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) S[nt][i] *= whole_b;
+        for (int i = 0; i < kOwn; ++i) S[nt][i] *= whole[set];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     }
     if constexpr (!KEEP) {  // (scale is in P)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) o[nt] *= a.scale * first_t;
+      for (int nt = 0; nt < NT; ++nt) o[nt] *= a.scale * first1[set];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
         if (p <= wave / 2) {
@@ -376,6 +376,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       }
       ask_p(next);
     }
+  };
+  for (int c = 0; c < seq.blocks; c += 2) {
+    block(c, 0);
+    if (c + 1 < seq.blocks) block(c + 1, 1);
   }
   if (a.S_out == nullptr || KEEP || !owner) return;
 #pragma unroll
