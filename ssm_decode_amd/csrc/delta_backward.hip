@@ -18,7 +18,7 @@
 //   gradients everything else                             (one workgroup per block and value head)
 //   share     dq and dk summed over the value heads of a key head, where they share
 // The kept states and corrections are fp32: dg and dbeta are differences of large sums.
-#include "scan.hpp"
+#include "walk.hpp"
 
 namespace rs {
 
@@ -32,241 +32,6 @@ struct BackwardBlock {
   static constexpr int64_t scan_bytes = tt;                   // what the forward scan reads, from the start
   static constexpr int64_t reverse_bytes = bytes - scalars;   // and the reverse scan, from the scalars
 };
-
-template <typename T, int DK, int NT>
-struct ReverseLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid, kSteps = kWide<DK> / 32;
-  // dS; dO; e^G d; dU; -e^G beta dX
-  static constexpr int s = 0, d = s + NT * kSteps * kStepBytes<mid>, df = d + NT * 2 * kStepBytes<in>,
-                       u = df + NT * 2 * kStepBytes<mid>, x = u + NT * 2 * kStepBytes<mid>,
-                       k = x + NT * 2 * kStepBytes<mid>, q = k + 4 * Tile<32, in>::kBytes,
-                       total = q + 4 * Tile<32, in>::kBytes;
-};
-
-// The scan's division of labour, from the last block to the first.
-template <typename T, int DK, int NT>
-__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
-    delta_reverse_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
-  constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
-  constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;
-  using L = ReverseLds<T, DK, NT>;
-  using Ops = BackwardBlock<mid>;
-  extern __shared__ __align__(16) char lds[];
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
-  int item, slice;
-  item_slice(slices, &item, &slice);
-  if (item >= a.n_seqs * a.H) return;
-  const int h = item % a.H, s = by_length(a, item / a.H);
-  const SeqRange seq = seq_range(a, s);
-  if (!seq.ok) return;  // (flagged by the scan)
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
-  const int hk = h / (a.H / a.Hk);
-  int col[NT];
-  bool live[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    col[nt] = 16 * NT * slice + 16 * nt + n;
-    live[nt] = col[nt] < a.dv;
-  }
-  const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
-  const int tile0 = wave * kOwn;
-  const bool owner = tile0 < kTiles;
-  const auto channel = [&](int tl) { return 32 * (tl >> 1) + 8 * g + 4 * (tl & 1); };
-  const auto s_frags = [&](int nt) { return lds + L::s + nt * kSteps * kStepBytes<mid>; };
-  f32x4 dS[NT][kOwn];  // transposed, as S in the scan
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      dS[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int c = channel(tile0 + i);
-      if (owner && a.dS_out != nullptr && live[nt] && c < DK)
-        dS[nt][i] = ld4(a.dS_out + state + (int64_t)col[nt] * DK + c);
-      if (owner) put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
-    }
-
-  const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
-  const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
-  const int64_t do_stride = (int64_t)a.H * a.dv;
-  const T* dop = static_cast<const T*>(a.dout) + (int64_t)h * a.dv;
-  const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
-  const int64_t ws_step = (int64_t)a.H * Ops::bytes;
-  const int ks_own = owner ? tile0 >> 1 : 0;
-  RowOperand<T, DK> K(wave);
-  ColumnStage<T, DK> Kc(a.k_stride, ks_own), Qc(a.q_stride, ks_own);
-  using Columns = typename ColumnStage<T, DK>::Columns;
-  const Columns Kt(lds + L::k + wave * Columns::kBytes), Qt(lds + L::q + wave * Columns::kBytes);
-  Split<mid> tf[2], pf[2];
-  T d[NT][4];
-  f32x4 first4[2], last4[2], beta4[2];  // two sets, as in the scan
-  float whole[2];
-  const int row4 = dealt(wave, 4 * g);
-  const auto token = [&](int c) { return (int64_t)seq.begin + (int64_t)c * kBlock; };
-  const auto rows_of = [&](int c) {
-    const int64_t left = seq.end - token(c);
-    return left < kBlock ? (int)left : kBlock;
-  };
-  const auto ask_values = [&](int c, int set) {
-    const int rows = rows_of(c);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const T* p = dop + (token(c) + (row4 + r < rows ? row4 + r : rows - 1)) * do_stride;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) d[nt][r] = p[live[nt] ? col[nt] : 0];
-    }
-    const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
-    first4[set] = ld4(sc->first + row4);
-    last4[set] = ld4(sc->last + row4);
-    beta4[set] = ld4(sc->beta + row4);
-    whole[set] = sc->first[kBlock - 1];
-  };
-  const auto ask_columns = [&](int c) {
-    Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
-    Qc.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
-  };
-  const auto ask_p = [&](int c) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      pf[p] = get_frag<mid>(ws + c * ws_step + Ops::pt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
-  };
-  const auto ask_t = [&](int c) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      tf[p] = get_frag<mid>(ws + c * ws_step + Ops::tt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
-  };
-  const auto d_frags = [&](int nt) { return lds + L::d + nt * 2 * kStepBytes<in>; };
-  // dO of the block that was asked for, as an operand
-  const auto put_values = [&](int c) {
-    const int rows = rows_of(c);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      f32x4 x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = row4 + r < rows && live[nt] ? (float)d[nt][r] : 0.f;
-      put_half<in>(d_frags(nt), wave >> 1, wave & 1, lane, x);  // exact
-    }
-  };
-  if (seq.blocks > 0) {
-    const int c = seq.blocks - 1;
-    ask_values(c, 0);
-    K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
-    ask_p(c);
-    ask_t(c);
-    ask_columns(c);
-    put_values(c);
-  }
-  const auto block = [&](int c, int set) {
-    const int rows = rows_of(c);
-    const int next = c > 0 ? c - 1 : 0;  // (loads under no condition, as in the scan)
-    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    __syncthreads();  // dS and dO are there
-    f32x4 y[NT], w[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      y[nt] = w[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      Split<mid> bs[kSteps];
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) bs[ks] = get_frag<mid>(s_frags(nt), ks, lane);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (p >= wave / 2) w[nt] = mma(pf[p], get_frag<in>(d_frags(nt), p, lane), w[nt]);
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) y[nt] = mma(K.get(ks), bs[ks], y[nt]);
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * y[nt] + a.scale * w[nt]);
-      f32x4 x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        x[r] = row4 + r < rows && live[nt] ? a.scale * first4[set][r] * (float)d[nt][r] : 0.f;
-      put_half<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);
-    }
-    if (owner) {
-      Kc.store(Kt, rows);
-      Qc.store(Qt, rows);
-    }
-    ask_values(next, set ^ 1);
-    K.load(kp + token(next) * a.k_stride, a.k_stride, rows_of(next));
-    ask_p(next);
-    // the gradient of the state after the block
-    if (owner) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-          if (live[nt] && channel(tile0 + i) < DK)
-            st4(kept.dS + (place * a.dv + col[nt]) * DK + channel(tile0 + i), dS[nt][i]);
-    }
-    __syncthreads();  // dU and e^G d are there
-    f32x4 dX[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      dX[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (p >= wave / 2) dX[nt] = mma(tf[p], get_frag<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, p, lane), dX[nt]);
-      put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, -first4[set] * beta4[set] * dX[nt]);
-    }
-    ask_t(next);
-    ask_columns(next);
-    // (Q's part of the update fills the time of the exchange)
-    Split<in> kc[kOwn][2];
-    if (owner) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) dS[nt][i] *= whole[set];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const Split<in> qc = Qt.template col8<true>((tile0 + i) & 1, p, lane);
-          kc[i][p] = Kt.template col8<true>((tile0 + i) & 1, p, lane);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            dS[nt][i] = mma(qc, get_frag<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, p, lane), dS[nt][i]);
-        }
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (live[nt]) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) kept.dX[(place * kBlock + row4 + r) * a.dv + col[nt]] = dX[nt][r];
-      }
-    __syncthreads();  // dX is there
-    if (owner) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Split<mid> bx = get_frag<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, p, lane);
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) dS[nt][i] = mma(kc[i][p], bx, dS[nt][i]);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-          put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
-    }
-    put_values(next);
-  };
-  for (int c = seq.blocks - 1; c >= 0; c -= 2) {
-    block(c, 0);
-    if (c > 0) block(c - 1, 1);
-  }
-  if (a.dS0 == nullptr || !owner) return;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (live[nt] && channel(tile0 + i) < DK)
-        st4(a.dS0 + state + (int64_t)col[nt] * DK + channel(tile0 + i), dS[nt][i]);
-}
 
 // The gradients kernel walks the state rows in slices of 32 (one MFMA step over dv), then needs
 // q, k and the two 64 x 64 matrices Y and M: the two sets share their LDS, and two workgroups a compute unit.
@@ -634,17 +399,6 @@ struct BackwardSizes {
   int64_t total() const { return ops + 2 * state + 2 * cols + 2 * part; }
 };
 
-template <typename T, int DK, int NT>
-hipError_t launch_reverse(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ReverseLds<T, DK, NT>;
-  constexpr auto kernel = delta_reverse_kernel<T, DK, NT>;
-  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
-  if (e != hipSuccess) return e;
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
-  kernel<<<dim3((unsigned)item_grid((int64_t)a.n_seqs * a.H, slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
-  return hipGetLastError();
-}
-
 template <typename T, int DK>
 hipError_t launch_backward(const DeltaArgs& a, hipStream_t s) {
   constexpr int mid = Parts<T>::mid;
@@ -659,10 +413,7 @@ hipError_t launch_backward(const DeltaArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   e = launch_scan<T, DK, BackwardBlock<mid>, true>(a, kept, s);
   if (e != hipSuccess) return e;
-  bool two = false;
-  e = wide_tiles(a, &two);
-  if (e != hipSuccess) return e;
-  e = two ? launch_reverse<T, DK, 2>(a, kept, s) : launch_reverse<T, DK, 1>(a, kept, s);
+  e = launch_reverse<T, DK, BackwardBlock<mid>>(a, kept, s);
   if (e != hipSuccess) return e;
   using L = GradLds<T, DK>;
   constexpr auto kernel = delta_gradients_kernel<T, DK>;

@@ -10,11 +10,10 @@
 //   prepare  (one workgroup per block and value head): T and P as matrix operands, and the
 //            block's decays. G is summed in fp64: differences of long sums of g stay exact enough, and
 //            a gate that is closed (g = -infinity, kept as -1e4) leaves later differences whole.
-//   scan     (one workgroup per sequence, value head and slice of state rows): walks the
-//            sequence's blocks. State rows are independent, so each wavefront keeps 16 or 32
-//            of them (transposed, as MFMA accumulators) and runs K S, T X, Q S, P U and
-//            the update from registers; only K, Q, T and P pass through LDS.
-#include "scan.hpp"
+//   scan     (workgroups per sequence, value head and slice of state rows): walks the
+//            sequence's blocks. State rows are independent; they and every product with them are
+//            kept transposed, so that a product's result is the next one's operand as it is.
+#include "walk.hpp"
 
 namespace rs {
 

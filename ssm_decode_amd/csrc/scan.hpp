@@ -1,19 +1,4 @@
-// The serial walk over a sequence's blocks, shared by the forward pass and the backward pass's
-// recomputation of states.
-//
-// A workgroup takes 16 NT state rows of one value head (rows are independent) and its four wavefronts
-// divide every product of a block by rows of the left operand: wavefront w has the block's 16 dealt
-// tokens w for K S, T X, Q S and P U, and a quarter of the channels for the update. What a wavefront
-// reads from memory - its rows of K and Q, its fragments of T and P, its columns of K - is read by no
-// other wavefront of the workgroup, comes straight into registers, and is asked for again right after its last
-// use, a block ahead; only K's columns pass through LDS, to be transposed, in a tile of the wavefront's
-// own. The right operands (S, X, U) are exchanged through LDS in operand layout, 16 bytes per lane, with three
-// barriers per block.
-//
-// The serial chain of a block is then 8 + 3..6 + 8 matrix instructions (dk = 128) and four exchanges, which is
-// what bounds a long sequence: 2.0 us per block of 64 tokens less than a workgroup whose wavefronts each take whole
-// rows of state through all products (3.1 us for 16 rows per wavefront, whose operands all pass through LDS four
-// times).
+// What both ways to walk over a sequence's blocks share.
 #pragma once
 
 #include "prepare.hpp"
@@ -46,376 +31,24 @@ __device__ __forceinline__ int by_length(const DeltaArgs& a, int place) {
   return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.n_seqs && rank == place));
 }
 
-// Workgroup index -> item (sequence and head) and slice of its rows. Workgroups go to the eight dies in turn; the
-// slices of one item read the same K, Q, T and P, so they are placed on one die, behind one L2.
-__device__ __forceinline__ void item_slice(int slices, int* item, int* slice) {
-  const int per = 8 * slices, round = blockIdx.x / per, in_round = blockIdx.x - round * per;
-  *slice = in_round / 8;
-  *item = round * 8 + (in_round & 7);
-}
-__host__ __device__ constexpr int64_t item_grid(int64_t items, int slices) { return (items + 7) / 8 * 8 * slices; }
+// Which way, and with how many state rows per workgroup: 64 or 128 by rows, 16 or 32 split.
+enum class Walk { kRows64, kRows128, kSplit16, kSplit32 };
 
-// Right operands in LDS: [step][part][lane] of 16 bytes; a result tile of a pair fills its half of each lane's.
-template <int N>
-__device__ __forceinline__ void put_half(char* base, int step, int half, int lane, const f32x4& x) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  f32x4 rest = x;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    u32x2 packed;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const bf16x2 pair = __builtin_convertvector((f32x2{rest[2 * e], rest[2 * e + 1]}), bf16x2);
-      packed[e] = __builtin_bit_cast(uint32_t, pair);
-      rest[2 * e] -= bf16_lo(packed[e]);
-      rest[2 * e + 1] -= bf16_hi(packed[e]);
-    }
-    *reinterpret_cast<u32x2*>(base + ((step * N + i) * 64 + lane) * 16 + half * 8) = packed;
-  }
-}
-template <int N>
-constexpr int kStepBytes = N * 1024;  // of one step's right operand
-
-// A wavefront's columns 32 ks .. 32 ks + 31 of a block's 64 rows: loads (16 rows of 64 bytes of a 16-bit type per
-// instruction), then stores into its own tile, from which they are read transposed.
-template <typename T, int DK>
-struct ColumnStage {
-  static constexpr int kPer = 4;
-  using Columns = Tile<32, Parts<T>::in>;
-  Raw8<T> x[kPer];
-  int64_t offset;
-  int row, chunk;
-  bool in;
-  __device__ __forceinline__ ColumnStage(int64_t stride, int ks) {
-    const int lane = threadIdx.x & 63;
-    row = lane >> 2;
-    chunk = lane & 3;
-    in = 32 * ks + chunk * 8 < DK;
-    offset = row * stride + (in ? 32 * ks + chunk * 8 : 0);
-  }
-  // p: the block's first row; n rows of the block exist (others read the last one, and are zeroed on the way)
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int n) {
-    const int64_t edge = (int64_t)(n - 1 - row) * stride;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i].load(p + offset + (row + 16 * i < n ? 16 * i * stride : edge));
-  }
-  __device__ __forceinline__ void store(const Columns& t, int n) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (!in || row + 16 * i >= n) x[i].zero();
-      t.put(row + 16 * i, chunk, x[i].split());
-    }
-  }
-};
-
-// A wavefront's 16 dealt rows of a block as left operands, straight from memory.
-template <typename T, int DK>
-struct RowOperand {
-  static constexpr int kSteps = kWide<DK> / 32;
-  Raw8<T> x[kSteps];
-  int row, g;
-  bool there;  // whether the row exists in the block that was asked for
-  __device__ __forceinline__ RowOperand(int tile) : row(dealt(tile, threadIdx.x & 15)), g((threadIdx.x & 63) >> 4) {}
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int n) {
-    there = row < n;
-    const T* q = p + (int64_t)(there ? row : n - 1) * stride;
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) x[ks].load(q + (32 * ks + 8 * g < DK ? 32 * ks + 8 * g : 0));
-  }
-  __device__ __forceinline__ Split<Parts<T>::in> get(int ks) {
-    if (!there || 32 * ks + 8 * g >= DK) x[ks].zero();
-    return x[ks].split();
-  }
-};
-
-template <typename T, int DK, int NT>
-struct ScanLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid, kSteps = kWide<DK> / 32;
-  static constexpr int s = 0, x = s + NT * kSteps * kStepBytes<mid>, u = x + NT * 2 * kStepBytes<mid>,
-                       ul = u + NT * 2 * kStepBytes<mid>, k = ul + NT * 2 * kStepBytes<mid>,
-                       total = k + 4 * Tile<32, in>::kBytes;
-};
-
-// With KEEP (the backward pass) it writes the state before each block and the block's corrections in place of
-// outputs. Outputs are computed transposed (state rows by tokens): the operands of a product can change places, and
-// a lane then holds 4 NT neighbouring state rows of one token, which it stores in one piece.
-template <typename T, int DK, int NT, typename Ops, bool KEEP>
-__global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
-    delta_scan_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
-  constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
-  constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;  // state tiles of a wavefront
-  constexpr bool kDealt = NT == 2 && !KEEP;           // a lane's output rows of both tiles are neighbours
-  using L = ScanLds<T, DK, NT>;
-  extern __shared__ __align__(16) char lds[];
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
-  int item, slice;
-  item_slice(slices, &item, &slice);
-  if (item >= a.n_seqs * a.H) return;
-  const int h = item % a.H, s = by_length(a, item / a.H);
-  const SeqRange seq = seq_range(a, s);
-  if (!seq.ok) {
-    if (threadIdx.x == 0 && slice == 0 && h == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
-    return;
-  }
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
-  const int hk = h / (a.H / a.Hk);
-  int col[NT];  // of the head's dv, per tile
-  bool live[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    col[nt] = 16 * NT * slice + (kDealt ? dealt(nt, n) : 16 * nt + n);
-    live[nt] = col[nt] < a.dv;
-  }
-  const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
-  const int tile0 = wave * kOwn;  // the wavefront's state tiles; with dk <= 32 two wavefronts have none
-  const bool owner = tile0 < kTiles;
-
-  // S^T: a tile's rows are channels, dealt; its columns state rows
-  const auto channel = [&](int tl) { return 32 * (tl >> 1) + 8 * g + 4 * (tl & 1); };
-  f32x4 S[NT][kOwn];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      S[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int c = channel(tile0 + i);
-      if (owner && a.S0 != nullptr && live[nt] && c < DK) S[nt][i] = ld4(a.S0 + state + (int64_t)col[nt] * DK + c);
-      if (owner) put_half<mid>(lds + L::s + nt * kSteps * kStepBytes<mid>, (tile0 + i) >> 1, (tile0 + i) & 1, lane, S[nt][i]);
-    }
-
-  const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
-  const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
-  const T* vp = static_cast<const T*>(a.v) + (int64_t)h * a.dv;
-  const int64_t out_stride = (int64_t)a.H * a.dv;
-  const int out_col = 16 * NT * slice + 4 * NT * g;  // the first of the lane's neighbouring output rows
-  T* op = static_cast<T*>(a.out) + (int64_t)h * a.dv + out_col;
-  const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
-  const int64_t ws_step = (int64_t)a.H * Ops::bytes;
-
-  RowOperand<T, DK> K(wave), Q(wave);
-  ColumnStage<T, DK> Kc(a.k_stride, owner ? tile0 >> 1 : 0);
-  const typename ColumnStage<T, DK>::Columns Kt(lds + L::k + wave * Tile<32, in>::kBytes);
-  Split<mid> tf[2], pf[2];
-  T v[NT][4];
-  // A block's scalars: of the lane's four tokens (rows of a result tile), of token dealt(wave, n), and of the block.
-  // Two sets, of even and odd blocks: one is still in use when the next is asked for.
-  f32x4 first4[2], last4[2];
-  float first1[2], whole[2];
-  const int row4 = dealt(wave, 4 * g);
-  const auto token = [&](int c) { return (int64_t)seq.begin + (int64_t)c * kBlock; };
-  const auto rows_of = [&](int c) {
-    const int64_t left = seq.end - token(c);
-    return left < kBlock ? (int)left : kBlock;
-  };
-  const auto ask_rows = [&](int c) {
-    K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
-    if constexpr (!KEEP) Q.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
-  };
-  const auto ask_columns = [&](int c) {
-    Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
-  };
-  const auto ask_values = [&](int c, int set) {
-    const int rows = rows_of(c);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const T* p = vp + (token(c) + (row4 + r < rows ? row4 + r : rows - 1)) * a.v_stride;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) v[nt][r] = p[live[nt] ? col[nt] : 0];
-    }
-    const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
-    first4[set] = ld4(sc->first + row4);
-    last4[set] = ld4(sc->last + row4);
-    first1[set] = sc->first[dealt(wave, n)];
-    whole[set] = sc->first[kBlock - 1];
-  };
-  const auto ask_t = [&](int c) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      tf[p] = get_frag<mid>(ws + c * ws_step + Ops::t, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
-  };
-  const auto ask_p = [&](int c) {
-    if constexpr (!KEEP) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        pf[p] = get_frag<mid>(ws + c * ws_step + Ops::p, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
-    }
-  };
-  if (seq.blocks > 0) {
-    ask_rows(0);
-    ask_values(0, 0);
-    ask_t(0);
-    ask_columns(0);
-    ask_p(0);
-  }
-  const auto block = [&](int c, int set) {
-    const int rows = rows_of(c);
-    const int64_t t0 = token(c);
-    // (The last block asks for itself again. Loads under a condition would join their registers with the old ones
-    // by moves, and a move waits for the load right where it was asked for.)
-    const int next = c + 1 < seq.blocks ? c + 1 : c;
-    const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    __syncthreads();  // S is there; the block before has been read
-    f32x4 y[NT], o[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) y[nt] = o[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    {
-      Split<mid> bs[NT][kSteps];
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          bs[nt][ks] = get_frag<mid>(lds + L::s + nt * kSteps * kStepBytes<mid>, ks, lane);
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {
-        const Split<in> kf = K.get(ks);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) y[nt] = mma(kf, bs[nt][ks], y[nt]);
-      }
-      // (the chain goes on from y; Q S fills the time of its exchange)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f32x4 x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = (row4 + r < rows && live[nt] ? (float)v[nt][r] : 0.f) - first4[set][r] * y[nt][r];
-        put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);  // (beta is in T's columns)
-      }
-      if constexpr (!KEEP) {
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          const Split<in> qf = Q.get(ks);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) o[nt] = mma(bs[nt][ks], qf, o[nt]);
-        }
-      }
-    }
-    if (owner) Kc.store(Kt, rows);
-    ask_rows(next);
-    ask_values(next, set ^ 1);
-    __syncthreads();  // X is there
-    f32x4 U[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) U[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      if (p <= wave / 2) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          U[nt] = mma(tf[p], get_frag<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, p, lane), U[nt]);
-      }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      put_half<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * U[nt]);
-      if constexpr (!KEEP) put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, U[nt]);
-    }
-    // the update's left operands, transposed
-    Split<in> kc[kOwn][2];
-    if (owner) {
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) kc[i][p] = Kt.template col8<true>((tile0 + i) & 1, p, lane);
-    }
-    ask_t(next);
-    ask_columns(next);
-    if constexpr (KEEP) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (live[nt]) {
-          if (owner) {
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-              if (channel(tile0 + i) < DK)
-                st4(kept.S + (place * a.dv + col[nt]) * DK + channel(tile0 + i), S[nt][i]);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) kept.U[(place * kBlock + row4 + r) * a.dv + col[nt]] = U[nt][r];
-        }
-    }
-    __syncthreads();  // U is there
-    if (owner) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) S[nt][i] *= whole[set];
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Split<mid> ul = get_frag<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, p, lane);
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) S[nt][i] = mma(kc[i][p], ul, S[nt][i]);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-          put_half<mid>(lds + L::s + nt * kSteps * kStepBytes<mid>, (tile0 + i) >> 1, (tile0 + i) & 1, lane, S[nt][i]);
-    }
-    if constexpr (!KEEP) {  // (scale is in P)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) o[nt] *= a.scale * first1[set];
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (p <= wave / 2) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            o[nt] = mma(get_frag<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, p, lane), pf[p], o[nt]);
-        }
-      if (out_col < a.dv && dealt(wave, n) < rows) {
-        T* dst = op + (t0 + dealt(wave, n)) * out_stride;
-        if constexpr (NT == 2) {
-          store8(dst, join(o[0], o[1]));
-        } else {
-          typedef T vec __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<vec*>(dst) = __builtin_convertvector(o[0], vec);
-        }
-      }
-      ask_p(next);
-    }
-  };
-  for (int c = 0; c < seq.blocks; c += 2) {
-    block(c, 0);
-    if (c + 1 < seq.blocks) block(c + 1, 1);
-  }
-  if (a.S_out == nullptr || KEEP || !owner) return;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (live[nt] && channel(tile0 + i) < DK)
-        st4(a.S_out + state + (int64_t)col[nt] * DK + channel(tile0 + i), S[nt][i]);
-}
-
-template <typename T, int DK, int NT, typename Ops, bool KEEP>
-hipError_t launch_scan_tiles(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ScanLds<T, DK, NT>;
-  constexpr auto kernel = delta_scan_kernel<T, DK, NT, Ops, KEEP>;
-  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
-  if (e != hipSuccess) return e;
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
-  kernel<<<dim3((unsigned)item_grid((int64_t)a.n_seqs * a.H, slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
-  return hipGetLastError();
-}
-
-// 32 state rows per workgroup read K, Q, T and P half as often as 16; 16 give twice the workgroups where 32
-// would leave compute units without one.
-inline hipError_t wide_tiles(const DeltaArgs& a, bool* two) {
+// By rows once that fills most of the chip (half as many workgroups as compute units; the two ways cross between 64
+// and 256 workgroups, see scan_split.hpp), with two tiles per wavefront where there are workgroups enough, which
+// reads every left operand from LDS half as often (fp32's three parts would not fit). Split walks take 32 rows where
+// 16 would give over two workgroups per compute unit.
+template <typename T>
+hipError_t choose_walk(const DeltaArgs& a, Walk* walk) {
   int cus = 0;
   const hipError_t e = device_cus(&cus);
-  *two = e == hipSuccess && a.dv > 16 && (int64_t)a.n_seqs * a.H * ((a.dv + 31) / 32) >= 2 * cus;
-  return e;
-}
-
-template <typename T, int DK, typename Ops, bool KEEP>
-hipError_t launch_scan(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  bool two = false;
-  const hipError_t e = wide_tiles(a, &two);
   if (e != hipSuccess) return e;
-  return two ? launch_scan_tiles<T, DK, 2, Ops, KEEP>(a, kept, s) : launch_scan_tiles<T, DK, 1, Ops, KEEP>(a, kept, s);
+  const int64_t heads = (int64_t)a.n_seqs * a.H;
+  if (2 * heads * ((a.dv + 63) / 64) >= cus)
+    *walk = sizeof(T) == 2 && a.dv > 64 && heads * ((a.dv + 127) / 128) >= cus ? Walk::kRows128 : Walk::kRows64;
+  else
+    *walk = a.dv > 16 && heads * ((a.dv + 15) / 16) > 2 * cus ? Walk::kSplit32 : Walk::kSplit16;
+  return hipSuccess;
 }
 
 }  // namespace

@@ -1,0 +1,39 @@
+// Launches of the serial walks, by whichever way suits the batch.
+#pragma once
+
+#include "scan_rows.hpp"
+#include "scan_split.hpp"
+
+namespace rs {
+
+namespace {
+
+template <typename T, int DK, typename Ops, bool KEEP>
+hipError_t launch_scan(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
+  Walk walk;
+  const hipError_t e = choose_walk<T>(a, &walk);
+  if (e != hipSuccess) return e;
+  if constexpr (sizeof(T) == 2) {
+    if (walk == Walk::kRows128) return launch_scan_rows<T, DK, 2, Ops, KEEP>(a, kept, s);
+  }
+  if (walk == Walk::kSplit32) return launch_scan_split<T, DK, 2, Ops, KEEP>(a, kept, s);
+  if (walk == Walk::kSplit16) return launch_scan_split<T, DK, 1, Ops, KEEP>(a, kept, s);
+  return launch_scan_rows<T, DK, 1, Ops, KEEP>(a, kept, s);
+}
+
+template <typename T, int DK, typename Ops>
+hipError_t launch_reverse(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
+  Walk walk;
+  const hipError_t e = choose_walk<T>(a, &walk);
+  if (e != hipSuccess) return e;
+  if constexpr (sizeof(T) == 2) {
+    if (walk == Walk::kRows128) return launch_reverse_rows<T, DK, 2, Ops>(a, kept, s);
+  }
+  if (walk == Walk::kSplit32) return launch_reverse_split<T, DK, 2, Ops>(a, kept, s);
+  if (walk == Walk::kSplit16) return launch_reverse_split<T, DK, 1, Ops>(a, kept, s);
+  return launch_reverse_rows<T, DK, 1, Ops>(a, kept, s);
+}
+
+}  // namespace
+
+}  // namespace rs

@@ -83,10 +83,11 @@ class Delta:
     def bar(self):
         return 8 * 2.0 ** -18 if self.dtype != "f32" else 64 * 2.0 ** -24
 
-    def check_forward(self, out, last, bar=None):
+    def check_forward(self, out, last, bar=None, every=1):
+        """every: check every so many-th head (starting with each sequence's own)."""
         bar = self.bar() if bar is None else bar
         for s in range(self.N):
-            for h in range(self.H):
+            for h in range(s % every, self.H, every):
                 args, at, _ = self.head(s, h)
                 o, S, before = oracle.delta_rule(*args)
                 mag = max([np.abs(S).max()] + [np.abs(x).max() for x in before[:1]] + [1e-30])

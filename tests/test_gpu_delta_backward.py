@@ -31,12 +31,12 @@ def _run(d, maps=None, dS0=True, ws=None):
     return r
 
 
-def _check(d, r):
+def _check(d, r, every=1):
     bar = d.bar()
     assert d.err[0].item() == 0
     group = d.H // d.Hk
     for s in range(d.N):
-        for hk in range(d.Hk):
+        for hk in range(s % every, d.Hk, every):
             sums = [0.0, 0.0]
             mags = [0.0, 0.0]
             for h in range(hk * group, (hk + 1) * group):
@@ -101,6 +101,28 @@ def test_enough_heads_for_two_tiles_per_wavefront():
     d = Delta([65] * 33, H=8, Hk=4, dk=128, dv=128, dtype="bf16", seed=3)
     r = _run(d)
     _check(d, r)
+
+
+@pytest.mark.parametrize("dk", [16, 32, 64, 128])
+@pytest.mark.parametrize("dv", [16, 80, 128, 144])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_head_shapes_with_many_heads(dk, dv, dtype):
+    """Batches that fill the chip walk their blocks another way."""
+    d = Delta([129, 1, 64], H=132, Hk=66, dk=dk, dv=dv, dtype=dtype, room=5)
+    r = _run(d)
+    _check(d, r, every=17)
+    for x in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert (r[x][d.used:] == 7.0).all()
+
+
+def test_a_bad_sequence_of_shared_heads_is_left_alone():
+    d = Delta([70, 65], H=4, Hk=2, dk=32, dv=32)
+    m = d.maps()
+    m.block_seq[0] = 7  # the first block of the first sequence belongs to nobody
+    r = _run(d, m)
+    assert d.err[0].item() & rs.DEVERR_RANGE
+    for x in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert (r[x][:64] == 7.0).all() and not (r[x][70:] == 7.0).any()
 
 
 def test_a_longer_sequence():

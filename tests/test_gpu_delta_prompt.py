@@ -66,6 +66,40 @@ def test_enough_heads_for_two_tiles_per_wavefront():
     few.check_forward(out, last)
 
 
+@pytest.mark.parametrize("dk", [16, 32, 64, 128])
+@pytest.mark.parametrize("dv", [16, 80, 128, 144])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_head_shapes_with_many_heads(dk, dv, dtype):
+    """Batches that fill the chip walk their blocks another way."""
+    d = Delta([129, 1, 64], H=132, Hk=66, dk=dk, dv=dv, dtype=dtype, room=5)
+    out, last = _run(d)
+    d.check_forward(out, last, every=23)
+    assert (out[d.used:] == 7.0).all() and d.err[0].item() == 0
+
+
+def test_many_heads_at_the_end_of_the_arrays_and_past_it():
+    """The last block's rows: nothing behind them, and another sequence's behind them."""
+    for lens, room in (([70], 0), ([70], 40), ([3, 67], 0), ([70, 3], 0)):
+        d = Delta(lens, H=256, Hk=128, dk=64, dv=64, dtype="bf16", room=room)
+        if room:
+            d.v[d.used:] = float("nan")
+            d.k[d.used:] = float("inf")
+        d.check_forward(*_run(d), every=61)
+
+
+def test_both_walks_agree():
+    """The same sequence alone and among enough heads to fill the chip: other sums, within the bars of both."""
+    one = Delta([200], H=2, dk=128, dv=128, dtype="bf16", wide=False)
+    many = Delta([200] * 70, H=2, dk=128, dv=128, dtype="bf16", wide=False)
+    for x in ("q", "k", "v", "g", "beta"):
+        getattr(many, x).copy_(getattr(one, x).repeat(70, *[1] * (getattr(one, x).dim() - 1)))
+    many.S0.copy_(one.S0.expand_as(many.S0))
+    (a, la), (b, lb) = _run(one), _run(many)
+    assert torch.equal(b[:200], b[-200:]) and torch.equal(lb[0], lb[-1])
+    assert (la[0] - lb[0]).abs().max().item() <= 2 * one.bar() * max(1.0, la.abs().max().item())
+    one.check_forward(a, la)
+
+
 def test_a_longer_sequence():
     d = Delta([1500], H=2, Hk=1, dk=128, dv=128, dtype="bf16")
     d.check_forward(*_run(d))
