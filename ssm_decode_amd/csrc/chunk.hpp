@@ -5,9 +5,12 @@
 // the rounded remainder of the ones before it. Two parts keep 17 bits of it (relative error
 // at most 2^-18), three keep 24. A product of parts (i, j) is left out where i + j reaches the
 // larger part count, which is the size of the rounding already made. bf16 inputs are one
-// exact part and fp16 inputs two exact parts; what is computed on the way (states,
-// corrections, the inverse, decayed scores) takes two parts beside 16-bit inputs, which leaves
-// states and gradients within a few 1e-6 of 64-bit ones, and three beside fp32 inputs.
+// exact part and fp16 inputs two exact parts (their products with each other are kept to the parts of
+// what they go into). What the forward pass computes on the way (states, corrections, the
+// inverse, decayed scores) takes two parts beside 16-bit inputs, which leaves states within a few 1e-6 of
+// 64-bit ones, and three beside fp32 inputs. The backward pass takes three beside all: the gradients of g
+// and beta are differences of products' sums, and in batches of a few tokens two parts left one in a hundred
+// of them 1e-5 off and more, three 1e-6 (for a seventh more time).
 //
 // Layout. In D = A B + C of v_mfma_f32_16x16x32_bf16 lane l (n = l & 15, g = l >> 4) holds
 // A[l & 15][8g .. 8g + 7], B[8g .. 8g + 7][n] and D[4g .. 4g + 3][n]. A result can be the next
@@ -36,6 +39,8 @@ template <>
 struct Parts<float> {
   static constexpr int in = 3, mid = 3;
 };
+
+constexpr int kGradParts = 3;  // of what the backward pass computes on the way, for every type
 
 template <int N>
 struct Split {
@@ -68,14 +73,14 @@ __device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) {
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// How many products of parts are kept, and the products, smallest first: f(i, j) for part i of A and part j of B.
+// How many products of parts are kept, and the products, smallest first: f(i, j) for part i of A and part j of B
+// where i + j < ORDER.
 template <int NA, int NB>
 constexpr int kProducts = NA * NB - (NA < NB ? NA * (NA - 1) / 2 : NB * (NB - 1) / 2);
-template <int NA, int NB, typename F>
+template <int NA, int NB, int ORDER = (NA > NB ? NA : NB), typename F>
 __device__ __forceinline__ void products(const F& f) {
-  constexpr int kOrder = NA > NB ? NA : NB;
 #pragma unroll
-  for (int o = kOrder - 1; o >= 0; --o)
+  for (int o = ORDER - 1; o >= 0; --o)
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       if (o - i >= 0 && o - i < NB) f(i, o - i);
@@ -87,10 +92,15 @@ __device__ __forceinline__ f32x4 mfma(const bf16x8& a, const bf16x8& b, const f3
 
 // acc += A B. (Its products wait for each other; where several results are built at once, `products`
 // around the loop over them keeps the matrix pipe full.)
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 mma(const Split<NA>& a, const Split<NB>& b, f32x4 acc) {
-  products<NA, NB>([&](int i, int j) { acc = mfma(a.p[i], b.p[j], acc); });
+template <int ORDER, int NA, int NB>
+__device__ __forceinline__ f32x4 mma_to(const Split<NA>& a, const Split<NB>& b, f32x4 acc) {
+  products<NA, NB, ORDER>([&](int i, int j) { acc = mfma(a.p[i], b.p[j], acc); });
   return acc;
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Split<NA>& a, const Split<NB>& b, const f32x4& acc) {
+  return mma_to<(NA > NB ? NA : NB)>(a, b, acc);
 }
 
 // The index of row m of result tile `tile` (see above).

@@ -24,11 +24,12 @@ namespace rs {
 
 namespace {
 
-template <int MID>
+// Where a block's operands lie in the workspace.
 struct BackwardBlock {
   static constexpr bool backward = true;
-  static constexpr int64_t t = 0, scalars = t + frag_bytes(MID), tt = scalars + sizeof(BlockScalars),
-                           pt = tt + frag_bytes(MID), bytes = pt + frag_bytes(MID);
+  static constexpr int mid = kGradParts;
+  static constexpr int64_t t = 0, scalars = t + frag_bytes(mid), tt = scalars + sizeof(BlockScalars),
+                           pt = tt + frag_bytes(mid), bytes = pt + frag_bytes(mid);
   static constexpr int64_t scan_bytes = tt;                   // what the forward scan reads, from the start
   static constexpr int64_t reverse_bytes = bytes - scalars;   // and the reverse scan, from the scalars
 };
@@ -37,12 +38,12 @@ struct BackwardBlock {
 // q, k and the two 64 x 64 matrices Y and M: the two sets share their LDS, and two workgroups a compute unit.
 template <typename T, int DK>
 struct GradLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  static constexpr int in = Parts<T>::in, mid = BackwardBlock::mid;
   using State = Tile<kWide<DK>, mid, 32>;
   using Cols = Tile<32, mid>;
   using DOut = Tile<32, in>;
   using Rows = Tile<kWide<DK>, in>;
-  using Square = Tile<64, mid>;
+  using Square = Tile<64, Parts<T>::mid>;  // (they go into dq and dk only)
   static constexpr int s = 0, ds = s + State::kBytes, u = ds + State::kBytes, x = u + Cols::kBytes, d = x + Cols::kBytes,
                        end1 = d + DOut::kBytes;
   static constexpr int k = 0, q = k + Rows::kBytes, y = q + Rows::kBytes, m = y + Square::kBytes,
@@ -57,10 +58,10 @@ struct GradLds {
 template <typename T, int DK>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_gradients_kernel(const DeltaArgs a, const Kept kept, float* dq_part, float* dk_part) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = BackwardBlock::mid, sq = Parts<T>::mid;
   constexpr int kTiles = kWide<DK> / 16, kSteps = kTiles / 2;
   using L = GradLds<T, DK>;
-  using Ops = BackwardBlock<mid>;
+  using Ops = BackwardBlock;
   extern __shared__ __align__(16) char lds[];
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
   if (b >= a.cu_blocks[a.n_seqs]) return;
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
           const Split<in> kj = K.row8(16 * jt + n, ks, g);
-          qk = mma(kj, Q.row8(i, ks, g), qk);
-          kk = mma(kj, K.row8(i, ks, g), kk);
+          qk = mma_to<mid>(kj, Q.row8(i, ks, g), qk);
+          kk = mma_to<mid>(kj, K.row8(i, ks, g), kk);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -246,9 +247,9 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       }
       if (jt <= wave || (jt == wave + 1 && (wave & 1) == 0)) {  // (the zero tile that shares a step)
         const int chunk = 2 * jt + (g >> 1), half = (g & 1) * 8;
-        const Split<mid> ys = split8<mid>(join(y, m));
+        const Split<sq> ys = split8<sq>(join(y, m));
 #pragma unroll
-        for (int p = 0; p < mid; ++p) {
+        for (int p = 0; p < sq; ++p) {
           typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
           const int off = p * L::Square::kPlane + L::Square::at(i, chunk) + half;
           *reinterpret_cast<bf16x4*>(Yt.base + off) = __builtin_shufflevector(ys.p[p], ys.p[p], 0, 1, 2, 3);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
   for (int sj = 0; sj < 2; ++sj) {
     if (sj <= wave / 2) {
-      const Split<mid> yr = Yt.row8(i, sj, g), mr = Mt.row8(i, sj, g);
+      const Split<sq> yr = Yt.row8(i, sj, g), mr = Mt.row8(i, sj, g);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         const Split<in> kc = K.template col8<true>(t, sj, lane);
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       }
     }
     if (sj >= wave / 2) {
-      const Split<mid> yc = Yt.template col8<false>(wave, sj, lane), mc = Mt.template col8<false>(wave, sj, lane);
+      const Split<sq> yc = Yt.template col8<false>(wave, sj, lane), mc = Mt.template col8<false>(wave, sj, lane);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         f1[t] = mma(Q.template col8<true>(t, sj, lane), yc, f1[t]);
@@ -385,13 +386,12 @@ __global__ void __launch_bounds__(256) delta_share_kernel(const DeltaArgs a, con
   }
 }
 
-template <int MID>
 struct BackwardSizes {
   // 256-byte aligned pieces of the workspace: operands, S, dS, U, dX, and shared heads' dq and dk
   int64_t ops, state, cols, part;
   BackwardSizes(int64_t blocks, int64_t tokens, int H, int Hk, int dk, int dv) {
     const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-    ops = up(blocks * H * BackwardBlock<MID>::bytes);
+    ops = up(blocks * H * BackwardBlock::bytes);
     state = up(blocks * H * dv * dk * 4);
     cols = up(blocks * H * kBlock * dv * 4);
     part = H == Hk ? 0 : up(tokens * H * dk * 4);
@@ -401,19 +401,18 @@ struct BackwardSizes {
 
 template <typename T, int DK>
 hipError_t launch_backward(const DeltaArgs& a, hipStream_t s) {
-  constexpr int mid = Parts<T>::mid;
-  const BackwardSizes<mid> sizes(a.max_blocks, a.n_tokens, a.H, a.Hk, a.dk, a.dv);
+  const BackwardSizes sizes(a.max_blocks, a.n_tokens, a.H, a.Hk, a.dk, a.dv);
   char* p = static_cast<char*>(a.ws) + sizes.ops;
   Kept kept;
   kept.S = reinterpret_cast<float*>(p);
   kept.dS = reinterpret_cast<float*>(p + sizes.state);
   kept.U = reinterpret_cast<float*>(p + 2 * sizes.state);
   kept.dX = reinterpret_cast<float*>(p + 2 * sizes.state + sizes.cols);
-  hipError_t e = launch_prepare<T, DK, BackwardBlock<mid>>(a, s);
+  hipError_t e = launch_prepare<T, DK, BackwardBlock>(a, s);
   if (e != hipSuccess) return e;
-  e = launch_scan<T, DK, BackwardBlock<mid>, true>(a, kept, s);
+  e = launch_scan<T, DK, BackwardBlock, true>(a, kept, s);
   if (e != hipSuccess) return e;
-  e = launch_reverse<T, DK, BackwardBlock<mid>>(a, kept, s);
+  e = launch_reverse<T, DK, BackwardBlock>(a, kept, s);
   if (e != hipSuccess) return e;
   using L = GradLds<T, DK>;
   constexpr auto kernel = delta_gradients_kernel<T, DK>;
@@ -446,8 +445,7 @@ hipError_t launch_dk(const DeltaArgs& a, hipStream_t s) {
 }  // namespace
 
 int64_t delta_backward_bytes(const replayssm_delta_config& c, int max_blocks) {
-  return c.dtype == REPLAYSSM_F32 ? BackwardSizes<3>(max_blocks, c.n_tokens, c.H, c.Hk, c.dk, c.dv).total()
-                                  : BackwardSizes<2>(max_blocks, c.n_tokens, c.H, c.Hk, c.dk, c.dv).total();
+  return BackwardSizes(max_blocks, c.n_tokens, c.H, c.Hk, c.dk, c.dv).total();
 }
 
 hipError_t launch_delta_prompt_backward(const DeltaArgs& a, hipStream_t s) {

@@ -23,6 +23,7 @@ namespace {
 template <int MID>
 struct ForwardBlock {
   static constexpr bool backward = false;
+  static constexpr int mid = MID;
   static constexpr int64_t t = 0, scalars = t + frag_bytes(MID), p = scalars + sizeof(BlockScalars),
                            bytes = p + frag_bytes(MID), scan_bytes = bytes;
 };

@@ -38,6 +38,7 @@ struct FeedLayout {
   static constexpr int q = Rows::kBytes, v = q + (WITH_Q ? Rows::kBytes : 0), ops = v + Values::kBytes,
                        bytes = ops + OPS, total = bytes * (kAsync ? 2 : 1);
   static_assert(OPS % 1024 == 0, "whole instructions");
+  static_assert(total <= 160 * 1024, "the LDS of a compute unit");
 };
 
 // Common to both ways: where the current block's pieces are.

@@ -83,7 +83,7 @@ __device__ __forceinline__ void invert(const float* A, float* Tm) {
 
 template <typename T, int DK, typename Out>
 __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const DeltaArgs a) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = Out::mid;
   using L = PrepareLds<T, DK>;
   using Rows = typename L::Rows;
   extern __shared__ __align__(16) char lds[];
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
     for (int jt = 0; jt <= it; ++jt) {
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < kWide<DK> / 32; ++k) acc = mma<in, in>(K.row8(16 * jt + n, k, g), K.row8(i, k, g), acc);
+      for (int k = 0; k < kWide<DK> / 32; ++k) acc = mma_to<mid>(K.row8(16 * jt + n, k, g), K.row8(i, k, g), acc);
       f32x4 v;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
       for (int k = 0; k < kWide<DK> / 32; ++k) {
         const Split<in> qi = Q.row8(i, k, g);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) acc[p] = mma<in, in>(K.row8(dealt(2 * sj + p, n), k, g), qi, acc[p]);
+        for (int p = 0; p < 2; ++p) acc[p] = mma_to<mid>(K.row8(dealt(2 * sj + p, n), k, g), qi, acc[p]);
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p)
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
       for (int k = 0; k < kWide<DK> / 32; ++k) {
         const Split<in> kj = K.row8(j, k, g);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) acc[p] = mma<in, in>(Q.row8(dealt(2 * si + p, n), k, g), kj, acc[p]);
+        for (int p = 0; p < 2; ++p) acc[p] = mma_to<mid>(Q.row8(dealt(2 * si + p, n), k, g), kj, acc[p]);
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p)

@@ -67,7 +67,7 @@ using ScanLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::scan_bytes, !KEEP>;
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 __global__ void __launch_bounds__(kChunkThreads)
     delta_scan_rows_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = Ops::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
   constexpr bool kDealt = NT == 2 && !KEEP;  // a lane's output rows of both tiles are neighbours
@@ -348,7 +348,7 @@ using ReverseLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::reverse_bytes, true>;
 template <typename T, int DK, int NT, typename Ops>
 __global__ void __launch_bounds__(kChunkThreads)
     delta_reverse_rows_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = Ops::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
   using L = ReverseLayout<T, DK, NT, Ops>;

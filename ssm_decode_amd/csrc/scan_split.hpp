@@ -13,7 +13,7 @@
 // times as often for the same rows, so it is used where those would leave most compute units idle. Measured,
 // bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 1.17 against 1.56 ms; 24 ragged
 // sequences of 32 heads, 0.43 against 0.29 ms; the backward pass's two walks over 8 sequences of 2048 tokens and 16
-// heads, 0.49 against 0.34 ms.
+// heads, 0.65 against 0.40 ms.
 #pragma once
 
 #include "scan.hpp"
@@ -106,9 +106,9 @@ struct RowOperand {
   }
 };
 
-template <typename T, int DK, int NT>
+template <typename T, int DK, int NT, int MID>
 struct SplitLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid, kSteps = kWide<DK> / 32;
+  static constexpr int in = Parts<T>::in, mid = MID, kSteps = kWide<DK> / 32;
   static constexpr int s = 0, x = s + NT * kSteps * kStepBytes<mid>, u = x + NT * 2 * kStepBytes<mid>,
                        ul = u + NT * 2 * kStepBytes<mid>, k = ul + NT * 2 * kStepBytes<mid>,
                        total = k + 4 * Tile<32, in>::kBytes;
@@ -120,11 +120,11 @@ struct SplitLds {
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_scan_split_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = Ops::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;  // state tiles of a wavefront
   constexpr bool kDealt = NT == 2 && !KEEP;           // a lane's output rows of both tiles are neighbours
-  using L = SplitLds<T, DK, NT>;
+  using L = SplitLds<T, DK, NT, Ops::mid>;
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
   int item, slice;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 hipError_t launch_scan_split(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = SplitLds<T, DK, NT>;
+  using L = SplitLds<T, DK, NT, Ops::mid>;
   constexpr auto kernel = delta_scan_split_kernel<T, DK, NT, Ops, KEEP>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
@@ -377,9 +377,9 @@ hipError_t launch_scan_split(const DeltaArgs& a, const Kept& kept, hipStream_t s
   return hipGetLastError();
 }
 
-template <typename T, int DK, int NT>
+template <typename T, int DK, int NT, int MID>
 struct ReverseSplitLds {
-  static constexpr int in = Parts<T>::in, mid = Parts<T>::mid, kSteps = kWide<DK> / 32;
+  static constexpr int in = Parts<T>::in, mid = MID, kSteps = kWide<DK> / 32;
   // dS; dO; e^G d; dU; -e^G beta dX
   static constexpr int s = 0, d = s + NT * kSteps * kStepBytes<mid>, df = d + NT * 2 * kStepBytes<in>,
                        u = df + NT * 2 * kStepBytes<mid>, x = u + NT * 2 * kStepBytes<mid>,
@@ -391,10 +391,10 @@ struct ReverseSplitLds {
 template <typename T, int DK, int NT, typename Ops>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_reverse_split_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = Ops::mid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;
-  using L = ReverseSplitLds<T, DK, NT>;
+  using L = ReverseSplitLds<T, DK, NT, Ops::mid>;
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
   int item, slice;
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 
 template <typename T, int DK, int NT, typename Ops>
 hipError_t launch_reverse_split(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ReverseSplitLds<T, DK, NT>;
+  using L = ReverseSplitLds<T, DK, NT, Ops::mid>;
   constexpr auto kernel = delta_reverse_split_kernel<T, DK, NT, Ops>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
