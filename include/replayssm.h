@@ -569,7 +569,7 @@ int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ra
 /* Gradients of replayssm_delta_prompt: from dout [n_tokens][H][dv] (of out) and dS_out
  * [n_seqs][H][dv][dk] (of S_out; NULL: zero) to dq, dk [n_tokens][Hk][dk] (summed over the value
  * heads that share a key head), dv [n_tokens][H][dv], dg, dbeta [n_tokens][H] fp32, and dS0
- * (of S0; NULL: not wanted; must not be dS_out). dq, dk and dv are contiguous, in `dtype`.
+ * (of S0; NULL: not wanted; may be dS_out). dq, dk and dv are contiguous, in `dtype`.
  * The inputs, tables and S0 are those of the forward call; states are computed again, so nothing
  * of the forward call's workspace is needed. workspace: backward_bytes of replayssm_delta_sizes.
  * Sums have a fixed order: equal calls give equal bits. Rows of tokens that no sequence holds are

@@ -596,6 +596,15 @@ def _delta_inputs(cfg, dev, t, q, k, v, g, beta):
             _dev(beta, dev, f32, (n, cfg.H), "beta"))
 
 
+def _maps(cfg, maps, dev):
+    """The C struct of a batch's tables; those of RaggedMaps are checked against the batch."""
+    tensors = getattr(maps, "tensors", None)
+    if tensors is not None:
+        for t, what in zip(tensors[:2], ("cu_tokens", "cu_blocks")):
+            _dev(t, dev, torch.int32, (cfg.n_seqs + 1,), what)
+    return ctypes.byref(maps)
+
+
 def delta_step(cfg, cu_tokens, slots, n_slots, q, k, v, g, beta, S_in, S_out, out, err, stream=None):
     dev, s = _device_and_stream(stream)
     t, i32, n = _torch_dtype(cfg.dtype, "delta_step"), torch.int32, cfg.n_seqs
@@ -613,7 +622,7 @@ def delta_prompt(cfg, maps, q, k, v, g, beta, S0, out, S_out, workspace, err, st
     t, f32 = _torch_dtype(cfg.dtype, "delta_prompt"), torch.float32
     states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
     _check(lib().replayssm_delta_prompt(
-        ctypes.byref(cfg), ctypes.byref(maps), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
+        ctypes.byref(cfg), _maps(cfg, maps, dev), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
         _dev(S0, dev, f32, states, "S0"), _dev(out, dev, t, (cfg.n_tokens, cfg.H, cfg.dv), "out"),
         _dev(S_out, dev, f32, states, "S_out"), _workspace(workspace, dev, need),
         _dev(err, dev, torch.int32, None, "err"), s), "delta_prompt")
@@ -626,7 +635,7 @@ def delta_prompt_backward(cfg, maps, q, k, v, g, beta, S0, dout, dS_out, dq, dk,
     t, n, f32 = _torch_dtype(cfg.dtype, "delta_prompt_backward"), cfg.n_tokens, torch.float32
     states, keys, values = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk), (n, cfg.Hk, cfg.dk), (n, cfg.H, cfg.dv)
     _check(lib().replayssm_delta_prompt_backward(
-        ctypes.byref(cfg), ctypes.byref(maps), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
+        ctypes.byref(cfg), _maps(cfg, maps, dev), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
         _dev(S0, dev, f32, states, "S0"), _dev(dout, dev, t, values, "dout"),
         _dev(dS_out, dev, f32, states, "dS_out"), _dev(dq, dev, t, keys, "dq"), _dev(dk, dev, t, keys, "dk"),
         _dev(dv, dev, t, values, "dv"), _dev(dg, dev, f32, (n, cfg.H), "dg"),

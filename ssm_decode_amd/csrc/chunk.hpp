@@ -350,6 +350,9 @@ struct BlockScalars {
   float unused[kBlock];
 };
 
+// A log decay that can be summed: e^-1e4 is 0 in fp32 as e^-infinity is, and later differences stay whole. (NaN stays.)
+__device__ __forceinline__ float closed_gate(float g) { return g < -1e4f ? -1e4f : g; }
+
 // A sequence's place in the packed batch; ok = false where the tables contradict each other or
 // leave the arrays (nothing of the sequence is touched then).
 struct SeqRange {

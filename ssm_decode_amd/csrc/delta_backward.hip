@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     sc->first[lane] = src->first[lane];
     sc->last[lane] = src->last[lane];
     sc->beta[lane] = src->beta[lane];
-    double sum = lane < rows ? (double)fmaxf(a.g[(t0 + lane) * a.H + h], -1e4f) : 0.0;
+    double sum = lane < rows ? (double)closed_gate(a.g[(t0 + lane) * a.H + h]) : 0.0;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double up = __shfl_up(sum, d);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
   if (wave == 0) {
     const bool live = lane < rows;
     const int64_t at = (t0 + lane) * a.H + h;
-    double sum = live ? (double)fmaxf(a.g[at], -1e4f) : 0.0;
+    double sum = live ? (double)closed_gate(a.g[at]) : 0.0;
     const float bt = live ? a.beta[at] : 0.f;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {

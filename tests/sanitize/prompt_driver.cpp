@@ -95,6 +95,9 @@ int main() {
         const int r = replayssm_delta_sizes(&c, &n, &w);
         EXPECT(replayssm_delta_step(&c, I(1), I(2), 4, p(3), p(4), p(5), F(6), F(7), F(8), F(9), p(10), I(11), nullptr), r);
         EXPECT(replayssm_delta_prompt(&c, &m, p(3), p(4), p(5), F(6), F(7), F(8), p(9), F(10), p(11), I(12), nullptr), r);
+        EXPECT(replayssm_delta_prompt_backward(&c, &m, p(3), p(4), p(5), F(6), F(7), F(8), p(9), F(10), p(11), p(12), p(13),
+                                               F(14), F(15), F(16), p(17), I(18), nullptr),
+               r);
       }
   EXPECT(replayssm_delta_sizes(nullptr, &n, &w), REPLAYSSM_EINVAL);
   EXPECT(replayssm_ragged_sizes(nullptr, &n), REPLAYSSM_EINVAL);

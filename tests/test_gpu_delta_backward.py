@@ -225,3 +225,15 @@ def test_captured_and_replayed_with_other_inputs():
         torch.cuda.synchronize()
         for x in NAMES:
             assert torch.equal(r[x], want[x]), x
+
+
+@pytest.mark.parametrize("H", [2, 260])
+def test_state_gradients_in_place(H):
+    d = Delta([70, 0, 3], H=H, dk=32, dv=32)
+    want = _run(d)
+    r, m = {x: torch.empty_like(y) for x, y in want.items()}, d.maps()
+    S = d.dS.clone()
+    r["dS0"] = S
+    rs.delta_prompt_backward(d.cfg, m.struct, d.q, d.k, d.v, d.g, d.beta, d.S0, d.do, S, *[r[x] for x in NAMES], d.workspace(1), d.err)
+    for x in NAMES:
+        assert torch.equal(r[x], want[x]), x

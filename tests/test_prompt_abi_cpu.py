@@ -130,6 +130,24 @@ def test_delta_pointers(lib):
     assert lib.replayssm_delta_step(ctypes.byref(cfg), P, None, 1, *[P] * 9, None) == rs.EINVAL
 
 
+def test_delta_backward_pointers(lib):
+    cfg = rs.make_delta_config(2, 100, 4, 2, 32, 32)
+    m = rs.Ragged(*[P] * 6)
+    # of q, k, v, g, beta, S0, dout, dS_out, dq, dk, dv, dg, dbeta, dS0, workspace, err
+    optional = (5, 7, 13)
+    for i in range(16):
+        for bad in (P + 4,) if i in optional else (None, P + 4):
+            args = [P] * 16 + [None]
+            args[i] = bad
+            assert lib.replayssm_delta_prompt_backward(ctypes.byref(cfg), ctypes.byref(m), *args) == rs.EINVAL, (i, bad)
+    assert lib.replayssm_delta_prompt_backward(ctypes.byref(cfg), None, *[P] * 16, None) == rs.EINVAL
+    for i in (0, 1, 4):  # of cu_tokens, cu_blocks, token_seq, token_pos, block_seq, err
+        bad = rs.Ragged(*[None if j == i else P for j in range(6)])
+        assert lib.replayssm_delta_prompt_backward(ctypes.byref(cfg), ctypes.byref(bad), *[P] * 16, None) == rs.EINVAL, i
+    cfg.dk = 48
+    assert lib.replayssm_delta_prompt_backward(ctypes.byref(cfg), ctypes.byref(m), *[P] * 16, None) == rs.EINVAL
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     import torch
 
