@@ -3,14 +3,13 @@
 //
 // Precision. The matrix cores take bf16; an fp32 value goes in as a sum of bf16 parts, each
 // the rounded remainder of the ones before it. Two parts keep 17 bits of it (relative error
-// at most 2^-18), three keep 24. A product of parts (i, j) is left out where i + j reaches the
-// larger part count, which is the size of the rounding already made. bf16 inputs are one
-// exact part and fp16 inputs two exact parts (their products with each other are kept to the parts of
-// what they go into). What the forward pass computes on the way (states, corrections, the
-// inverse, decayed scores) takes two parts beside 16-bit inputs, which leaves states within a few 1e-6 of
-// 64-bit ones, and three beside fp32 inputs. The backward pass takes three beside all: the gradients of g
-// and beta are differences of products' sums, and in batches of a few tokens two parts left one in a hundred
-// of them 1e-5 off and more, three 1e-6 (for a seventh more time).
+// at most 2^-18), three keep 24. A product of parts (i, j) is left out where i + j reaches the larger
+// part count, which is the size of the rounding already made. bf16 inputs are one exact part
+// and fp16 inputs two. What is computed on the way to a state or an fp32 gradient (states,
+// corrections, the inverse) takes three parts for every type, as the products of the inputs that
+// it is made of do; what goes into 16-bit outputs alone (Q S, P U; the gradients' Y and M)
+// takes two. With two throughout, states were 4e-6 to 9e-6 off and dg and dbeta of one batch of a few
+// tokens in a hundred over 1e-5; three leave 1e-7 and cost a tenth of the time.
 //
 // Layout. In D = A B + C of v_mfma_f32_16x16x32_bf16 lane l (n = l & 15, g = l >> 4) holds
 // A[l & 15][8g .. 8g + 7], B[8g .. 8g + 7][n] and D[4g .. 4g + 3][n]. A result can be the next
@@ -26,21 +25,21 @@
 namespace rs {
 
 template <typename T>
-struct Parts;
+struct Parts;  // of inputs, and of what goes into outputs of type T alone
 template <>
 struct Parts<__bf16> {
-  static constexpr int in = 1, mid = 2;
+  static constexpr int in = 1, low = 2;
 };
 template <>
 struct Parts<_Float16> {
-  static constexpr int in = 2, mid = 2;
+  static constexpr int in = 2, low = 2;
 };
 template <>
 struct Parts<float> {
-  static constexpr int in = 3, mid = 3;
+  static constexpr int in = 3, low = 3;
 };
 
-constexpr int kGradParts = 3;  // of what the backward pass computes on the way, for every type
+constexpr int kMid = 3;  // of everything else
 
 template <int N>
 struct Split {
@@ -69,6 +68,15 @@ __device__ __forceinline__ Split<N> split8(const f32x8& x) {
   return s;
 }
 
+// The first N parts.
+template <int N, int M>
+__device__ __forceinline__ Split<N> first_parts(const Split<M>& x) {
+  Split<N> s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s.p[i] = x.p[i];
+  return s;
+}
+
 __device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) {
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
@@ -76,8 +84,10 @@ __device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) {
 // How many products of parts are kept, and the products, smallest first: f(i, j) for part i of A and part j of B
 // where i + j < ORDER.
 template <int NA, int NB>
+constexpr int kOrder = NA > NB ? NA : NB;
+template <int NA, int NB>
 constexpr int kProducts = NA * NB - (NA < NB ? NA * (NA - 1) / 2 : NB * (NB - 1) / 2);
-template <int NA, int NB, int ORDER = (NA > NB ? NA : NB), typename F>
+template <int NA, int NB, int ORDER = kOrder<NA, NB>, typename F>
 __device__ __forceinline__ void products(const F& f) {
 #pragma unroll
   for (int o = ORDER - 1; o >= 0; --o)
@@ -97,10 +107,9 @@ __device__ __forceinline__ f32x4 mma_to(const Split<NA>& a, const Split<NB>& b, 
   products<NA, NB, ORDER>([&](int i, int j) { acc = mfma(a.p[i], b.p[j], acc); });
   return acc;
 }
-
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Split<NA>& a, const Split<NB>& b, const f32x4& acc) {
-  return mma_to<(NA > NB ? NA : NB)>(a, b, acc);
+  return mma_to<kOrder<NA, NB>>(a, b, acc);
 }
 
 // The index of row m of result tile `tile` (see above).
@@ -321,9 +330,9 @@ __device__ __forceinline__ void zero_tile(const Tile<W, N, ROWS>& t) {
 
 // What the kernels pass to each other per (block, value head), in 16-byte units of a lane:
 // triangular 64 x 64 operands as 6 fragments (row tile t, 32-column step s; the two that are
-// zero are not kept) of `mid` parts, and the block's scalars.
+// zero are not kept) of `parts` parts, and the block's scalars.
 constexpr int kFrags = 6;
-__host__ __device__ constexpr int64_t frag_bytes(int mid) { return (int64_t)kFrags * mid * 1024; }
+__host__ __device__ constexpr int64_t frag_bytes(int parts) { return (int64_t)kFrags * parts * 1024; }
 // lower triangle: s <= t / 2; upper triangle: s >= t / 2
 __device__ __forceinline__ int lower_frag(int t, int s) { return t < 2 ? t : 2 + 2 * (t - 2) + s; }
 __device__ __forceinline__ int upper_frag(int t, int s) { return t < 2 ? 2 * t + s : 2 + t; }

@@ -27,9 +27,8 @@ namespace {
 // Where a block's operands lie in the workspace.
 struct BackwardBlock {
   static constexpr bool backward = true;
-  static constexpr int mid = kGradParts;
-  static constexpr int64_t t = 0, scalars = t + frag_bytes(mid), tt = scalars + sizeof(BlockScalars),
-                           pt = tt + frag_bytes(mid), bytes = pt + frag_bytes(mid);
+  static constexpr int64_t t = 0, scalars = t + frag_bytes(kMid), tt = scalars + sizeof(BlockScalars),
+                           pt = tt + frag_bytes(kMid), bytes = pt + frag_bytes(kMid);
   static constexpr int64_t scan_bytes = tt;                   // what the forward scan reads, from the start
   static constexpr int64_t reverse_bytes = bytes - scalars;   // and the reverse scan, from the scalars
 };
@@ -38,12 +37,12 @@ struct BackwardBlock {
 // q, k and the two 64 x 64 matrices Y and M: the two sets share their LDS, and two workgroups a compute unit.
 template <typename T, int DK>
 struct GradLds {
-  static constexpr int in = Parts<T>::in, mid = BackwardBlock::mid;
+  static constexpr int in = Parts<T>::in, mid = kMid;
   using State = Tile<kWide<DK>, mid, 32>;
   using Cols = Tile<32, mid>;
   using DOut = Tile<32, in>;
   using Rows = Tile<kWide<DK>, in>;
-  using Square = Tile<64, Parts<T>::mid>;  // (they go into dq and dk only)
+  using Square = Tile<64, Parts<T>::low>;  // (they go into dq and dk only)
   static constexpr int s = 0, ds = s + State::kBytes, u = ds + State::kBytes, x = u + Cols::kBytes, d = x + Cols::kBytes,
                        end1 = d + DOut::kBytes;
   static constexpr int k = 0, q = k + Rows::kBytes, y = q + Rows::kBytes, m = y + Square::kBytes,
@@ -58,7 +57,7 @@ struct GradLds {
 template <typename T, int DK>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_gradients_kernel(const DeltaArgs a, const Kept kept, float* dq_part, float* dk_part) {
-  constexpr int in = Parts<T>::in, mid = BackwardBlock::mid, sq = Parts<T>::mid;
+  constexpr int in = Parts<T>::in, mid = kMid, sq = Parts<T>::low;
   constexpr int kTiles = kWide<DK> / 16, kSteps = kTiles / 2;
   using L = GradLds<T, DK>;
   using Ops = BackwardBlock;

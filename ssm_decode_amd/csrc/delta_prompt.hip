@@ -20,19 +20,18 @@ namespace rs {
 namespace {
 
 // Where a block's operands lie in the workspace.
-template <int MID>
+template <int LOW>
 struct ForwardBlock {
   static constexpr bool backward = false;
-  static constexpr int mid = MID;
-  static constexpr int64_t t = 0, scalars = t + frag_bytes(MID), p = scalars + sizeof(BlockScalars),
-                           bytes = p + frag_bytes(MID), scan_bytes = bytes;
+  static constexpr int64_t t = 0, scalars = t + frag_bytes(kMid), p = scalars + sizeof(BlockScalars),
+                           bytes = p + frag_bytes(LOW), scan_bytes = bytes;
 };
 
 template <typename T, int DK>
 hipError_t launch_forward(const DeltaArgs& a, hipStream_t s) {
-  hipError_t e = launch_prepare<T, DK, ForwardBlock<Parts<T>::mid>>(a, s);
+  hipError_t e = launch_prepare<T, DK, ForwardBlock<Parts<T>::low>>(a, s);
   if (e != hipSuccess) return e;
-  return launch_scan<T, DK, ForwardBlock<Parts<T>::mid>, false>(a, Kept{}, s);
+  return launch_scan<T, DK, ForwardBlock<Parts<T>::low>, false>(a, Kept{}, s);
 }
 
 template <typename T>
@@ -45,12 +44,10 @@ hipError_t launch_dk(const DeltaArgs& a, hipStream_t s) {
   }
 }
 
-int mid_parts(int dtype) { return dtype == REPLAYSSM_F32 ? 3 : 2; }
-
 }  // namespace
 
 int64_t delta_forward_bytes(const replayssm_delta_config& c, int max_blocks) {
-  const int64_t block = mid_parts(c.dtype) == 3 ? ForwardBlock<3>::bytes : ForwardBlock<2>::bytes;
+  const int64_t block = c.dtype == REPLAYSSM_F32 ? ForwardBlock<3>::bytes : ForwardBlock<2>::bytes;
   return (int64_t)max_blocks * c.H * block;
 }
 

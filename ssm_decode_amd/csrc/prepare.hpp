@@ -83,7 +83,7 @@ __device__ __forceinline__ void invert(const float* A, float* Tm) {
 
 template <typename T, int DK, typename Out>
 __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const DeltaArgs a) {
-  constexpr int in = Parts<T>::in, mid = Out::mid;
+  constexpr int in = Parts<T>::in, mid = kMid;
   using L = PrepareLds<T, DK>;
   using Rows = typename L::Rows;
   extern __shared__ __align__(16) char lds[];
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
           const int j = 32 * sj + 8 * g + 4 * p + r;
           acc[p][r] = j <= i ? a.scale * acc[p][r] * expf((float)(G[i] - G[j])) : 0.f;
         }
-      put_frag<mid>(out + Out::p, lower_frag(wave, sj), lane, split8<mid>(join(acc[0], acc[1])));
+      put_frag<Parts<T>::low>(out + Out::p, lower_frag(wave, sj), lane, split8<Parts<T>::low>(join(acc[0], acc[1])));
     }
   } else {  // P^T as the left operand of P^T dO
     const int j = dealt(wave, n);

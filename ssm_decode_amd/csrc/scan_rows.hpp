@@ -67,7 +67,7 @@ using ScanLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::scan_bytes, !KEEP>;
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 __global__ void __launch_bounds__(kChunkThreads)
     delta_scan_rows_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Ops::mid;
+  constexpr int in = Parts<T>::in, mid = kMid, low = Parts<T>::low;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
   constexpr bool kDealt = NT == 2 && !KEEP;  // a lane's output rows of both tiles are neighbours
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kChunkThreads)
     Split<in> kc[kHold ? 1 : 2][kTileGroup][2];
     // The next block's pieces, an equal share at each of the places that call this.
     constexpr int kFirstPiece = kSteps > 1 ? kSteps / 2 : 0;
-    constexpr int kSlots = (kSteps - kFirstPiece) * kProducts<in, mid> * 4 + 6 * kProducts<mid, mid> * (KEEP ? 1 : 2);
+    constexpr int kSlots = (kSteps - kFirstPiece) * kProducts<in, mid> * 4 + 6 * (kProducts<mid, mid> + (KEEP ? 0 : kProducts<low, low>));
     int slot = 0;
     const auto piece = [&]() {
 #pragma unroll
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kChunkThreads)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               y[nt][t] = mfma(kf[ks & 1][t].p[i], bs[nt].p[j], y[nt][t]);
-              if constexpr (!KEEP) o[nt][t] = mfma(bs[nt].p[j], qf[ks & 1][t].p[i], o[nt][t]);
+              if (!KEEP && j < low && i + j < kOrder<in, low>) o[nt][t] = mfma(bs[nt].p[j], qf[ks & 1][t].p[i], o[nt][t]);
             }
             if (ks >= kFirstPiece) piece();
           }
@@ -245,13 +245,13 @@ __global__ void __launch_bounds__(kChunkThreads)
     if constexpr (KEEP) {
       store_cols<NT>(kept.U + place * kBlock * a.dv + col[0], a.dv, g, live, u);
     } else {  // outputs (scale is in P)
-      Split<mid> bu[NT][2], pf[kFrags];
+      Split<low> bu[NT][2], pf[kFrags];
 #pragma unroll
-      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<mid>(ops + Ops::p, i, lane);
+      for (int i = 0; i < kFrags; ++i) pf[i] = get_frag<low>(ops + Ops::p, i, lane);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) bu[nt][p] = split8<mid>(u[nt][p]);
+        for (int p = 0; p < 2; ++p) bu[nt][p] = split8<low>(u[nt][p]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float first = a.scale * sc.first[dealt(t, n)];
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kChunkThreads)
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        products<mid, mid>([&](int i, int j) {
+        products<low, low>([&](int i, int j) {
 #pragma unroll
           for (int t = 2 * p; t < 4; ++t) {
 #pragma unroll
@@ -348,7 +348,7 @@ using ReverseLayout = FeedLayout<T, DK, 64 * NT, (int)Ops::reverse_bytes, true>;
 template <typename T, int DK, int NT, typename Ops>
 __global__ void __launch_bounds__(kChunkThreads)
     delta_reverse_rows_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Ops::mid;
+  constexpr int in = Parts<T>::in, mid = kMid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kCols = 64 * NT;
   using L = ReverseLayout<T, DK, NT, Ops>;

@@ -106,11 +106,11 @@ struct RowOperand {
   }
 };
 
-template <typename T, int DK, int NT, int MID>
+template <typename T, int DK, int NT>
 struct SplitLds {
-  static constexpr int in = Parts<T>::in, mid = MID, kSteps = kWide<DK> / 32;
+  static constexpr int in = Parts<T>::in, mid = kMid, low = Parts<T>::low, kSteps = kWide<DK> / 32;
   static constexpr int s = 0, x = s + NT * kSteps * kStepBytes<mid>, u = x + NT * 2 * kStepBytes<mid>,
-                       ul = u + NT * 2 * kStepBytes<mid>, k = ul + NT * 2 * kStepBytes<mid>,
+                       ul = u + NT * 2 * kStepBytes<low>, k = ul + NT * 2 * kStepBytes<mid>,
                        total = k + 4 * Tile<32, in>::kBytes;
 };
 
@@ -120,11 +120,11 @@ struct SplitLds {
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_scan_split_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Ops::mid;
+  constexpr int in = Parts<T>::in, mid = kMid, low = Parts<T>::low;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;  // state tiles of a wavefront
   constexpr bool kDealt = NT == 2 && !KEEP;           // a lane's output rows of both tiles are neighbours
-  using L = SplitLds<T, DK, NT, Ops::mid>;
+  using L = SplitLds<T, DK, NT>;
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
   int item, slice;
@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   RowOperand<T, DK> K(wave), Q(wave);
   ColumnStage<T, DK> Kc(a.k_stride, owner ? tile0 >> 1 : 0);
   const typename ColumnStage<T, DK>::Columns Kt(lds + L::k + wave * Tile<32, in>::kBytes);
-  Split<mid> tf[2], pf[2];
+  Split<mid> tf[2];
+  Split<low> pf[2];
   T v[NT][4];
   // A block's scalars: of the lane's four tokens (rows of a result tile), of token dealt(wave, n), and of the block.
   // Two sets, of even and odd blocks: one is still in use when the next is asked for.
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     if constexpr (!KEEP) {
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        pf[p] = get_frag<mid>(ws + c * ws_step + Ops::p, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
+        pf[p] = get_frag<low>(ws + c * ws_step + Ops::p, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
     }
   };
   if (seq.blocks > 0) {
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
         for (int ks = 0; ks < kSteps; ++ks) {
           const Split<in> qf = Q.get(ks);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) o[nt] = mma(bs[nt][ks], qf, o[nt]);
+          for (int nt = 0; nt < NT; ++nt) o[nt] = mma(first_parts<low>(bs[nt][ks]), qf, o[nt]);
         }
       }
     }
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       put_half<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * U[nt]);
-      if constexpr (!KEEP) put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, U[nt]);
+      if constexpr (!KEEP) put_half<low>(lds + L::u + nt * 2 * kStepBytes<low>, wave >> 1, wave & 1, lane, U[nt]);
     }
     // the update's left operands, transposed
     Split<in> kc[kOwn][2];
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
         if (p <= wave / 2) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            o[nt] = mma(get_frag<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, p, lane), pf[p], o[nt]);
+            o[nt] = mma(get_frag<low>(lds + L::u + nt * 2 * kStepBytes<low>, p, lane), pf[p], o[nt]);
         }
       if (out_col < a.dv && dealt(wave, n) < rows) {
         T* dst = op + (t0 + dealt(wave, n)) * out_stride;
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 
 template <typename T, int DK, int NT, typename Ops, bool KEEP>
 hipError_t launch_scan_split(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = SplitLds<T, DK, NT, Ops::mid>;
+  using L = SplitLds<T, DK, NT>;
   constexpr auto kernel = delta_scan_split_kernel<T, DK, NT, Ops, KEEP>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
@@ -377,9 +378,9 @@ hipError_t launch_scan_split(const DeltaArgs& a, const Kept& kept, hipStream_t s
   return hipGetLastError();
 }
 
-template <typename T, int DK, int NT, int MID>
+template <typename T, int DK, int NT>
 struct ReverseSplitLds {
-  static constexpr int in = Parts<T>::in, mid = MID, kSteps = kWide<DK> / 32;
+  static constexpr int in = Parts<T>::in, mid = kMid, kSteps = kWide<DK> / 32;
   // dS; dO; e^G d; dU; -e^G beta dX
   static constexpr int s = 0, d = s + NT * kSteps * kStepBytes<mid>, df = d + NT * 2 * kStepBytes<in>,
                        u = df + NT * 2 * kStepBytes<mid>, x = u + NT * 2 * kStepBytes<mid>,
@@ -391,10 +392,10 @@ struct ReverseSplitLds {
 template <typename T, int DK, int NT, typename Ops>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_reverse_split_kernel(const DeltaArgs a, const Kept kept) {
-  constexpr int in = Parts<T>::in, mid = Ops::mid;
+  constexpr int in = Parts<T>::in, mid = kMid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;
-  using L = ReverseSplitLds<T, DK, NT, Ops::mid>;
+  using L = ReverseSplitLds<T, DK, NT>;
   extern __shared__ __align__(16) char lds[];
   const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
   int item, slice;
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 
 template <typename T, int DK, int NT, typename Ops>
 hipError_t launch_reverse_split(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ReverseSplitLds<T, DK, NT, Ops::mid>;
+  using L = ReverseSplitLds<T, DK, NT>;
   constexpr auto kernel = delta_reverse_split_kernel<T, DK, NT, Ops>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
