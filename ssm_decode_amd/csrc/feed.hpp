@@ -5,7 +5,7 @@
 // bf16 rows go straight into LDS (global_load_lds, 1 KiB per instruction, the lanes' source
 // addresses permuted as the tiles' chunks are), into the other one of two buffers: no registers
 // are held and one barrier per block is left. (One buffer and two workgroups per compute unit instead,
-// each computing while the other waits, made a block take 6.7 us where this takes about 5, and a ragged batch as
+// each computing while the other waits, made a block take a third longer, and a ragged batch as
 // long, since its longest sequence decides.) Types that are taken apart on the way, and heads of 16
 // whose tiles are wider than their rows, go through registers into a single buffer.
 #pragma once

@@ -11,8 +11,8 @@
 // The chain of a block is then 8 + 3..6 + 8 matrix instructions (dk = 128) and four exchanges. Against the
 // kernels whose wavefronts take whole rows through all products (scan_rows.hpp) it reads K, Q, T and P four
 // times as often for the same rows, so it is used where those would leave most compute units idle. Measured,
-// bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 1.17 against 1.56 ms; 24 ragged
-// sequences of 32 heads, 0.43 against 0.29 ms; the backward pass's two walks over 8 sequences of 2048 tokens and 16
+// bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 1.27 against 1.92 ms; 24 ragged
+// sequences of 32 heads, 0.48 against 0.33 ms; the backward pass's two walks over 8 sequences of 2048 tokens and 16
 // heads, 0.65 against 0.40 ms.
 #pragma once
 
