@@ -3,15 +3,15 @@
 // A workgroup takes 16 or 32 state rows of one value head (rows are independent) and its four wavefronts
 // divide every product of a block by rows of the left operand: wavefront w has the block's 16 dealt
 // tokens w for K S, T X, Q S and P U, and a quarter of the channels for the update. What a wavefront
-// reads from memory - its rows of K and Q, its fragments of T and P, its columns of K - comes straight into
-// registers and is asked for again right after its last use, a block ahead; only K's columns pass through LDS,
-// to be transposed, in a tile of the wavefront's own. The right operands (S, X, U) are exchanged through LDS in
+// reads from memory - its rows of K and Q, its fragments of T and P - comes straight into
+// registers and is asked for again right after its last use, a block ahead; K's rows then go to LDS, where
+// the wavefronts read their channels of it transposed. The right operands (S, X, U) are exchanged through LDS in
 // operand layout, 16 bytes per lane, with three barriers per block.
 //
 // The chain of a block is then 8 + 3..6 + 8 matrix instructions (dk = 128) and four exchanges. Against the
 // kernels whose wavefronts take whole rows through all products (scan_rows.hpp) it reads K, Q, T and P four
 // times as often for the same rows, so it is used where those would leave most compute units idle. Measured,
-// bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 1.27 against 1.92 ms; 24 ragged
+// bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 1.19 against 1.92 ms; 24 ragged
 // sequences of 32 heads, 0.48 against 0.33 ms; the backward pass's two walks over 8 sequences of 2048 tokens and 16
 // heads, 0.65 against 0.40 ms.
 #pragma once
@@ -104,6 +104,11 @@ struct RowOperand {
     if (!there || 32 * ks + 8 * g >= DK) x[ks].zero();
     return x[ks].split();
   }
+  // all of them, for the wavefronts that read columns of the block
+  __device__ __forceinline__ void store(const Tile<kWide<DK>, Parts<T>::in>& t) {
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) t.put(row, 4 * ks + g, get(ks));
+  }
 };
 
 template <typename T, int DK, int NT>
@@ -111,7 +116,7 @@ struct SplitLds {
   static constexpr int in = Parts<T>::in, mid = kMid, low = Parts<T>::low, kSteps = kWide<DK> / 32;
   static constexpr int s = 0, x = s + NT * kSteps * kStepBytes<mid>, u = x + NT * 2 * kStepBytes<mid>,
                        ul = u + NT * 2 * kStepBytes<low>, k = ul + NT * 2 * kStepBytes<mid>,
-                       total = k + 4 * Tile<32, in>::kBytes;
+                       total = k + Tile<kWide<DK>, in>::kBytes;
 };
 
 // With KEEP (the backward pass) it writes the state before each block and the block's corrections in place of
@@ -173,8 +178,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const int64_t ws_step = (int64_t)a.H * Ops::bytes;
 
   RowOperand<T, DK> K(wave), Q(wave);
-  ColumnStage<T, DK> Kc(a.k_stride, owner ? tile0 >> 1 : 0);
-  const typename ColumnStage<T, DK>::Columns Kt(lds + L::k + wave * Tile<32, in>::kBytes);
+  const Tile<kWide<DK>, in> Kt(lds + L::k);
   Split<mid> tf[2];
   Split<low> pf[2];
   T v[NT][4];
@@ -191,9 +195,6 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const auto ask_rows = [&](int c) {
     K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
     if constexpr (!KEEP) Q.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
-  };
-  const auto ask_columns = [&](int c) {
-    Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
   };
   const auto ask_values = [&](int c, int set) {
     const int rows = rows_of(c);
@@ -225,7 +226,6 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     ask_rows(0);
     ask_values(0, 0);
     ask_t(0);
-    ask_columns(0);
     ask_p(0);
   }
   const auto block = [&](int c, int set) {
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
         }
       }
     }
-    if (owner) Kc.store(Kt, rows);
+    K.store(Kt);
     ask_rows(next);
     ask_values(next, set ^ 1);
     __syncthreads();  // X is there
@@ -294,10 +294,9 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) kc[i][p] = Kt.template col8<true>((tile0 + i) & 1, p, lane);
+        for (int p = 0; p < 2; ++p) kc[i][p] = Kt.template col8<true>(tile0 + i, p, lane);
     }
     ask_t(next);
-    ask_columns(next);
     if constexpr (KEEP) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -384,7 +383,7 @@ struct ReverseSplitLds {
   // dS; dO; e^G d; dU; -e^G beta dX
   static constexpr int s = 0, d = s + NT * kSteps * kStepBytes<mid>, df = d + NT * 2 * kStepBytes<in>,
                        u = df + NT * 2 * kStepBytes<mid>, x = u + NT * 2 * kStepBytes<mid>,
-                       k = x + NT * 2 * kStepBytes<mid>, q = k + 4 * Tile<32, in>::kBytes,
+                       k = x + NT * 2 * kStepBytes<mid>, q = k + Tile<kWide<DK>, in>::kBytes,
                        total = q + 4 * Tile<32, in>::kBytes;
 };
 
@@ -439,9 +438,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const int64_t ws_step = (int64_t)a.H * Ops::bytes;
   const int ks_own = owner ? tile0 >> 1 : 0;
   RowOperand<T, DK> K(wave);
-  ColumnStage<T, DK> Kc(a.k_stride, ks_own), Qc(a.q_stride, ks_own);
+  ColumnStage<T, DK> Qc(a.q_stride, ks_own);
   using Columns = typename ColumnStage<T, DK>::Columns;
-  const Columns Kt(lds + L::k + wave * Columns::kBytes), Qt(lds + L::q + wave * Columns::kBytes);
+  const Tile<kWide<DK>, in> Kt(lds + L::k);
+  const Columns Qt(lds + L::q + wave * Columns::kBytes);
   Split<mid> tf[2], pf[2];
   T d[NT][4];
   f32x4 first4[2], last4[2], beta4[2];  // two sets, as in the scan
@@ -467,7 +467,6 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     whole[set] = sc->first[kBlock - 1];
   };
   const auto ask_columns = [&](int c) {
-    Kc.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
     Qc.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
   };
   const auto ask_p = [&](int c) {
@@ -528,10 +527,8 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
         x[r] = row4 + r < rows && live[nt] ? a.scale * first4[set][r] * (float)d[nt][r] : 0.f;
       put_half<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);
     }
-    if (owner) {
-      Kc.store(Kt, rows);
-      Qc.store(Qt, rows);
-    }
+    K.store(Kt);
+    if (owner) Qc.store(Qt, rows);
     ask_values(next, set ^ 1);
     K.load(kp + token(next) * a.k_stride, a.k_stride, rows_of(next));
     ask_p(next);
@@ -568,7 +565,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
           const Split<in> qc = Qt.template col8<true>((tile0 + i) & 1, p, lane);
-          kc[i][p] = Kt.template col8<true>((tile0 + i) & 1, p, lane);
+          kc[i][p] = Kt.template col8<true>(tile0 + i, p, lane);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             dS[nt][i] = mma(qc, get_frag<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, p, lane), dS[nt][i]);
