@@ -31,23 +31,22 @@ __device__ __forceinline__ int by_length(const DeltaArgs& a, int place) {
   return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.n_seqs && rank == place));
 }
 
-// Which way, and with how many state rows per workgroup: 64 or 128 by rows, 16 or 32 split.
-enum class Walk { kRows64, kRows128, kSplit16, kSplit32 };
+// Which way: by rows, with 64 or 128 state rows per workgroup, or split, with 16.
+enum class Walk { kRows64, kRows128, kSplit };
 
-// By rows once that fills most of the chip (half as many workgroups as compute units; the two ways cross between 64
-// and 256 workgroups, see scan_split.hpp), with two tiles per wavefront where there are workgroups enough, which
-// reads every left operand from LDS half as often (fp32's three parts would not fit). Split walks take 32 rows where
-// 16 would give over two workgroups per compute unit.
+// By rows once that gives three workgroups of 64 rows to four compute units (measured on both sides, see
+// scan_split.hpp), with two tiles per wavefront where there are workgroups enough, which
+// reads every left operand from LDS half as often (fp32's three parts would not fit).
 template <typename T>
 hipError_t choose_walk(const DeltaArgs& a, Walk* walk) {
   int cus = 0;
   const hipError_t e = device_cus(&cus);
   if (e != hipSuccess) return e;
   const int64_t heads = (int64_t)a.n_seqs * a.H;
-  if (2 * heads * ((a.dv + 63) / 64) >= cus)
+  if (4 * heads * ((a.dv + 63) / 64) >= 3 * cus)
     *walk = sizeof(T) == 2 && a.dv > 64 && heads * ((a.dv + 127) / 128) >= cus ? Walk::kRows128 : Walk::kRows64;
   else
-    *walk = a.dv > 16 && heads * ((a.dv + 15) / 16) > 2 * cus ? Walk::kSplit32 : Walk::kSplit16;
+    *walk = Walk::kSplit;
   return hipSuccess;
 }
 

@@ -1,19 +1,20 @@
 // The serial walk over a sequence's blocks where there are few sequences and heads.
 //
-// A workgroup takes 16 or 32 state rows of one value head (rows are independent) and its four wavefronts
+// A workgroup takes 16 state rows of one value head (rows are independent) and its four wavefronts
 // divide every product of a block by rows of the left operand: wavefront w has the block's 16 dealt
 // tokens w for K S, T X, Q S and P U, and a quarter of the channels for the update. What a wavefront
-// reads from memory - its rows of K and Q, its fragments of T and P - comes straight into
-// registers and is asked for again right after its last use, a block ahead; K's rows then go to LDS, where
-// the wavefronts read their channels of it transposed. The right operands (S, X, U) are exchanged through LDS in
-// operand layout, 16 bytes per lane, with three barriers per block.
+// reads from memory - its rows of K and Q, its fragments of T and P - comes into
+// registers and is asked for a block ahead; the rows go to LDS when the block in front is done, for the wavefront's own
+// left operands and, transposed, for everybody's channels in the update. The right operands (S, X, U) are
+// exchanged through LDS in operand layout, 16 bytes per lane, with three barriers per block.
 //
-// The chain of a block is then 8 + 3..6 + 8 matrix instructions (dk = 128) and four exchanges. Against the
+// The chain of a block is then 12 + 6..12 + 12 matrix instructions (bf16, dk = 128) and four exchanges. Against the
 // kernels whose wavefronts take whole rows through all products (scan_rows.hpp) it reads K, Q, T and P four
 // times as often for the same rows, so it is used where those would leave most compute units idle. Measured,
-// bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 1.19 against 1.92 ms; 24 ragged
-// sequences of 32 heads, 0.48 against 0.33 ms; the backward pass's two walks over 8 sequences of 2048 tokens and 16
-// heads, 0.65 against 0.40 ms.
+// bf16, 128 x 128, split against rows: one sequence of 32768 tokens, 32 heads, 0.97 against 1.92 ms; 24 ragged
+// sequences of 32 heads, 0.52 against 0.33 ms; the backward pass's two walks over 8 sequences of 2048 tokens and 16
+// heads, 0.58 against 0.40 ms. Whole calls of 4096 tokens a sequence, with 64 sequences times heads: 272 against 329 us, backward
+// 1103 against 1163; with 96: 431 against 374, backward 1663 against 1480.
 #pragma once
 
 #include "scan.hpp"
@@ -54,84 +55,54 @@ __device__ __forceinline__ void put_half(char* base, int step, int half, int lan
 template <int N>
 constexpr int kStepBytes = N * 1024;  // of one step's right operand
 
-// A wavefront's columns 32 ks .. 32 ks + 31 of a block's 64 rows: loads (16 rows of 64 bytes of a 16-bit type per
-// instruction), then stores into its own tile, from which they are read transposed.
+// A wavefront's 16 dealt rows of a block: loads of whole rows (16 segments of 64 bytes per instruction, as the
+// operands want them, made the walk a fifth longer), then stores into a tile of the block, where the
+// wavefront finds its left operands and all wavefronts find columns.
 template <typename T, int DK>
-struct ColumnStage {
-  static constexpr int kPer = 4;
-  using Columns = Tile<32, Parts<T>::in>;
+struct OwnRows {
+  static constexpr int kPer = kWide<DK> / 32, kChunks = kWide<DK> / 8, kRows = 64 / kChunks;  // rows per instruction
+  using Block = Tile<kWide<DK>, Parts<T>::in>;
   Raw8<T> x[kPer];
-  int64_t offset;
-  int row, chunk;
-  bool in;
-  __device__ __forceinline__ ColumnStage(int64_t stride, int ks) {
-    const int lane = threadIdx.x & 63;
-    row = lane >> 2;
-    chunk = lane & 3;
-    in = 32 * ks + chunk * 8 < DK;
-    offset = row * stride + (in ? 32 * ks + chunk * 8 : 0);
-  }
+  int wave, row, chunk;  // row: the lane's place among the instruction's rows
+  __device__ __forceinline__ explicit OwnRows(int w)
+      : wave(w), row((threadIdx.x & 63) / kChunks), chunk(threadIdx.x % kChunks) {}
+  __device__ __forceinline__ int at(int i) const { return dealt(wave, i * kRows + row); }
   // p: the block's first row; n rows of the block exist (others read the last one, and are zeroed on the way)
   __device__ __forceinline__ void load(const T* p, int64_t stride, int n) {
-    const int64_t edge = (int64_t)(n - 1 - row) * stride;
+    const T* q = p + (chunk * 8 < DK ? chunk * 8 : 0);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i].load(p + offset + (row + 16 * i < n ? 16 * i * stride : edge));
+    for (int i = 0; i < kPer; ++i) x[i].load(q + (int64_t)(at(i) < n ? at(i) : n - 1) * stride);
   }
-  __device__ __forceinline__ void store(const Columns& t, int n) {
+  __device__ __forceinline__ void store(const Block& t, int n) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if (!in || row + 16 * i >= n) x[i].zero();
-      t.put(row + 16 * i, chunk, x[i].split());
+      if (at(i) >= n || chunk * 8 >= DK) x[i].zero();
+      t.put(at(i), chunk, x[i].split());
     }
   }
 };
 
-// A wavefront's 16 dealt rows of a block as left operands, straight from memory.
 template <typename T, int DK>
-struct RowOperand {
-  static constexpr int kSteps = kWide<DK> / 32;
-  Raw8<T> x[kSteps];
-  int row, g;
-  bool there;  // whether the row exists in the block that was asked for
-  __device__ __forceinline__ RowOperand(int tile) : row(dealt(tile, threadIdx.x & 15)), g((threadIdx.x & 63) >> 4) {}
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int n) {
-    there = row < n;
-    const T* q = p + (int64_t)(there ? row : n - 1) * stride;
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) x[ks].load(q + (32 * ks + 8 * g < DK ? 32 * ks + 8 * g : 0));
-  }
-  __device__ __forceinline__ Split<Parts<T>::in> get(int ks) {
-    if (!there || 32 * ks + 8 * g >= DK) x[ks].zero();
-    return x[ks].split();
-  }
-  // all of them, for the wavefronts that read columns of the block
-  __device__ __forceinline__ void store(const Tile<kWide<DK>, Parts<T>::in>& t) {
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) t.put(row, 4 * ks + g, get(ks));
-  }
-};
-
-template <typename T, int DK, int NT>
 struct SplitLds {
   static constexpr int in = Parts<T>::in, mid = kMid, low = Parts<T>::low, kSteps = kWide<DK> / 32;
-  static constexpr int s = 0, x = s + NT * kSteps * kStepBytes<mid>, u = x + NT * 2 * kStepBytes<mid>,
-                       ul = u + NT * 2 * kStepBytes<low>, k = ul + NT * 2 * kStepBytes<mid>,
-                       total = k + Tile<kWide<DK>, in>::kBytes;
+  static constexpr int s = 0, x = s + kSteps * kStepBytes<mid>, u = x + 2 * kStepBytes<mid>,
+                       ul = u + 2 * kStepBytes<low>, k = ul + 2 * kStepBytes<mid>,
+                       q = k + Tile<kWide<DK>, in>::kBytes,
+                       total = q + Tile<kWide<DK>, in>::kBytes;
 };
 
 // With KEEP (the backward pass) it writes the state before each block and the block's corrections in place of
 // outputs. Outputs are computed transposed (state rows by tokens): the operands of a product can change places, and
-// a lane then holds 4 NT neighbouring state rows of one token, which it stores in one piece.
-template <typename T, int DK, int NT, typename Ops, bool KEEP>
+// a lane then holds four neighbouring state rows of one token, which it stores in one piece.
+template <typename T, int DK, typename Ops, bool KEEP>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_scan_split_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = kMid, low = Parts<T>::low;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;  // state tiles of a wavefront
-  constexpr bool kDealt = NT == 2 && !KEEP;           // a lane's output rows of both tiles are neighbours
-  using L = SplitLds<T, DK, NT>;
+  using L = SplitLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
+  const int slices = (a.dv + 15) / 16;
   int item, slice;
   item_slice(slices, &item, &slice);
   if (item >= a.n_seqs * a.H) return;
@@ -144,44 +115,37 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int hk = h / (a.H / a.Hk);
-  int col[NT];  // of the head's dv, per tile
-  bool live[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    col[nt] = 16 * NT * slice + (kDealt ? dealt(nt, n) : 16 * nt + n);
-    live[nt] = col[nt] < a.dv;
-  }
+  const int col = 16 * slice + n;  // of the head's dv
+  const bool live = col < a.dv;
   const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
   const int tile0 = wave * kOwn;  // the wavefront's state tiles; with dk <= 32 two wavefronts have none
   const bool owner = tile0 < kTiles;
 
   // S^T: a tile's rows are channels, dealt; its columns state rows
   const auto channel = [&](int tl) { return 32 * (tl >> 1) + 8 * g + 4 * (tl & 1); };
-  f32x4 S[NT][kOwn];
+  f32x4 S[kOwn];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      S[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int c = channel(tile0 + i);
-      if (owner && a.S0 != nullptr && live[nt] && c < DK) S[nt][i] = ld4(a.S0 + state + (int64_t)col[nt] * DK + c);
-      if (owner) put_half<mid>(lds + L::s + nt * kSteps * kStepBytes<mid>, (tile0 + i) >> 1, (tile0 + i) & 1, lane, S[nt][i]);
-    }
+  for (int i = 0; i < kOwn; ++i) {
+    S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int c = channel(tile0 + i);
+    if (owner && a.S0 != nullptr && live && c < DK) S[i] = ld4(a.S0 + state + (int64_t)col * DK + c);
+    if (owner) put_half<mid>(lds + L::s, (tile0 + i) >> 1, (tile0 + i) & 1, lane, S[i]);
+  }
 
   const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
   const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
   const T* vp = static_cast<const T*>(a.v) + (int64_t)h * a.dv;
   const int64_t out_stride = (int64_t)a.H * a.dv;
-  const int out_col = 16 * NT * slice + 4 * NT * g;  // the first of the lane's neighbouring output rows
+  const int out_col = 16 * slice + 4 * g;  // the first of the lane's neighbouring output rows
   T* op = static_cast<T*>(a.out) + (int64_t)h * a.dv + out_col;
   const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
   const int64_t ws_step = (int64_t)a.H * Ops::bytes;
 
-  RowOperand<T, DK> K(wave), Q(wave);
-  const Tile<kWide<DK>, in> Kt(lds + L::k);
+  OwnRows<T, DK> K(wave), Q(wave);
+  const typename OwnRows<T, DK>::Block Kt(lds + L::k), Qt(lds + L::q);
   Split<mid> tf[2];
   Split<low> pf[2];
-  T v[NT][4];
+  T v[4];
   // A block's scalars: of the lane's four tokens (rows of a result tile), of token dealt(wave, n), and of the block.
   // Two sets, of even and odd blocks: one is still in use when the next is asked for.
   f32x4 first4[2], last4[2];
@@ -201,8 +165,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const T* p = vp + (token(c) + (row4 + r < rows ? row4 + r : rows - 1)) * a.v_stride;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) v[nt][r] = p[live[nt] ? col[nt] : 0];
+      v[r] = p[live ? col : 0];
     }
     const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
     first4[set] = ld4(sc->first + row4);
@@ -222,11 +185,16 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
         pf[p] = get_frag<low>(ws + c * ws_step + Ops::p, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
     }
   };
+  const auto put_rows = [&](int c) {
+    K.store(Kt, rows_of(c));
+    if constexpr (!KEEP) Q.store(Qt, rows_of(c));
+  };
   if (seq.blocks > 0) {
     ask_rows(0);
     ask_values(0, 0);
     ask_t(0);
     ask_p(0);
+    put_rows(0);
   }
   const auto block = [&](int c, int set) {
     const int rows = rows_of(c);
@@ -235,59 +203,40 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     // by moves, and a move waits for the load right where it was asked for.)
     const int next = c + 1 < seq.blocks ? c + 1 : c;
     const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    __syncthreads();  // S is there; the block before has been read
-    f32x4 y[NT], o[NT];
+    const int own = dealt(wave, n);
+    Split<in> kf[kSteps];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) y[nt] = o[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ks = 0; ks < kSteps; ++ks) kf[ks] = Kt.row8(own, ks, g);  // (the wavefront's own)
+    __syncthreads();  // S and K are there
+    ask_rows(next);  // (asked for after Q S, a block took 0.2 us longer)
+    f32x4 y = {0.f, 0.f, 0.f, 0.f}, o = y;
     {
-      Split<mid> bs[NT][kSteps];
+      Split<mid> bs[kSteps];
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks)
+      for (int ks = 0; ks < kSteps; ++ks) bs[ks] = get_frag<mid>(lds + L::s, ks, lane);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          bs[nt][ks] = get_frag<mid>(lds + L::s + nt * kSteps * kStepBytes<mid>, ks, lane);
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {
-        const Split<in> kf = K.get(ks);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) y[nt] = mma(kf, bs[nt][ks], y[nt]);
-      }
+      for (int ks = 0; ks < kSteps; ++ks) y = mma(kf[ks], bs[ks], y);
       // (the chain goes on from y; Q S fills the time of its exchange)
+      f32x4 x;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f32x4 x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = (row4 + r < rows && live[nt] ? (float)v[nt][r] : 0.f) - first4[set][r] * y[nt][r];
-        put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);  // (beta is in T's columns)
-      }
+      for (int r = 0; r < 4; ++r) x[r] = (row4 + r < rows && live ? (float)v[r] : 0.f) - first4[set][r] * y[r];
+      put_half<mid>(lds + L::x, wave >> 1, wave & 1, lane, x);  // (beta is in T's columns)
       if constexpr (!KEEP) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
-          const Split<in> qf = Q.get(ks);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) o[nt] = mma(first_parts<low>(bs[nt][ks]), qf, o[nt]);
+          const Split<in> qf = Qt.row8(own, ks, g);
+          o = mma(first_parts<low>(bs[ks]), qf, o);
         }
       }
     }
-    K.store(Kt);
-    ask_rows(next);
     ask_values(next, set ^ 1);
     __syncthreads();  // X is there
-    f32x4 U[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) U[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 U = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 0; p < 2; ++p)
-      if (p <= wave / 2) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          U[nt] = mma(tf[p], get_frag<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, p, lane), U[nt]);
-      }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      put_half<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * U[nt]);
-      if constexpr (!KEEP) put_half<low>(lds + L::u + nt * 2 * kStepBytes<low>, wave >> 1, wave & 1, lane, U[nt]);
-    }
+      if (p <= wave / 2) U = mma(tf[p], get_frag<mid>(lds + L::x, p, lane), U);
+    put_half<mid>(lds + L::ul, wave >> 1, wave & 1, lane, last4[set] * U);
+    if constexpr (!KEEP) put_half<low>(lds + L::u, wave >> 1, wave & 1, lane, U);
     // the update's left operands, transposed
     Split<in> kc[kOwn][2];
     if (owner) {
@@ -297,58 +246,39 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
         for (int p = 0; p < 2; ++p) kc[i][p] = Kt.template col8<true>(tile0 + i, p, lane);
     }
     ask_t(next);
-    if constexpr (KEEP) {
+    if (KEEP && live) {
+      if (owner) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        if (live[nt]) {
-          if (owner) {
+        for (int i = 0; i < kOwn; ++i)
+          if (channel(tile0 + i) < DK) st4(kept.S + (place * a.dv + col) * DK + channel(tile0 + i), S[i]);
+      }
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-              if (channel(tile0 + i) < DK)
-                st4(kept.S + (place * a.dv + col[nt]) * DK + channel(tile0 + i), S[nt][i]);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) kept.U[(place * kBlock + row4 + r) * a.dv + col[nt]] = U[nt][r];
-        }
+      for (int r = 0; r < 4; ++r) kept.U[(place * kBlock + row4 + r) * a.dv + col] = U[r];
     }
     __syncthreads();  // U is there
     if (owner) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < kOwn; ++i) S[i] *= whole[set];
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) S[nt][i] *= whole[set];
+      for (int p = 0; p < 2; ++p) {
+        const Split<mid> ul = get_frag<mid>(lds + L::ul, p, lane);
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+        for (int i = 0; i < kOwn; ++i) S[i] = mma(kc[i][p], ul, S[i]);
+      }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Split<mid> ul = get_frag<mid>(lds + L::ul + nt * 2 * kStepBytes<mid>, p, lane);
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) S[nt][i] = mma(kc[i][p], ul, S[nt][i]);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-          put_half<mid>(lds + L::s + nt * kSteps * kStepBytes<mid>, (tile0 + i) >> 1, (tile0 + i) & 1, lane, S[nt][i]);
+      for (int i = 0; i < kOwn; ++i)
+        put_half<mid>(lds + L::s, (tile0 + i) >> 1, (tile0 + i) & 1, lane, S[i]);
     }
+    put_rows(next);  // (the update's operands have been read)
     if constexpr (!KEEP) {  // (scale is in P)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) o[nt] *= a.scale * first1[set];
+      o *= a.scale * first1[set];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        if (p <= wave / 2) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            o[nt] = mma(get_frag<low>(lds + L::u + nt * 2 * kStepBytes<low>, p, lane), pf[p], o[nt]);
-        }
+        if (p <= wave / 2) o = mma(get_frag<low>(lds + L::u, p, lane), pf[p], o);
       if (out_col < a.dv && dealt(wave, n) < rows) {
         T* dst = op + (t0 + dealt(wave, n)) * out_stride;
-        if constexpr (NT == 2) {
-          store8(dst, join(o[0], o[1]));
-        } else {
-          typedef T vec __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<vec*>(dst) = __builtin_convertvector(o[0], vec);
-        }
+        typedef T vec __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<vec*>(dst) = __builtin_convertvector(o, vec);
       }
       ask_p(next);
     }
@@ -359,44 +289,42 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   }
   if (a.S_out == nullptr || KEEP || !owner) return;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (live[nt] && channel(tile0 + i) < DK)
-        st4(a.S_out + state + (int64_t)col[nt] * DK + channel(tile0 + i), S[nt][i]);
+  for (int i = 0; i < kOwn; ++i)
+    if (live && channel(tile0 + i) < DK)
+      st4(a.S_out + state + (int64_t)col * DK + channel(tile0 + i), S[i]);
 }
 
-template <typename T, int DK, int NT, typename Ops, bool KEEP>
+template <typename T, int DK, typename Ops, bool KEEP>
 hipError_t launch_scan_split(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = SplitLds<T, DK, NT>;
-  constexpr auto kernel = delta_scan_split_kernel<T, DK, NT, Ops, KEEP>;
+  using L = SplitLds<T, DK>;
+  constexpr auto kernel = delta_scan_split_kernel<T, DK, Ops, KEEP>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
+  const int slices = (a.dv + 15) / 16;
   kernel<<<dim3((unsigned)item_grid((int64_t)a.n_seqs * a.H, slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
   return hipGetLastError();
 }
 
-template <typename T, int DK, int NT>
+template <typename T, int DK>
 struct ReverseSplitLds {
   static constexpr int in = Parts<T>::in, mid = kMid, kSteps = kWide<DK> / 32;
   // dS; dO; e^G d; dU; -e^G beta dX
-  static constexpr int s = 0, d = s + NT * kSteps * kStepBytes<mid>, df = d + NT * 2 * kStepBytes<in>,
-                       u = df + NT * 2 * kStepBytes<mid>, x = u + NT * 2 * kStepBytes<mid>,
-                       k = x + NT * 2 * kStepBytes<mid>, q = k + Tile<kWide<DK>, in>::kBytes,
-                       total = q + 4 * Tile<32, in>::kBytes;
+  static constexpr int s = 0, d = s + kSteps * kStepBytes<mid>, df = d + 2 * kStepBytes<in>,
+                       u = df + 2 * kStepBytes<mid>, x = u + 2 * kStepBytes<mid>,
+                       k = x + 2 * kStepBytes<mid>, q = k + Tile<kWide<DK>, in>::kBytes,
+                       total = q + Tile<kWide<DK>, in>::kBytes;
 };
 
 // The scan's division of labour, from the last block to the first.
-template <typename T, int DK, int NT, typename Ops>
+template <typename T, int DK, typename Ops>
 __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     delta_reverse_split_kernel(const DeltaArgs a, const Kept kept) {
   constexpr int in = Parts<T>::in, mid = kMid;
   constexpr int kSteps = kWide<DK> / 32, kTiles = 2 * kSteps;
   constexpr int kOwn = kTiles >= 4 ? kTiles / 4 : 1;
-  using L = ReverseSplitLds<T, DK, NT>;
+  using L = ReverseSplitLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
+  const int slices = (a.dv + 15) / 16;
   int item, slice;
   item_slice(slices, &item, &slice);
   if (item >= a.n_seqs * a.H) return;
@@ -406,29 +334,21 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int hk = h / (a.H / a.Hk);
-  int col[NT];
-  bool live[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    col[nt] = 16 * NT * slice + 16 * nt + n;
-    live[nt] = col[nt] < a.dv;
-  }
+  const int col = 16 * slice + n;
+  const bool live = col < a.dv;
   const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
   const int tile0 = wave * kOwn;
   const bool owner = tile0 < kTiles;
   const auto channel = [&](int tl) { return 32 * (tl >> 1) + 8 * g + 4 * (tl & 1); };
-  const auto s_frags = [&](int nt) { return lds + L::s + nt * kSteps * kStepBytes<mid>; };
-  f32x4 dS[NT][kOwn];  // transposed, as S in the scan
+  char* const s_frags = lds + L::s;
+  f32x4 dS[kOwn];  // transposed, as S in the scan
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      dS[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int c = channel(tile0 + i);
-      if (owner && a.dS_out != nullptr && live[nt] && c < DK)
-        dS[nt][i] = ld4(a.dS_out + state + (int64_t)col[nt] * DK + c);
-      if (owner) put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
-    }
+  for (int i = 0; i < kOwn; ++i) {
+    dS[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int c = channel(tile0 + i);
+    if (owner && a.dS_out != nullptr && live && c < DK) dS[i] = ld4(a.dS_out + state + (int64_t)col * DK + c);
+    if (owner) put_half<mid>(s_frags, (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[i]);
+  }
 
   const T* kp = static_cast<const T*>(a.k) + (int64_t)hk * DK;
   const T* qp = static_cast<const T*>(a.q) + (int64_t)hk * DK;
@@ -436,14 +356,10 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   const T* dop = static_cast<const T*>(a.dout) + (int64_t)h * a.dv;
   const char* ws = static_cast<const char*>(a.ws) + ((int64_t)seq.block0 * a.H + h) * Ops::bytes;
   const int64_t ws_step = (int64_t)a.H * Ops::bytes;
-  const int ks_own = owner ? tile0 >> 1 : 0;
-  RowOperand<T, DK> K(wave);
-  ColumnStage<T, DK> Qc(a.q_stride, ks_own);
-  using Columns = typename ColumnStage<T, DK>::Columns;
-  const Tile<kWide<DK>, in> Kt(lds + L::k);
-  const Columns Qt(lds + L::q + wave * Columns::kBytes);
+  OwnRows<T, DK> K(wave), Q(wave);
+  const typename OwnRows<T, DK>::Block Kt(lds + L::k), Qt(lds + L::q);
   Split<mid> tf[2], pf[2];
-  T d[NT][4];
+  T d[4];
   f32x4 first4[2], last4[2], beta4[2];  // two sets, as in the scan
   float whole[2];
   const int row4 = dealt(wave, 4 * g);
@@ -457,8 +373,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const T* p = dop + (token(c) + (row4 + r < rows ? row4 + r : rows - 1)) * do_stride;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) d[nt][r] = p[live[nt] ? col[nt] : 0];
+      d[r] = p[live ? col : 0];
     }
     const BlockScalars* sc = reinterpret_cast<const BlockScalars*>(ws + c * ws_step + Ops::scalars);
     first4[set] = ld4(sc->first + row4);
@@ -466,8 +381,13 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     beta4[set] = ld4(sc->beta + row4);
     whole[set] = sc->first[kBlock - 1];
   };
-  const auto ask_columns = [&](int c) {
-    Qc.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
+  const auto ask_rows = [&](int c) {
+    K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
+    Q.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
+  };
+  const auto put_rows = [&](int c) {
+    K.store(Kt, rows_of(c));
+    Q.store(Qt, rows_of(c));
   };
   const auto ask_p = [&](int c) {
 #pragma unroll
@@ -479,122 +399,101 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     for (int p = 0; p < 2; ++p)
       tf[p] = get_frag<mid>(ws + c * ws_step + Ops::tt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
   };
-  const auto d_frags = [&](int nt) { return lds + L::d + nt * 2 * kStepBytes<in>; };
+  char* const d_frags = lds + L::d;
   // dO of the block that was asked for, as an operand
   const auto put_values = [&](int c) {
     const int rows = rows_of(c);
+    f32x4 x;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      f32x4 x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = row4 + r < rows && live[nt] ? (float)d[nt][r] : 0.f;
-      put_half<in>(d_frags(nt), wave >> 1, wave & 1, lane, x);  // exact
-    }
+    for (int r = 0; r < 4; ++r) x[r] = row4 + r < rows && live ? (float)d[r] : 0.f;
+    put_half<in>(d_frags, wave >> 1, wave & 1, lane, x);  // exact
   };
   if (seq.blocks > 0) {
     const int c = seq.blocks - 1;
     ask_values(c, 0);
-    K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
+    ask_rows(c);
     ask_p(c);
     ask_t(c);
-    ask_columns(c);
     put_values(c);
+    put_rows(c);
   }
   const auto block = [&](int c, int set) {
     const int rows = rows_of(c);
     const int next = c > 0 ? c - 1 : 0;  // (loads under no condition, as in the scan)
     const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
-    __syncthreads();  // dS and dO are there
-    f32x4 y[NT], w[NT];
+    Split<in> kf[kSteps];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      y[nt] = w[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ks = 0; ks < kSteps; ++ks) kf[ks] = Kt.row8(dealt(wave, n), ks, g);  // (the wavefront's own)
+    __syncthreads();  // dS, dO, K and Q are there
+    ask_rows(next);
+    f32x4 y = {0.f, 0.f, 0.f, 0.f}, w = y;
+    {
       Split<mid> bs[kSteps];
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) bs[ks] = get_frag<mid>(s_frags(nt), ks, lane);
+      for (int ks = 0; ks < kSteps; ++ks) bs[ks] = get_frag<mid>(s_frags, ks, lane);
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        if (p >= wave / 2) w[nt] = mma(pf[p], get_frag<in>(d_frags(nt), p, lane), w[nt]);
+        if (p >= wave / 2) w = mma(pf[p], get_frag<in>(d_frags, p, lane), w);
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) y[nt] = mma(K.get(ks), bs[ks], y[nt]);
+      for (int ks = 0; ks < kSteps; ++ks) y = mma(kf[ks], bs[ks], y);
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      put_half<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, last4[set] * y[nt] + a.scale * w[nt]);
+    {
+      put_half<mid>(lds + L::u, wave >> 1, wave & 1, lane, last4[set] * y + a.scale * w);
       f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        x[r] = row4 + r < rows && live[nt] ? a.scale * first4[set][r] * (float)d[nt][r] : 0.f;
-      put_half<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, x);
+        x[r] = row4 + r < rows && live ? a.scale * first4[set][r] * (float)d[r] : 0.f;
+      put_half<mid>(lds + L::df, wave >> 1, wave & 1, lane, x);
     }
-    K.store(Kt);
-    if (owner) Qc.store(Qt, rows);
     ask_values(next, set ^ 1);
-    K.load(kp + token(next) * a.k_stride, a.k_stride, rows_of(next));
     ask_p(next);
     // the gradient of the state after the block
     if (owner) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-          if (live[nt] && channel(tile0 + i) < DK)
-            st4(kept.dS + (place * a.dv + col[nt]) * DK + channel(tile0 + i), dS[nt][i]);
+      for (int i = 0; i < kOwn; ++i)
+        if (live && channel(tile0 + i) < DK)
+          st4(kept.dS + (place * a.dv + col) * DK + channel(tile0 + i), dS[i]);
     }
     __syncthreads();  // dU and e^G d are there
-    f32x4 dX[NT];
+    f32x4 dX = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      dX[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (p >= wave / 2) dX[nt] = mma(tf[p], get_frag<mid>(lds + L::u + nt * 2 * kStepBytes<mid>, p, lane), dX[nt]);
-      put_half<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, wave >> 1, wave & 1, lane, -first4[set] * beta4[set] * dX[nt]);
-    }
+    for (int p = 0; p < 2; ++p)
+      if (p >= wave / 2) dX = mma(tf[p], get_frag<mid>(lds + L::u, p, lane), dX);
+    put_half<mid>(lds + L::x, wave >> 1, wave & 1, lane, -first4[set] * beta4[set] * dX);
     ask_t(next);
-    ask_columns(next);
     // (Q's part of the update fills the time of the exchange)
     Split<in> kc[kOwn][2];
     if (owner) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) dS[nt][i] *= whole[set];
+      for (int i = 0; i < kOwn; ++i) dS[i] *= whole[set];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
-          const Split<in> qc = Qt.template col8<true>((tile0 + i) & 1, p, lane);
+          const Split<in> qc = Qt.template col8<true>(tile0 + i, p, lane);
           kc[i][p] = Kt.template col8<true>(tile0 + i, p, lane);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            dS[nt][i] = mma(qc, get_frag<mid>(lds + L::df + nt * 2 * kStepBytes<mid>, p, lane), dS[nt][i]);
+          dS[i] = mma(qc, get_frag<mid>(lds + L::df, p, lane), dS[i]);
         }
       }
     }
+    if (live) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (live[nt]) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) kept.dX[(place * kBlock + row4 + r) * a.dv + col[nt]] = dX[nt][r];
-      }
+      for (int r = 0; r < 4; ++r) kept.dX[(place * kBlock + row4 + r) * a.dv + col] = dX[r];
+    }
     __syncthreads();  // dX is there
     if (owner) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < 2; ++p) {
+        const Split<mid> bx = get_frag<mid>(lds + L::x, p, lane);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const Split<mid> bx = get_frag<mid>(lds + L::x + nt * 2 * kStepBytes<mid>, p, lane);
+        for (int i = 0; i < kOwn; ++i) dS[i] = mma(kc[i][p], bx, dS[i]);
+      }
 #pragma unroll
-          for (int i = 0; i < kOwn; ++i) dS[nt][i] = mma(kc[i][p], bx, dS[nt][i]);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-          put_half<mid>(s_frags(nt), (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[nt][i]);
+      for (int i = 0; i < kOwn; ++i)
+        put_half<mid>(s_frags, (tile0 + i) >> 1, (tile0 + i) & 1, lane, dS[i]);
     }
     put_values(next);
+    put_rows(next);  // (the update's operands have been read)
   };
   for (int c = seq.blocks - 1; c >= 0; c -= 2) {
     block(c, 0);
@@ -602,20 +501,18 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   }
   if (a.dS0 == nullptr || !owner) return;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
     for (int i = 0; i < kOwn; ++i)
-      if (live[nt] && channel(tile0 + i) < DK)
-        st4(a.dS0 + state + (int64_t)col[nt] * DK + channel(tile0 + i), dS[nt][i]);
+      if (live && channel(tile0 + i) < DK)
+        st4(a.dS0 + state + (int64_t)col * DK + channel(tile0 + i), dS[i]);
 }
 
-template <typename T, int DK, int NT, typename Ops>
+template <typename T, int DK, typename Ops>
 hipError_t launch_reverse_split(const DeltaArgs& a, const Kept& kept, hipStream_t s) {
-  using L = ReverseSplitLds<T, DK, NT>;
-  constexpr auto kernel = delta_reverse_split_kernel<T, DK, NT, Ops>;
+  using L = ReverseSplitLds<T, DK>;
+  constexpr auto kernel = delta_reverse_split_kernel<T, DK, Ops>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total);
   if (e != hipSuccess) return e;
-  const int slices = (a.dv + 16 * NT - 1) / (16 * NT);
+  const int slices = (a.dv + 15) / 16;
   kernel<<<dim3((unsigned)item_grid((int64_t)a.n_seqs * a.H, slices)), dim3(kChunkThreads), L::total, s>>>(a, kept);
   return hipGetLastError();
 }
