@@ -76,7 +76,7 @@ class Delta:
                 f64(self.beta[a:b, h]), S0, self.scale), slice(a, b), hk
 
     # What the kernels may be off by, relative to the terms' magnitudes. Every product that takes a
-    # computed operand rounds it to two bf16 parts (2^-18) and leaves out one product of parts
+    # computed operand rounds it to two bf16 parts or more (2^-18) and leaves out one product of parts
     # (2^-18); a state passes four such products per block (K S, T X, the update, and the carried
     # state's own earlier ones): 8 * 2^-18. fp32 inputs take three parts (2^-24 in place of 2^-18), where
     # the fp32 sums over up to 128 terms dominate: 64 * 2^-24.
