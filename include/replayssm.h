@@ -560,8 +560,8 @@ int replayssm_delta_sizes(const replayssm_delta_config* cfg, int64_t* forward_by
  * cu_tokens, cu_blocks, block_seq). out as above; S_out [n_seqs][H][dv][dk] receives
  * the states after the last tokens (S0 for an empty sequence; NULL: not wanted; may be S0).
  * workspace: forward_bytes of replayssm_delta_sizes, free again when the call's work is done. A
- * sequence whose tables contradict each other or leave the arrays is skipped and
- * REPLAYSSM_DEVERR_RANGE set in err. Results do not depend on what else is in the batch. */
+ * sequence whose tables contradict each other or leave the arrays is skipped (out and S_out are left as
+ * they were) and REPLAYSSM_DEVERR_RANGE set in err. Results do not depend on what else is in the batch. */
 int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
                            const void* k, const void* v, const float* g, const float* beta, const float* S0,
                            void* out, float* S_out, void* workspace, int32_t* err, void* stream);
@@ -573,7 +573,8 @@ int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ra
  * The inputs, tables and S0 are those of the forward call; states are computed again, so nothing
  * of the forward call's workspace is needed. workspace: backward_bytes of replayssm_delta_sizes.
  * Sums have a fixed order: equal calls give equal bits. Rows of tokens that no sequence holds are
- * left as they were; a sequence with bad tables is skipped and flagged as in the forward call. */
+ * left as they were; a sequence with bad tables is skipped, all of its gradients left as they were, and
+ * flagged as in the forward call. */
 int replayssm_delta_prompt_backward(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
                                     const void* k, const void* v, const float* g, const float* beta, const float* S0,
                                     const void* dout, const float* dS_out, void* dq, void* dk, void* dv, float* dg,

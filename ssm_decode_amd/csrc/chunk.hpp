@@ -20,7 +20,7 @@
 #pragma once
 
 #include "element.hpp"
-#include "prompt.hpp"
+#include "sequences.hpp"
 
 namespace rs {
 
@@ -356,29 +356,10 @@ struct BlockScalars {
   float first[kBlock];
   float last[kBlock];
   float beta[kBlock];
-  float unused[kBlock];
+  uint32_t ready[kBlock];  // backward: [0] is nonzero while the block is good, see owns
 };
 
 // A log decay that can be summed: e^-1e4 is 0 in fp32 as e^-infinity is, and later differences stay whole. (NaN stays.)
 __device__ __forceinline__ float closed_gate(float g) { return g < -1e4f ? -1e4f : g; }
-
-// A sequence's place in the packed batch; ok = false where the tables contradict each other or
-// leave the arrays (nothing of the sequence is touched then).
-struct SeqRange {
-  int begin, end, block0, blocks;
-  bool ok;
-};
-__device__ __forceinline__ SeqRange seq_range(const DeltaArgs& a, int s) {
-  SeqRange r;
-  r.begin = a.cu_tokens[s];
-  r.end = a.cu_tokens[s + 1];
-  r.block0 = a.cu_blocks[s];
-  const int block1 = a.cu_blocks[s + 1];
-  r.ok = r.begin >= 0 && r.end >= r.begin && (int64_t)r.end <= a.n_tokens && r.block0 >= 0 && block1 >= r.block0 &&
-         block1 <= a.max_blocks;
-  r.blocks = r.ok ? block1 - r.block0 : 0;
-  if (r.ok && r.blocks != (int)(((int64_t)r.end - r.begin + kBlock - 1) / kBlock)) r.ok = false;
-  return r;
-}
 
 }  // namespace rs

@@ -33,6 +33,13 @@ struct BackwardBlock {
   static constexpr int64_t reverse_bytes = bytes - scalars;   // and the reverse scan, from the scalars
 };
 
+// Whether `prepare` has written block b and the scan has not skipped its sequence (the same for every head).
+__device__ __forceinline__ bool block_ready(const DeltaArgs& a, int b, int h) {
+  const char* ops = static_cast<const char*>(a.ws) + ((int64_t)b * a.H + h) * BackwardBlock::bytes;
+  const uint32_t ready = reinterpret_cast<const BlockScalars*>(ops + BackwardBlock::scalars)->ready[0];
+  return b < a.cu_blocks[a.n_seqs] && ready != 0;
+}
+
 // The gradients kernel walks the state rows in slices of 32 (one MFMA step over dv), then needs
 // q, k and the two 64 x 64 matrices Y and M: the two sets share their LDS, and two workgroups a compute unit.
 template <typename T, int DK>
@@ -65,7 +72,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
   using Ops = BackwardBlock;
   extern __shared__ __align__(16) char lds[];
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
-  if (b >= a.cu_blocks[a.n_seqs]) return;
+  if (!block_ready(a, b, h)) return;
   const int s = a.block_seq[b];
   if (s < 0 || s >= a.n_seqs) return;  // (flagged by prepare)
   const SeqRange seq = seq_range(a, s);
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
 template <typename T>
 __global__ void __launch_bounds__(256) delta_share_kernel(const DeltaArgs a, const float* dq_part, const float* dk_part) {
   const int b = blockIdx.x;
-  if (b >= a.cu_blocks[a.n_seqs]) return;
+  if (!block_ready(a, b, 0)) return;
   const int s = a.block_seq[b];
   if (s < 0 || s >= a.n_seqs) return;
   const SeqRange seq = seq_range(a, s);

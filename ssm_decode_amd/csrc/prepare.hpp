@@ -100,8 +100,10 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
     seq = seq_range(a, s);
     ok = seq.ok && b >= seq.block0 && b < seq.block0 + seq.blocks;
   }
+  char* out = static_cast<char*>(a.ws) + ((int64_t)b * a.H + h) * Out::bytes;
   if (!ok) {
     if (threadIdx.x == 0 && h == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
+    if (Out::backward && threadIdx.x == 0) reinterpret_cast<BlockScalars*>(out + Out::scalars)->ready[0] = 0;
     return;
   }
   const int64_t t0 = (int64_t)seq.begin + (int64_t)(b - seq.block0) * kBlock;
@@ -118,7 +120,6 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
   float* Tm = reinterpret_cast<float*>(lds + L::t);
   double* G = reinterpret_cast<double*>(lds + L::g);
   float* beta = reinterpret_cast<float*>(lds + L::beta);
-  char* out = static_cast<char*>(a.ws) + ((int64_t)b * a.H + h) * Out::bytes;
   if (DK < 32) {
     zero_tile(K);
     zero_tile(Q);
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
     sc->first[lane] = expf((float)sum);
     sc->last[lane] = expf((float)(end - sum));
     sc->beta[lane] = bt;
+    if (Out::backward && lane == 0) sc->ready[0] = 1;
   }
   ks.store(K);
   qs.store(Q);

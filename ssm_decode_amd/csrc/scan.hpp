@@ -16,6 +16,20 @@ struct Kept {
   float* dX;
 };
 
+// A walk that skips its sequence says so: the call's error word, and (backward) the blocks that `prepare` took for
+// good. One workgroup per value head does it.
+template <typename Ops>
+__device__ __forceinline__ void skip_sequence(const DeltaArgs& a, int s, const SeqRange& r, int h) {
+  if (threadIdx.x == 0 && h == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
+  if constexpr (Ops::backward) {
+    for (int c = threadIdx.x; c < r.blocks; c += kChunkThreads) {
+      const int64_t b = r.block0 + c;
+      if (a.block_seq[b] == s)
+        reinterpret_cast<BlockScalars*>(static_cast<char*>(a.ws) + (b * a.H + h) * Ops::bytes + Ops::scalars)->ready[0] = 0;
+    }
+  }
+}
+
 // The place-th longest sequence. Workgroups start in index order, and a long sequence that starts last is
 // finished last; with over 64 sequences the heads of many are in flight and short ones fill the gaps,
 // so those keep their order.

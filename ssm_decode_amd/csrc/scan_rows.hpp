@@ -97,6 +97,10 @@ __global__ void __launch_bounds__(kChunkThreads)
   const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
   StateTiles<DK, NT> S;
   S.load(a.S0 == nullptr ? nullptr : a.S0 + state, col, live, g);
+  if (!owns(a, s, seq)) {  // (before the first copy into LDS, which has to land before its workgroup ends)
+    if (slice == 0) skip_sequence<Ops>(a, s, seq, h);
+    return;
+  }
 
   const int64_t out_stride = (int64_t)a.H * a.dv;
   // the first of the lane's 4 NT neighbouring output rows
@@ -373,6 +377,7 @@ __global__ void __launch_bounds__(kChunkThreads)
   const int64_t state = ((int64_t)s * a.H + h) * a.dv * DK;
   StateTiles<DK, NT> dS;
   dS.load(a.dS_out == nullptr ? nullptr : a.dS_out + state, col, live, g);
+  if (!owns(a, s, seq)) return;
 
   FeedSource<T> src;
   src.k = static_cast<const T*>(a.k) + (int64_t)hk * DK;

@@ -194,8 +194,12 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     ask_values(0, 0);
     ask_t(0);
     ask_p(0);
-    put_rows(0);
   }
+  if (!owns(a, s, seq)) {
+    if (slice == 0) skip_sequence<Ops>(a, s, seq, h);
+    return;
+  }
+  if (seq.blocks > 0) put_rows(0);
   const auto block = [&](int c, int set) {
     const int rows = rows_of(c);
     const int64_t t0 = token(c);
@@ -409,13 +413,15 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     put_half<in>(d_frags, wave >> 1, wave & 1, lane, x);  // exact
   };
   if (seq.blocks > 0) {
-    const int c = seq.blocks - 1;
-    ask_values(c, 0);
-    ask_rows(c);
-    ask_p(c);
-    ask_t(c);
-    put_values(c);
-    put_rows(c);
+    ask_values(seq.blocks - 1, 0);
+    ask_rows(seq.blocks - 1);
+    ask_p(seq.blocks - 1);
+    ask_t(seq.blocks - 1);
+  }
+  if (!owns(a, s, seq)) return;
+  if (seq.blocks > 0) {
+    put_values(seq.blocks - 1);
+    put_rows(seq.blocks - 1);
   }
   const auto block = [&](int c, int set) {
     const int rows = rows_of(c);
