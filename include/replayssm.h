@@ -544,8 +544,9 @@ typedef struct replayssm_delta_config {
  * [n_seqs] int32 within a pool of n_slots states, or NULL for slots[i] = i. A negative slot
  * is a padded entry and skipped. A slot >= n_slots and every further sequence on a slot that an
  * earlier one names are skipped and set REPLAYSSM_DEVERR_INDEX; offsets cu_tokens [n_seqs + 1]
- * that fall or leave 0..n_tokens skip their sequence and set REPLAYSSM_DEVERR_RANGE. Slots
- * that no sequence names are left as they were. */
+ * that fall or leave 0..n_tokens skip their sequence and set REPLAYSSM_DEVERR_RANGE. (Behind offsets
+ * that fell, two sequences may hold the same tokens: both states come out right, and those tokens' rows of
+ * out from either.) Slots that no sequence names are left as they were. */
 int replayssm_delta_step(const replayssm_delta_config* cfg, const int32_t* cu_tokens, const int32_t* slots,
                          int n_slots, const void* q, const void* k, const void* v, const float* g,
                          const float* beta, const float* S_in, float* S_out, void* out, int32_t* err,
@@ -560,8 +561,11 @@ int replayssm_delta_sizes(const replayssm_delta_config* cfg, int64_t* forward_by
  * cu_tokens, cu_blocks, block_seq). out as above; S_out [n_seqs][H][dv][dk] receives
  * the states after the last tokens (S0 for an empty sequence; NULL: not wanted; may be S0).
  * workspace: forward_bytes of replayssm_delta_sizes, free again when the call's work is done. A
- * sequence whose tables contradict each other or leave the arrays is skipped (out and S_out are left as
- * they were) and REPLAYSSM_DEVERR_RANGE set in err. Results do not depend on what else is in the batch. */
+ * sequence whose tables contradict each other (offsets that fall, another number of blocks than its
+ * tokens make, a block that block_seq does not give to it) or leave the arrays is skipped (out and S_out are
+ * left as they were) and REPLAYSSM_DEVERR_RANGE set in err. Tokens that two sequences hold, behind offsets
+ * that fell, are taken by both, and their rows of out come from either. Results do not depend on what else
+ * is in the batch. */
 int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
                            const void* k, const void* v, const float* g, const float* beta, const float* S0,
                            void* out, float* S_out, void* workspace, int32_t* err, void* stream);

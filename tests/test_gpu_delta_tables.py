@@ -85,3 +85,56 @@ def test_a_sequence_with_a_wrong_entry_gets_no_gradients(table, at, value, who, 
     getattr(m, table)[at] = {"block_seq": [0, 0, 1, 1, 1, 2], "cu_blocks": [0, 2, 5, 6]}[table][at]
     again = _backward(d, m, ws=ws)
     assert all(torch.equal(again[x], want[x]) for x in NAMES)
+
+
+@pytest.mark.parametrize("H", [2, 200])
+def test_two_sequences_that_hold_the_same_tokens(H):
+    """0..100, a fall, and 50..120: the one between is skipped, both others have their states and the rows that they hold alone."""
+    d = Delta([100, 20, 0], H=H, dk=32, dv=32, dtype="bf16")
+    m = d.maps()
+    m.cu_tokens.copy_(torch.tensor([0, 100, 50, 120]))
+    m.cu_blocks.copy_(torch.tensor([0, 2, 2, 4]))
+    m.block_seq.copy_(torch.tensor([0, 0, 2, 2]))
+    out, last = _forward(d, m)
+    assert d.err[0].item() == rs.DEVERR_RANGE and (last[1] == 7.0).all()
+    grads = _backward(d, m)
+    assert (grads["dS0"][1] == 7.0).all()
+    for lens, s, at, alone in (([100, 20, 0], 0, 0, slice(0, 50)), ([50, 70, 0], 1, 2, slice(100, 120))):
+        one = Delta(lens, H=H, dk=32, dv=32, dtype="bf16")
+        one.S0[s], one.dS[s] = d.S0[at], d.dS[at]
+        want, states = _forward(one, one.maps())
+        assert torch.equal(out[alone], want[alone]) and torch.equal(last[at], states[s])
+        ref = _backward(one, one.maps())
+        assert torch.equal(grads["dS0"][at], ref["dS0"][s])
+        for x in ROWS:
+            assert torch.equal(grads[x][alone], ref[x][alone])
+
+
+def test_recurrent_form_of_two_sequences_that_hold_one_token():
+    d = Delta([3, 0, 2], H=2, dk=32, dv=32)
+    one = Delta([3, 2, 0], H=2, dk=32, dv=32)
+    one.cu.copy_(torch.tensor([0, 2, 5, 5]))
+    one.S0[1] = d.S0[2]
+    call = lambda x, after, out: rs.delta_step(x.cfg, x.cu, None, 3, x.q, x.k, x.v, x.g, x.beta, x.S0, after, out, x.err)  # noqa: E731
+    outs, pools = [d.new_out() for _ in range(3)], [d.new_states() for _ in range(3)]
+    call(d, pools[0], outs[0])
+    call(one, pools[1], outs[1])
+    d.cu.copy_(torch.tensor([0, 3, 2, 5]))
+    call(d, pools[2], outs[2])
+    assert d.err[0].item() == rs.DEVERR_RANGE and (pools[2][1] == 7.0).all()
+    assert torch.equal(pools[2][0], pools[0][0]) and torch.equal(pools[2][2], pools[1][1])
+    assert torch.equal(outs[2][:2], outs[0][:2]) and torch.equal(outs[2][3:], outs[1][3:])
+
+
+def test_offsets_that_fall_without_an_overlap():
+    """50..120, a fall, and 0..50: both sequences hold their tokens alone."""
+    d = Delta([70, 0, 50], H=2, dk=32, dv=32, dtype="bf16")
+    m = d.maps()
+    m.cu_tokens.copy_(torch.tensor([50, 120, 0, 50]))
+    one = Delta([50, 70, 0], H=2, dk=32, dv=32, dtype="bf16")
+    one.S0[0], one.S0[1] = d.S0[2], d.S0[0]
+    want, states = _forward(one, one.maps())
+    out, last = _forward(d, m)
+    assert d.err[0].item() == rs.DEVERR_RANGE  # (the one between them)
+    assert torch.equal(out, want) and torch.equal(last[0], states[1]) and torch.equal(last[2], states[0])
+    assert (last[1] == 7.0).all()
