@@ -564,8 +564,9 @@ int replayssm_delta_sizes(const replayssm_delta_config* cfg, int64_t* forward_by
  * sequence whose tables contradict each other (offsets that fall, another number of blocks than its
  * tokens make, a block that block_seq does not give to it) or leave the arrays is skipped (out and S_out are
  * left as they were) and REPLAYSSM_DEVERR_RANGE set in err. Tokens that two sequences hold, behind offsets
- * that fell, are taken by both, and their rows of out come from either. Results do not depend on what else
- * is in the batch. */
+ * that fell, are taken by both, and their rows of out come from either. block_seq is read up to the
+ * smaller of cu_blocks' total and cu_tokens' total / 64 + n_seqs, never past n_tokens / 64 + n_seqs entries.
+ * Results do not depend on what else is in the batch. */
 int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
                            const void* k, const void* v, const float* g, const float* beta, const float* S0,
                            void* out, float* S_out, void* workspace, int32_t* err, void* stream);

@@ -37,7 +37,7 @@ struct BackwardBlock {
 __device__ __forceinline__ bool block_ready(const DeltaArgs& a, int b, int h) {
   const char* ops = static_cast<const char*>(a.ws) + ((int64_t)b * a.H + h) * BackwardBlock::bytes;
   const uint32_t ready = reinterpret_cast<const BlockScalars*>(ops + BackwardBlock::scalars)->ready[0];
-  return b < a.cu_blocks[a.n_seqs] && ready != 0;
+  return b < table_blocks(a) && ready != 0;
 }
 
 // The gradients kernel walks the state rows in slices of 32 (one MFMA step over dv), then needs

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kChunkThreads) delta_prepare_kernel(const Delt
   using Rows = typename L::Rows;
   extern __shared__ __align__(16) char lds[];
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
-  if (b >= a.cu_blocks[a.n_seqs]) return;
+  if (b >= table_blocks(a)) return;  // (a total that is too large is flagged by the walk)
   const int s = a.block_seq[b];
   bool ok = s >= 0 && s < a.n_seqs;
   SeqRange seq{};

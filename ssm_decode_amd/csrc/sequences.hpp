@@ -13,6 +13,14 @@ struct SeqRange {
   bool ok;
 };
 
+// How many blocks the tables hold. The total of the tokens bounds it as the total of the blocks does, so that
+// one wrong total does not lead past the end of a block_seq that is shorter than max_blocks.
+__device__ __forceinline__ int table_blocks(const DeltaArgs& a) {
+  const int tokens = a.cu_tokens[a.n_seqs], blocks = a.cu_blocks[a.n_seqs];
+  const int most = (tokens > 0 ? tokens / kBlock : 0) + a.n_seqs;
+  return blocks < most ? (blocks < a.max_blocks ? blocks : a.max_blocks) : (most < a.max_blocks ? most : a.max_blocks);
+}
+
 __device__ __forceinline__ SeqRange seq_range(const DeltaArgs& a, int s) {
   SeqRange r;
   r.begin = a.cu_tokens[s];
@@ -20,7 +28,7 @@ __device__ __forceinline__ SeqRange seq_range(const DeltaArgs& a, int s) {
   r.block0 = a.cu_blocks[s];
   const int block1 = a.cu_blocks[s + 1];
   r.ok = r.begin >= 0 && r.end >= r.begin && (int64_t)r.end <= a.n_tokens && r.block0 >= 0 && block1 >= r.block0 &&
-         block1 <= a.max_blocks;
+         block1 <= table_blocks(a);
   r.blocks = r.ok ? block1 - r.block0 : 0;
   if (r.ok && r.blocks != (int)(((int64_t)r.end - r.begin + kBlock - 1) / kBlock)) r.ok = false;
   return r;

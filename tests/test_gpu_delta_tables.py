@@ -138,3 +138,18 @@ def test_offsets_that_fall_without_an_overlap():
     assert d.err[0].item() == rs.DEVERR_RANGE  # (the one between them)
     assert torch.equal(out, want) and torch.equal(last[0], states[1]) and torch.equal(last[2], states[0])
     assert (last[1] == 7.0).all()
+
+
+def test_a_wrong_total_of_blocks_over_tables_with_less_room():
+    """Tables of 73 tokens for arrays of 1000: the 3 blocks they hold are looked at, whatever their total says."""
+    d = Delta([70, 3], H=2, dk=32, dv=32, room=927)
+    m = rs.RaggedMaps(rs.make_ragged_config(2, 73))
+    rs.ragged_maps(m.cfg, m.struct, torch.tensor([70, 3], dtype=torch.int32, device="cuda"))
+    want, states = _forward(d, d.maps())
+    out, last = _forward(d, m)
+    assert torch.equal(out, want) and torch.equal(last, states) and d.err[0].item() == 0
+    m.cu_blocks[2] = 15
+    out, last = _forward(d, m)
+    assert d.err[0].item() == rs.DEVERR_RANGE
+    assert torch.equal(out[:70], want[:70]) and torch.equal(last[0], states[0])
+    assert (out[70:] == 7.0).all() and (last[1] == 7.0).all()
