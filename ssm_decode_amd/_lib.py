@@ -495,8 +495,17 @@ def ragged_sizes(cfg: RaggedConfig) -> int:
 
 
 def ragged_maps(cfg, maps, lengths, history=None, stream=None):
+    """replayssm_ragged_maps. Tables of a RaggedMaps have to be large enough for cfg's batches."""
     n = (cfg.n_seqs,)
+    room = getattr(maps, "room", None)
+    if room is not None:
+        need = (cfg.n_seqs, cfg.max_tokens, cfg.max_tokens // max(cfg.block, 1) + cfg.n_seqs)
+        for have, want, what in zip(room, need, ("cu_tokens and cu_blocks: requests", "token_seq: tokens", "block_seq: blocks")):
+            if want > have:
+                raise ValueError(f"{what}: the tables have room for {have}, the configuration needs {want}")
     dev, s = _device_and_stream(stream)
+    if room is not None and maps.tensors[0].get_device() != dev:
+        raise _off_device(maps.tensors[0], dev, "maps")
     _check(lib().replayssm_ragged_maps(ctypes.byref(cfg), ctypes.byref(maps),
                                        _dev(lengths, dev, torch.int32, n, "lengths"),
                                        _dev(history, dev, torch.int32, n, "history"), s), "ragged_maps")
@@ -518,6 +527,7 @@ class RaggedMaps:
         tensors = (self.cu_tokens, self.cu_blocks, self.token_seq, self.token_pos, self.block_seq, self.err)
         self.struct = Ragged(*[t.data_ptr() for t in tensors])
         self.struct.tensors = tensors  # the struct may outlive this object
+        self.struct.room = (cfg.n_seqs, cfg.max_tokens, self.max_blocks)
 
 
 def make_qk_norm_config(n_tokens, Hq, Hk, D, norm="l2", rot=0, interleaved=False, rep=1, eps=1e-6, q_scale=1.0,
