@@ -606,13 +606,27 @@ def _delta_inputs(cfg, dev, t, q, k, v, g, beta):
             _dev(beta, dev, f32, (n, cfg.H), "beta"))
 
 
-def _maps(cfg, maps, dev):
-    """The C struct of a batch's tables; those of RaggedMaps are checked against the batch."""
+def _maps(cfg, maps):
+    """The C arguments of a batch's configuration and tables; those of a RaggedMaps are checked against the batch. Where
+    they have room for fewer tokens than the arrays hold, the call is told that room: no sequence goes further, and the
+    kernels then read no table past its end, whatever is in it."""
+    room = getattr(maps, "room", None)
+    if room is not None:
+        n_seqs, tokens, blocks = room
+        if n_seqs != cfg.n_seqs:
+            raise ValueError(f"cu_tokens: tables of {cfg.n_seqs} sequences expected, got {n_seqs}")
+        if blocks < tokens // DELTA_BLOCK + n_seqs:
+            raise ValueError(f"block_seq: tables of blocks of {DELTA_BLOCK} expected")
+        if tokens < cfg.n_tokens:
+            cfg = DeltaConfig.from_buffer_copy(cfg)
+            cfg.n_tokens = tokens
+    return ctypes.byref(cfg), ctypes.byref(maps)
+
+
+def _maps_device(maps, dev):
     tensors = getattr(maps, "tensors", None)
-    if tensors is not None:
-        for t, what in zip(tensors[:2], ("cu_tokens", "cu_blocks")):
-            _dev(t, dev, torch.int32, (cfg.n_seqs + 1,), what)
-    return ctypes.byref(maps)
+    if tensors is not None and tensors[0].get_device() != dev:
+        raise _off_device(tensors[0], dev, "maps")
 
 
 def delta_step(cfg, cu_tokens, slots, n_slots, q, k, v, g, beta, S_in, S_out, out, err, stream=None):
@@ -627,12 +641,14 @@ def delta_step(cfg, cu_tokens, slots, n_slots, q, k, v, g, beta, S_in, S_out, ou
 
 
 def delta_prompt(cfg, maps, q, k, v, g, beta, S0, out, S_out, workspace, err, stream=None):
+    config, tables = _maps(cfg, maps)
     dev, s = _device_and_stream(stream)
+    _maps_device(maps, dev)
     need = delta_sizes(cfg)[0]
     t, f32 = _torch_dtype(cfg.dtype, "delta_prompt"), torch.float32
     states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
     _check(lib().replayssm_delta_prompt(
-        ctypes.byref(cfg), _maps(cfg, maps, dev), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
+        config, tables, *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
         _dev(S0, dev, f32, states, "S0"), _dev(out, dev, t, (cfg.n_tokens, cfg.H, cfg.dv), "out"),
         _dev(S_out, dev, f32, states, "S_out"), _workspace(workspace, dev, need),
         _dev(err, dev, torch.int32, None, "err"), s), "delta_prompt")
@@ -640,12 +656,14 @@ def delta_prompt(cfg, maps, q, k, v, g, beta, S0, out, S_out, workspace, err, st
 
 def delta_prompt_backward(cfg, maps, q, k, v, g, beta, S0, dout, dS_out, dq, dk, dv, dg, dbeta, dS0, workspace, err,
                           stream=None):
+    config, tables = _maps(cfg, maps)
     dev, s = _device_and_stream(stream)
+    _maps_device(maps, dev)
     need = delta_sizes(cfg)[1]
     t, n, f32 = _torch_dtype(cfg.dtype, "delta_prompt_backward"), cfg.n_tokens, torch.float32
     states, keys, values = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk), (n, cfg.Hk, cfg.dk), (n, cfg.H, cfg.dv)
     _check(lib().replayssm_delta_prompt_backward(
-        ctypes.byref(cfg), _maps(cfg, maps, dev), *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
+        config, tables, *_delta_inputs(cfg, dev, t, q, k, v, g, beta),
         _dev(S0, dev, f32, states, "S0"), _dev(dout, dev, t, values, "dout"),
         _dev(dS_out, dev, f32, states, "dS_out"), _dev(dq, dev, t, keys, "dq"), _dev(dk, dev, t, keys, "dk"),
         _dev(dv, dev, t, values, "dv"), _dev(dg, dev, f32, (n, cfg.H), "dg"),
