@@ -566,7 +566,7 @@ int replayssm_delta_sizes(const replayssm_delta_config* cfg, int64_t* forward_by
  * left as they were) and REPLAYSSM_DEVERR_RANGE set in err. Tokens that two sequences hold, behind offsets
  * that fell, are taken by both, and their rows of out come from either. block_seq is read up to the
  * smaller of cu_blocks' total and cu_tokens' total / 64 + n_seqs, never past n_tokens / 64 + n_seqs entries.
- * Results do not depend on what else is in the batch. */
+ * Results do not depend on what else is in the batch, to the bit. */
 int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
                            const void* k, const void* v, const float* g, const float* beta, const float* S0,
                            void* out, float* S_out, void* workspace, int32_t* err, void* stream);
@@ -577,9 +577,9 @@ int replayssm_delta_prompt(const replayssm_delta_config* cfg, const replayssm_ra
  * (of S0; NULL: not wanted; may be dS_out). dq, dk and dv are contiguous, in `dtype`.
  * The inputs, tables and S0 are those of the forward call; states are computed again, so nothing
  * of the forward call's workspace is needed. workspace: backward_bytes of replayssm_delta_sizes.
- * Sums have a fixed order: equal calls give equal bits. Rows of tokens that no sequence holds are
- * left as they were; a sequence with bad tables is skipped, all of its gradients left as they were, and
- * flagged as in the forward call. */
+ * Sums have a fixed order: equal calls give equal bits, and so does a sequence in other batches. Rows of
+ * tokens that no sequence holds are left as they were; a sequence with bad tables is skipped, all of its
+ * gradients left as they were, and flagged as in the forward call. */
 int replayssm_delta_prompt_backward(const replayssm_delta_config* cfg, const replayssm_ragged* maps, const void* q,
                                     const void* k, const void* v, const float* g, const float* beta, const float* S0,
                                     const void* dout, const float* dS_out, void* dq, void* dk, void* dv, float* dg,

@@ -46,8 +46,16 @@ struct Split {
   bf16x8 p[N];
 };
 
+// a * b + c in one rounding, whatever the compiler would make of it: where two kernels have to give the same bits, none
+// of them leaves it to the compiler which product of a sum is fused (or, below, whether a part's remainder is).
+template <typename V>
+__device__ __forceinline__ V fused(const V& a, const V& b, const V& c) {
+  return __builtin_elementwise_fma(a, b, c);
+}
+
 template <int N>
 __device__ __forceinline__ Split<N> split8(const f32x8& x) {
+#pragma clang fp contract(off)
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   Split<N> s;
@@ -65,15 +73,6 @@ __device__ __forceinline__ Split<N> split8(const f32x8& x) {
     }
     s.p[i] = __builtin_bit_cast(bf16x8, packed);
   }
-  return s;
-}
-
-// The first N parts.
-template <int N, int M>
-__device__ __forceinline__ Split<N> first_parts(const Split<M>& x) {
-  Split<N> s;
-#pragma unroll
-  for (int i = 0; i < N; ++i) s.p[i] = x.p[i];
   return s;
 }
 

@@ -45,7 +45,8 @@ __device__ __forceinline__ int by_length(const DeltaArgs& a, int place) {
   return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.n_seqs && rank == place));
 }
 
-// Which way: by rows, with 64 or 128 state rows per workgroup, or split, with 16.
+// Which way: by rows, with 64 or 128 state rows per workgroup, or split, with 16. All form every sum in the same order
+// and give the same bits, so that a sequence's results do not depend on how many others there are.
 enum class Walk { kRows64, kRows128, kSplit };
 
 // By rows once that gives three workgroups of 64 rows to four compute units (measured on both sides, see

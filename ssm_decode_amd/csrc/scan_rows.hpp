@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kChunkThreads)
         const f32x8 first = scal8(sc.first, p);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          bx[nt][p] = split8<mid>(v[nt][p].f32() - first * join(y[nt][2 * p], y[nt][2 * p + 1]));
+          bx[nt][p] = split8<mid>(fused(-first, join(y[nt][2 * p], y[nt][2 * p + 1]), v[nt][p].f32()));
       }
       __builtin_amdgcn_sched_barrier(0);
       f32x4 U[NT][4];
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kChunkThreads)
       const f32x8 last = scal8(sc.last, p);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        bu[nt][p] = split8<mid>(last * join(y[nt][2 * p], y[nt][2 * p + 1]) + a.scale * join(w[nt][2 * p], w[nt][2 * p + 1]));
+        bu[nt][p] = split8<mid>(fused(last, join(y[nt][2 * p], y[nt][2 * p + 1]), a.scale * join(w[nt][2 * p], w[nt][2 * p + 1])));
     }
     f32x8 x[NT][2];
     {
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kChunkThreads)
         const f32x8 first = scal8(sc.first, p), rate = -first * scal8(sc.beta, p);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          bd[nt][p] = split8<mid>(d[nt][p].f32() * first * a.scale);
+          bd[nt][p] = split8<mid>(a.scale * first * d[nt][p].f32());
           bx[nt][p] = split8<mid>(rate * x[nt][p]);
         }
       }
@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(kChunkThreads)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) dS.x[nt][group * kGroup + i] *= whole;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          products<in, mid>([&](int x, int y) {
+        for (int z = 0; z < 2; ++z)
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
+          for (int p = 0; p < 2; ++p)
+            products<in, mid>([&](int x, int y) {
 #pragma unroll
               for (int i = 0; i < kGroup; ++i)
 #pragma unroll
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kChunkThreads)
                   acc = z == 0 ? mfma(qc[group & 1][i][p].p[x], bd[nt][p].p[y], acc)
                                : mfma(kc[group & 1][i][p].p[x], bx[nt][p].p[y], acc);
                 }
-          });
+            });
         __builtin_amdgcn_sched_barrier(0);
       }
     }

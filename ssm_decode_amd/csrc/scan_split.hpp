@@ -35,6 +35,7 @@ __host__ __device__ constexpr int64_t item_grid(int64_t items, int slices) { ret
 // Right operands in LDS: [step][part][lane] of 16 bytes; a result tile of a pair fills its half of each lane's.
 template <int N>
 __device__ __forceinline__ void put_half(char* base, int step, int half, int lane, const f32x4& x) {
+#pragma clang fp contract(off)
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -223,13 +224,13 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       // (the chain goes on from y; Q S fills the time of its exchange)
       f32x4 x;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = (row4 + r < rows && live ? (float)v[r] : 0.f) - first4[set][r] * y[r];
+      for (int r = 0; r < 4; ++r) x[r] = fused(-first4[set][r], y[r], row4 + r < rows && live ? (float)v[r] : 0.f);
       put_half<mid>(lds + L::x, wave >> 1, wave & 1, lane, x);  // (beta is in T's columns)
       if constexpr (!KEEP) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
           const Split<in> qf = Qt.row8(own, ks, g);
-          o = mma(first_parts<low>(bs[ks]), qf, o);
+          products<in, low>([&](int i, int j) { o = mfma(bs[ks].p[j], qf.p[i], o); });
         }
       }
     }
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
       for (int ks = 0; ks < kSteps; ++ks) y = mma(kf[ks], bs[ks], y);
     }
     {
-      put_half<mid>(lds + L::u, wave >> 1, wave & 1, lane, last4[set] * y + a.scale * w);
+      put_half<mid>(lds + L::u, wave >> 1, wave & 1, lane, fused(last4[set], y, a.scale * w));
       f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
