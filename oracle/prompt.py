@@ -114,3 +114,46 @@ def delta_rule_backward_magnitudes(q, k, v, g, beta, S0, scale, dout, dS_last):
         m[3][t] = a * ((A(dS) * A(S)).sum() + m[2][t] @ (A(S) @ A(k[t]))) + A(dout[t]) @ (A(after[t]) @ A(q[t])) * scale
         dS = a * (dS - np.outer(beta[t] * (dS @ k[t]), k[t]))
     return m
+
+
+def delta_rule_in_blocks(q, k, v, g, beta, S0, scale, dout, dS_last, held, block=64, drop_states=False):
+    """The rule and its gradients by blocks of tokens, one head of one sequence: the formulas of the chunked form in fp64, but
+    that every computed operand of a product is first put through `held` (what number format it is held in).
+
+    Returns a dict of out, state, dv, dg, dbeta, dS0. With drop_states the gradient of the decays lacks the part that acts
+    through the state a block starts from (a mistake for tests to find)."""
+    S, kept = S0.astype(np.float64).copy(), []
+    out = np.zeros((len(g), len(S0)))
+    for b in range(0, len(g), block):
+        i = slice(b, b + block)
+        G = np.cumsum(np.maximum(g[i], -1e4))
+        n = len(G)
+        low = np.tril(np.ones((n, n)))
+        decay = np.exp(np.where(low > 0, G[:, None] - G[None], 0.0)) * low
+        first, last, whole = np.exp(G)[:, None], np.exp(G[-1] - G)[:, None], np.exp(G[-1])
+        kk, P = k[i] @ k[i].T, (q[i] @ k[i].T) * decay
+        A = beta[i][:, None] * kk * np.tril(decay, -1)
+        T = held(np.linalg.inv(np.eye(n) + A))
+        U = T @ held(beta[i][:, None] * (v[i] - first * (k[i] @ held(S).T)))
+        out[i] = scale * (first * (q[i] @ held(S).T) + held(P) @ held(U))
+        kept.append((i, S, U, T, P, A, kk, decay, first, last, whole))
+        S = whole * S + held(last * U).T @ k[i]
+    r = {"out": out, "state": S, "dv": np.zeros(v.shape), "dg": np.zeros(len(g)), "dbeta": np.zeros(len(g))}
+    dS = dS_last.astype(np.float64).copy()
+    for i, S, U, T, P, A, kk, decay, first, last, whole in reversed(kept):
+        d, bt = scale * dout[i], beta[i][:, None]
+        kdS = last * (k[i] @ held(dS).T)
+        dX = T.T @ held(held(P).T @ d + kdS)
+        r["dv"][i] = bt * dX
+        hS, hU, hX = held(S), held(U), held(dX)
+        dA = np.tril(-hX @ hU.T, -1)
+        dP = np.tril(d @ hU.T)
+        r["dbeta"][i] = (dX * v[i]).sum(1) - (first * (hX @ hS) * k[i]).sum(1) + (dA * kk * np.tril(decay, -1)).sum(1)
+        e = dP * P + dA * A
+        kf = (last * (hU @ held(dS)) * k[i]).sum(1)
+        dG = e.sum(1) - e.sum(0) + (first * (d @ hS) * q[i]).sum(1) - (bt * first * (hX @ hS) * k[i]).sum(1) - kf
+        dG[-1] += kf.sum() + (0.0 if drop_states else whole * (held(S) * held(dS)).sum())
+        r["dg"][i] = np.cumsum(dG[::-1])[::-1]
+        dS = whole * dS + held(first * d).T @ q[i] - held(first * bt * dX).T @ k[i]
+    r["dS0"] = dS
+    return r

@@ -75,11 +75,11 @@ class Delta:
         return (f64(self.q[a:b, hk]), f64(self.k[a:b, hk]), f64(self.v[a:b, h]), f64(self.g[a:b, h]),
                 f64(self.beta[a:b, h]), S0, self.scale), slice(a, b), hk
 
-    # What the kernels may be off by, relative to the terms' magnitudes. Every product that takes a
-    # computed operand rounds it to two bf16 parts or more (2^-18) and leaves out one product of parts
-    # (2^-18); a state passes four such products per block (K S, T X, the update, and the carried
-    # state's own earlier ones): 8 * 2^-18. fp32 inputs take three parts (2^-24 in place of 2^-18), where
-    # the fp32 sums over up to 128 terms dominate: 64 * 2^-24.
+    # What the kernels may be off by, relative to the terms' magnitudes, for every element and any signs. A product on the
+    # way to 16-bit outputs alone holds its computed operand in two bf16 parts (2^-18) and leaves out one product of parts
+    # (2^-18); a result passes four products per block (K S, T X, the update, and the carried state's own earlier
+    # ones): 8 * 2^-18. With fp32 inputs all take three parts, and the fp32 sums over up to 128 terms dominate: 64 * 2^-24. States
+    # and fp32 gradients take three parts for every type; prompt_precision has the narrower bars that hold them to it, normwise.
     def bar(self):
         return 8 * 2.0 ** -18 if self.dtype != "f32" else 64 * 2.0 ** -24
 
