@@ -502,7 +502,9 @@ int replayssm_qk_norm(const replayssm_qk_norm_config* cfg, const void* q, const 
 /* Gradients: from dq_out, dk_out (laid out as q_out, k_out; a head's rep copies are summed)
  * to dq [n_tokens][Hq][D], dk [n_tokens][Hk][D] and dwq, dwk [D] (either may be NULL: not
  * wanted). workspace: replayssm_qk_norm_sizes bytes, used when dwq or dwk is wanted. The sums
- * over rows have a fixed order: equal calls give equal bits. */
+ * over rows have a fixed order: equal calls give equal bits. All n_tokens rows count, those behind a packed
+ * batch's last token too: replayssm_delta_prompt_backward leaves these as they were, so clear its dq and dk
+ * before it where they are dq_out and dk_out here (q and k have to be finite there). */
 int replayssm_qk_norm_backward(const replayssm_qk_norm_config* cfg, const void* q, const void* k,
                                const float* wq, const float* wk, const int32_t* positions,
                                const float* inv_freq, const void* dq_out, const void* dk_out, void* dq,
