@@ -455,7 +455,10 @@ def _dev(t, dev, dtype, shape, what):
 
 
 def _rows(t, dev, dtype, shape, stride, what):
-    """Pointer of [tokens, heads, dim] rows whose heads lie together and whose tokens lie `stride` elements apart."""
+    """Pointer of [tokens, heads, dim] rows whose heads lie together and whose tokens lie `stride` elements apart; None stays
+    None, which the library refuses by name."""
+    if t is None:
+        return None
     if t.get_device() != dev:
         raise _off_device(t, dev, what)
     if t.dtype is not dtype:

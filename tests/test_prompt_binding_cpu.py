@@ -55,3 +55,14 @@ def test_tables_without_a_binding_of_their_own_go_through():
     m = rs.Ragged(*[1 << 20] * 6)
     config, tables = rs._lib._maps(cfg, m)
     assert config._obj is cfg and tables._obj is m
+
+
+def test_rows_that_are_missing_are_named_by_the_library():
+    """No tensor in place of rows goes on as NULL, as it does for every other argument."""
+    assert rs._lib._rows(None, 0, torch.float32, (10, 2, 64), 128, "q") is None
+    P = 1 << 20
+    cfg = rs.make_qk_norm_config(10, 2, 2, 64)
+    for i, name in ((0, "q"), (1, "k")):
+        args = [P] * 9
+        args[i] = None
+        assert rs.lib().replayssm_qk_norm(ctypes.byref(cfg), *args) == rs.EINVAL and rs.last_error() == f"{name} is NULL"
