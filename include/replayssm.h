@@ -554,7 +554,11 @@ int replayssm_delta_step(const replayssm_delta_config* cfg, const int32_t* cu_to
                          const float* beta, const float* S_in, float* S_out, void* out, int32_t* err,
                          void* stream);
 
-/* Bytes of the prompt calls' workspaces (either pointer may be NULL). Host only. */
+/* Bytes of the prompt calls' workspaces (either pointer may be NULL). Host only. Per value head and block, of which
+ * n_tokens / 64 + n_seqs are counted: forward 31 KiB (fp32: 37 KiB), backward 55 KiB + 8 dv dk + 512 dv bytes
+ * (253 KB at 128 x 128), and backward 8 dk bytes per token and value head more where H != Hk. A long
+ * sequence can go in segments through S0 and S_out, and backward from the last to the first through dS_out and dS0;
+ * segments of whole blocks give the bits of one call. */
 int replayssm_delta_sizes(const replayssm_delta_config* cfg, int64_t* forward_bytes, int64_t* backward_bytes);
 
 /* Chunked form: every sequence of the batch from its state S0[i] ([n_seqs][H][dv][dk]; NULL:
