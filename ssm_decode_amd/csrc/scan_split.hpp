@@ -8,6 +8,9 @@
 // left operands and, transposed, for everybody's channels in the update. The right operands (S, X, U) are
 // exchanged through LDS in operand layout, 16 bytes per lane, with three barriers per block.
 //
+// The lambdas that ask and put are inlined by force: one that is not by the time the arrays are taken apart leaves them in
+// scratch memory, and every load is waited for where it is asked for (fp16 and fp32, dk = 128: a block took 10.4 and 14.9 us).
+//
 // The chain of a block is then 12 + 6..12 + 12 matrix instructions (bf16, dk = 128) and four exchanges. Against the
 // kernels whose wavefronts take whole rows through all products (scan_rows.hpp) it reads K, Q, T and P four
 // times as often for the same rows, so it is used where those would leave most compute units idle. Measured,
@@ -157,11 +160,11 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     const int64_t left = seq.end - token(c);
     return left < kBlock ? (int)left : kBlock;
   };
-  const auto ask_rows = [&](int c) {
+  const auto ask_rows = [&](int c) __attribute__((always_inline)) {
     K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
     if constexpr (!KEEP) Q.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
   };
-  const auto ask_values = [&](int c, int set) {
+  const auto ask_values = [&](int c, int set) __attribute__((always_inline)) {
     const int rows = rows_of(c);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -174,19 +177,19 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     first1[set] = sc->first[dealt(wave, n)];
     whole[set] = sc->first[kBlock - 1];
   };
-  const auto ask_t = [&](int c) {
+  const auto ask_t = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       tf[p] = get_frag<mid>(ws + c * ws_step + Ops::t, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
   };
-  const auto ask_p = [&](int c) {
+  const auto ask_p = [&](int c) __attribute__((always_inline)) {
     if constexpr (!KEEP) {
 #pragma unroll
       for (int p = 0; p < 2; ++p)
         pf[p] = get_frag<low>(ws + c * ws_step + Ops::p, lower_frag(wave, p <= wave / 2 ? p : 0), lane);
     }
   };
-  const auto put_rows = [&](int c) {
+  const auto put_rows = [&](int c) __attribute__((always_inline)) {
     K.store(Kt, rows_of(c));
     if constexpr (!KEEP) Q.store(Qt, rows_of(c));
   };
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     return;
   }
   if (seq.blocks > 0) put_rows(0);
-  const auto block = [&](int c, int set) {
+  const auto block = [&](int c, int set) __attribute__((always_inline)) {
     const int rows = rows_of(c);
     const int64_t t0 = token(c);
     // (The last block asks for itself again. Loads under a condition would join their registers with the old ones
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     const int64_t left = seq.end - token(c);
     return left < kBlock ? (int)left : kBlock;
   };
-  const auto ask_values = [&](int c, int set) {
+  const auto ask_values = [&](int c, int set) __attribute__((always_inline)) {
     const int rows = rows_of(c);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -386,27 +389,27 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     beta4[set] = ld4(sc->beta + row4);
     whole[set] = sc->first[kBlock - 1];
   };
-  const auto ask_rows = [&](int c) {
+  const auto ask_rows = [&](int c) __attribute__((always_inline)) {
     K.load(kp + token(c) * a.k_stride, a.k_stride, rows_of(c));
     Q.load(qp + token(c) * a.q_stride, a.q_stride, rows_of(c));
   };
-  const auto put_rows = [&](int c) {
+  const auto put_rows = [&](int c) __attribute__((always_inline)) {
     K.store(Kt, rows_of(c));
     Q.store(Qt, rows_of(c));
   };
-  const auto ask_p = [&](int c) {
+  const auto ask_p = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       pf[p] = get_frag<mid>(ws + c * ws_step + Ops::pt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
   };
-  const auto ask_t = [&](int c) {
+  const auto ask_t = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       tf[p] = get_frag<mid>(ws + c * ws_step + Ops::tt, upper_frag(wave, p >= wave / 2 ? p : 1), lane);
   };
   char* const d_frags = lds + L::d;
   // dO of the block that was asked for, as an operand
-  const auto put_values = [&](int c) {
+  const auto put_values = [&](int c) __attribute__((always_inline)) {
     const int rows = rows_of(c);
     f32x4 x;
 #pragma unroll
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kChunkThreads, Parts<T>::in == 1 ? 2 : 1)
     put_values(seq.blocks - 1);
     put_rows(seq.blocks - 1);
   }
-  const auto block = [&](int c, int set) {
+  const auto block = [&](int c, int set) __attribute__((always_inline)) {
     const int rows = rows_of(c);
     const int next = c > 0 ? c - 1 : 0;  // (loads under no condition, as in the scan)
     const int64_t place = (int64_t)(seq.block0 + c) * a.H + h;
