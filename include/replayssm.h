@@ -522,9 +522,13 @@ int replayssm_qk_norm_backward(const replayssm_qk_norm_config* cfg, const void* 
  *   of Hk, dk 16, 32, 64 or 128, dv a multiple of 16 in 16..256; token strides in elements,
  *   >= the row, a multiple of 16 bytes; and H * dv / 16 * n_seqs <= 2^23 and
  *   H * (n_tokens / 64 + n_seqs) <= 2^23.
- * Sums and states are fp32. Rows of out of tokens that no sequence holds are left as they
- * were. A non-finite input may reach every later token of its sequence, and in the
- * prompt calls the earlier tokens of its block of 64 too; other sequences are not touched. */
+ * Sums and states are fp32. In the prompt calls the operands of products are held in 24 bits on the way
+ * to states and fp32 gradients, and with fp32 inputs to all results. With 16-bit inputs, what goes into
+ * 16-bit results alone (S q and the scores' part of out; the scores' part of dq and dk) is held in 17 bits
+ * before it is summed, which adds 2.4e-6 of the terms to the result's own rounding (2^-8 or 2^-11).
+ * Rows of out of tokens that no sequence holds are left as they were. A non-finite input may reach every
+ * later token of its sequence, and in the prompt calls the earlier tokens of its block of 64 too; other
+ * sequences are not touched. */
 #define REPLAYSSM_DELTA_BLOCK 64
 typedef struct replayssm_delta_config {
   int32_t n_seqs;

@@ -9,7 +9,10 @@
 // corrections, the inverse) takes three parts for every type, as the products of the inputs that
 // it is made of do; what goes into 16-bit outputs alone (Q S, P U; the gradients' Y and M)
 // takes two. With two throughout, states were 4e-6 to 9e-6 off and dg and dbeta of one batch of a few
-// tokens in a hundred over 1e-5; three leave 1e-7 and cost a tenth of the time.
+// tokens in a hundred over 1e-5; three leave 1e-7 to 4e-7 and cost a tenth of the time. Two leave 2.4e-6 of its terms in an
+// output that is then rounded by up to 2^-8 (bf16) or 2^-11 (fp16) of itself; its distance to 64 bits is the same to two
+// digits, but one in some thousand elements falls to the other side of a rounding. Three there too cost 7 % of one long prompt,
+// 19 % of a ragged batch (whose 128 rows a workgroup then do not fit LDS beside P) and 20 % of a training batch's gradients.
 //
 // Layout. In D = A B + C of v_mfma_f32_16x16x32_bf16 lane l (n = l & 15, g = l >> 4) holds
 // A[l & 15][8g .. 8g + 7], B[8g .. 8g + 7][n] and D[4g .. 4g + 3][n]. A result can be the next

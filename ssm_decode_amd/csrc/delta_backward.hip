@@ -58,8 +58,8 @@ struct GradLds {
                        cols = g + kBlock * 8, rows = cols + 4 * kBlock * 4, red = rows + 4 * kBlock * 4, total = red + 32;
 };
 
-// One workgroup per block and value head. 4096 of them (128 x 128, bf16) take 370 us: 1.2 GB of kept states and corrections
-// through memory (3.2 TB/s) and, about as long, the products of three-part operands, a third of them read
+// One workgroup per block and value head. 4096 of them (128 x 128, bf16) take 370 us: 1.2 GB through memory, 0.8 of them
+// kept states and corrections (3.2 TB/s), and, about as long, the products of three-part operands, a third of them read
 // transposed, at half of LDS's rate. Results are kept transposed (channels by tokens), as in the scan: a
 // lane has eight neighbouring channels of one token, i = 16 wave + n, whose scalars are its own. Where value heads
 // share a key head, dq and dk go to fp32 rows per value head that delta_share_kernel adds up.

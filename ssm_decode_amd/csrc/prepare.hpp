@@ -1,9 +1,10 @@
 // The stateless part of a block of the chunked delta rule, shared by both directions: decays, the
 // inverse T of the block's corrections and the decayed scores P, as matrix operands.
 //
-// One workgroup per block and value head, about 67 KB of LDS (dk = 128, 16-bit), so two on a compute unit. It writes 31 KB
-// (forward, 16-bit types) and reads 32: 16384 blocks and heads take 300 us, 3.4 TB/s; bound by memory and by the inverse's
-// chain of four 16 x 16 steps, which the other workgroup covers in part.
+// One workgroup per block and value head. It takes 67 KiB of LDS for bf16 (dk = 128), so two fit a compute unit, and writes
+// 31 KiB and reads 32: 16384 blocks and heads take 300 us, 3.4 TB/s; bound by memory and by the inverse's
+// chain of four 16 x 16 steps, which the other workgroup covers in part. fp16, whose rows are two parts, takes 99 KiB and fp32
+// 131, one workgroup a compute unit, and nothing covers the chain: 640 and 710 us.
 #pragma once
 
 #include <atomic>

@@ -5,7 +5,7 @@
 //   block_seq[b] = the request of block b (blocks never cross requests)
 //
 // One launch: the lengths are a few KB, so every workgroup scans all of them into its LDS
-// (16 KB at 4096 requests) and then writes its share of the token and block rows, four
+// (32 KB at 4096 requests) and then writes its share of the token and block rows, four
 // consecutive rows per thread from one binary search. That trades re-reads that stay in L2
 // for the second launch that a separate scan would take. Measured: 256 requests of 20011 tokens 5.6 us, 4096 of
 // 1000003 tokens 10 us (a launch alone is 4 to 5; the scan of 4096 lengths is most of the rest). Sums saturate at max_tokens + 1

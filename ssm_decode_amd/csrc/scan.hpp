@@ -31,8 +31,9 @@ __device__ __forceinline__ void skip_sequence(const DeltaArgs& a, int s, const S
 }
 
 // The place-th longest sequence. Workgroups start in index order, and a long sequence that starts last is
-// finished last; with over 64 sequences the heads of many are in flight and short ones fill the gaps,
-// so those keep their order.
+// finished last. One wavefront ranks its 64 lanes' sequences; more than 64 keep their order, and a long one that comes
+// last among them is not moved forward: 8192 tokens behind 95 sequences of 256 tokens, 16 heads of 128 x 128, take 1.12 ms
+// (in front of them 0.97), behind 199 of them 1.45 (1.10).
 __device__ __forceinline__ int by_length(const DeltaArgs& a, int place) {
   if (a.n_seqs > 64) return place;
   const int lane = threadIdx.x & 63;
@@ -49,9 +50,13 @@ __device__ __forceinline__ int by_length(const DeltaArgs& a, int place) {
 // and give the same bits, so that a sequence's results do not depend on how many others there are.
 enum class Walk { kRows64, kRows128, kSplit };
 
-// By rows once that gives three workgroups of 64 rows to four compute units (measured on both sides, see
-// scan_split.hpp), with two tiles per wavefront where there are workgroups enough, which
-// reads every left operand from LDS half as often (fp32's three parts would not fit).
+// By rows once that gives three workgroups of 64 rows to four compute units, with two tiles per wavefront where there are
+// workgroups enough, which reads every left operand from LDS half as often (fp32's three parts would not fit). Measured on
+// both sides at 128 x 128, see scan_split.hpp. A last slice that is not full counts as one that is, so the rule is less good for
+// other heads; split against rows in us, 4 sequences of 2048 tokens, dk = 128, forward and backward call, with as many
+// sequences times heads as first make it choose rows: dv = 16, 192 heads: 217 / 239, 581 / 658; dv = 48, 192: 304 / 250, 878 / 800;
+// dv = 80, 96: 156 / 197, 587 / 595; dv = 144, 64: 185 / 175, 655 / 583 (and 96, whose 288
+// workgroups go round the chip twice: 245 / 310, 909 / 970).
 template <typename T>
 hipError_t choose_walk(const DeltaArgs& a, Walk* walk) {
   int cus = 0;
