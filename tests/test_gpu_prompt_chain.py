@@ -1,4 +1,4 @@
-"""What README shows of the prompt side: prompts into decoding with one scale on both sides, and long sequences in segments."""
+"""Prompts into decoding with one scale on both sides, long sequences in segments, and the sizes of workspaces."""
 import numpy as np
 import pytest
 import torch
