@@ -595,6 +595,160 @@ int replayssm_delta_prompt_backward(const replayssm_delta_config* cfg, const rep
                                     const void* dout, const float* dS_out, void* dq, void* dk, void* dv, float* dg,
                                     float* dbeta, float* dS0, void* workspace, int32_t* err, void* stream);
 
+/* ==== a Mamba-2 layer on whole sequences ===================================
+ * What such a layer does with a prompt, and in training, in place of the decode path above: the input side's
+ * convolution, the state-space step as linear attention with a decay for each head, and the norm with its gate on the output
+ * side. Packed batches, tables, types, strides and streams are those of the prompt side. */
+
+/* ---- the convolution over a packed batch -----------------------------------
+ * replayssm_conv_step's rule for whole sequences: with x_s for s < 0 of a sequence taken from its window
+ *     y_t[c] = act(bias[c] + sum_{j<W} w[c][j] x_{t-W+1+j}[c]),  act = SiLU where silu is nonzero.
+ *   n_seqs 1..REPLAYSSM_RAGGED_SEQS, n_tokens 1..2^30, D a multiple of 8 in 8..2^17, W 1..4;
+ *   x_stride: elements between tokens, >= D and whole 16-byte units (x may be a column range); y, dy and dx are contiguous.
+ * Windows are fp32 [n_seqs][W - 1][D], oldest input first, as replayssm_conv_restore takes them. Everything is computed in fp32
+ * and rounded once to `dtype`. Arrays must not overlap (`last` must not be `first`). */
+typedef struct replayssm_conv_prompt_config {
+  int32_t n_seqs;
+  int32_t D;
+  int32_t W;
+  int32_t silu;
+  int32_t dtype; /* of x, y, dy, dx (enum replayssm_dtype) */
+  int64_t n_tokens;
+  int64_t x_stride;
+} replayssm_conv_prompt_config;
+
+/* Bytes of the backward call's workspace. Host only. */
+int replayssm_conv_prompt_sizes(const replayssm_conv_prompt_config* cfg, int64_t* backward_bytes);
+
+/* y [n_tokens][D] from x [n_tokens][D], w [D][W], bias [D] (NULL: 0) and the windows `first` in front of the sequences
+ * (NULL: 0); `last` (NULL: not wanted) receives the inputs that the next tokens need: the sequence's last W - 1, those of
+ * `first` among them where it has fewer tokens. maps: the tables of this batch, of any block size, with max_tokens <= n_tokens
+ * (read: cu_tokens, token_seq). A sequence whose offsets fall or leave 0..n_tokens, and a token that the tables give to a
+ * sequence that does not hold it, are skipped (their rows left as they were) and set REPLAYSSM_DEVERR_RANGE. Rows of tokens that
+ * no sequence holds are left as they were. */
+int replayssm_conv_prompt(const replayssm_conv_prompt_config* cfg, const replayssm_ragged* maps, const void* x,
+                          const float* w, const float* bias, const float* first, void* y, float* last, int32_t* err,
+                          void* stream);
+
+/* Gradients: from dy [n_tokens][D] and dlast (of `last`; NULL: 0) to dx [n_tokens][D] in `dtype`, dw [D][W], dbias [D] and
+ * dfirst (of `first`), fp32; dw, dbias and dfirst may be NULL: not wanted. x, w, bias and `first` are those of the forward
+ * call. workspace: replayssm_conv_prompt_sizes bytes, used when dw or dbias is wanted. Sums have a fixed order: equal calls give
+ * equal bits. Rows and sequences are skipped as in the forward call. */
+int replayssm_conv_prompt_backward(const replayssm_conv_prompt_config* cfg, const replayssm_ragged* maps, const void* x,
+                                   const float* w, const float* bias, const float* first, const void* dy, const float* dlast,
+                                   void* dx, float* dw, float* dbias, float* dfirst, void* workspace, int32_t* err,
+                                   void* stream);
+
+/* Starts sequences seqs[0..n) (device int32) of a decode ring from windows [n][W - 1][D]: their inputs become the window,
+ * nothing is pending. Indices outside 0..B-1 are skipped and set REPLAYSSM_DEVERR_INDEX in st->err; a sequence that is named
+ * twice gets either window's rows. 0 <= n <= 65535. */
+int replayssm_conv_restore(const replayssm_conv_config* cfg, const replayssm_conv_state* st, int n, const int32_t* seqs,
+                           const float* windows, void* stream);
+
+/* ---- linear attention with a decay for each head ---------------------------
+ * The state-space step of a Mamba-2 layer over sequences. Per value head, with state S [dv][dk], log decay g, rate beta and
+ * skip weight D:
+ *   S_t = e^{g_t} S_{t-1} + beta_t v_t k_t^T,   o_t = scale S_t q_t + D v_t
+ * (the recurrence of REPLAYSSM_MAMBA2 with alpha = e^g and v = beta v; g = -infinity closes the gate exactly; the layer's
+ * time step is beta, or 1 where it is in v already).
+ *   q, k [n_tokens][Hk][dk], v, out [n_tokens][H][dv] in `dtype`; g, beta [n_tokens][H] and skip [H] fp32 (beta NULL: 1, skip
+ *   NULL: 0); states [..][H][dv][dk] fp32, the logical layout of replayssm_restore.
+ * Value head h uses query and key head h / (H / Hk). Sizes and strides as for the delta rule; n_seqs 1..65535 (prompt
+ * calls: 1..REPLAYSSM_RAGGED_SEQS).
+ * `segment` (prompt calls): sequences are cut into segments of so many tokens, which are computed in parallel from states
+ * that a first pass finds; a multiple of REPLAYSSM_DELTA_BLOCK up to 65536. replayssm_linear_segment gives one that suits the
+ * sizes. H * (n_tokens / segment + n_seqs) * ceil(dv / 32) <= 2^23.
+ * Sums and states are fp32. In the prompt calls the operands of products are held in 24 bits on the way to states and fp32
+ * gradients, and with fp32 inputs to all results; what goes into 16-bit results alone is held in 17 bits before it is summed.
+ * Rows of out of tokens that no sequence holds are left as they were. A non-finite input may reach every later token of its
+ * sequence, and in the prompt calls the earlier tokens of its block of 64 too; other sequences are not touched. */
+typedef struct replayssm_linear_config {
+  int32_t n_seqs;
+  int32_t H;     /* value heads          */
+  int32_t Hk;    /* query and key heads  */
+  int32_t dk;
+  int32_t dv;
+  int32_t dtype; /* enum replayssm_dtype */
+  int64_t n_tokens;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  float scale;
+  int32_t segment; /* prompt calls; replayssm_linear_step does not look at it */
+} replayssm_linear_config;
+
+/* Tokens of a segment for these sizes (cfg->segment is not looked at). Host only. */
+int replayssm_linear_segment(const replayssm_linear_config* cfg, int32_t* segment);
+
+/* Recurrent form, for the one or few new tokens of each sequence: replayssm_delta_step's arrays, slots, flags and treatment of
+ * padded entries. */
+int replayssm_linear_step(const replayssm_linear_config* cfg, const int32_t* cu_tokens, const int32_t* slots, int n_slots,
+                          const void* q, const void* k, const void* v, const float* g, const float* beta, const float* skip,
+                          const float* S_in, float* S_out, void* out, int32_t* err, void* stream);
+
+/* Bytes of the prompt calls' workspaces (either pointer may be NULL). Host only. Forward: a state per segment, of which n_tokens /
+ * segment + n_seqs are counted; none where n_tokens <= segment. */
+int replayssm_linear_sizes(const replayssm_linear_config* cfg, int64_t* forward_bytes, int64_t* backward_bytes);
+
+/* Chunked form: every sequence of the batch from its state S0[i] ([n_seqs][H][dv][dk]; NULL: zero), however long or short. maps:
+ * the tables of this batch, built by replayssm_ragged_maps with block = cfg->segment and max_tokens <= n_tokens (read: cu_tokens,
+ * cu_blocks, block_seq). S_out [n_seqs][H][dv][dk] receives the states after the last tokens (S0 for an empty sequence; NULL:
+ * not wanted; may be S0). workspace: forward_bytes of replayssm_linear_sizes (may be NULL if that is 0), free again when the call's
+ * work is done. A sequence whose tables contradict each other or leave the arrays is skipped (out and S_out are left as they
+ * were) and REPLAYSSM_DEVERR_RANGE set in err, as by replayssm_delta_prompt. For one configuration results do not depend on
+ * what else is in the batch, to the bit. */
+int replayssm_linear_prompt(const replayssm_linear_config* cfg, const replayssm_ragged* maps, const void* q, const void* k,
+                            const void* v, const float* g, const float* beta, const float* skip, const float* S0, void* out,
+                            float* S_out, void* workspace, int32_t* err, void* stream);
+
+/* Gradients of replayssm_linear_prompt: from dout [n_tokens][H][dv] (of out) and dS_out [n_seqs][H][dv][dk] (of S_out; NULL:
+ * zero) to dq, dk [n_tokens][Hk][dk] (summed over the value heads that share a key head), dv [n_tokens][H][dv], dg and dbeta
+ * [n_tokens][H] fp32, dskip [H] fp32 and dS0 (of S0; may be dS_out); dbeta, dskip and dS0 may be NULL: not wanted. dq, dk and dv are
+ * contiguous, in `dtype`. The inputs, tables and S0 are those of the forward call; states are computed again. workspace:
+ * backward_bytes of replayssm_linear_sizes. Sums have a fixed order: equal calls give equal bits. Rows of tokens that no sequence
+ * holds are left as they were; a sequence with bad tables is skipped, its gradients left as they were (it adds nothing to dskip), and
+ * flagged as in the forward call. */
+int replayssm_linear_prompt_backward(const replayssm_linear_config* cfg, const replayssm_ragged* maps, const void* q,
+                                     const void* k, const void* v, const float* g, const float* beta, const float* skip,
+                                     const float* S0, const void* dout, const float* dS_out, void* dq, void* dk, void* dv,
+                                     float* dg, float* dbeta, float* dskip, float* dS0, void* workspace, int32_t* err,
+                                     void* stream);
+
+/* ---- the gated group norm ---------------------------------------------------
+ * The output side: per token and group of D channels, with G = silu(z),
+ *   GATE_BEFORE:  y = u r w,    u = x G,  r = (sum u^2 / D + eps)^(-1/2)
+ *   GATE_AFTER:   y = x r w G,            r = (sum x^2 / D + eps)^(-1/2)
+ *   GATE_NONE:    y = x r w  (z, dz unused)
+ *   n_tokens 1..2^23, D a multiple of 8 in 8..8192, groups 1..4096 with groups * D <= 2^20, eps >= 0 (with 0 a row of zeros has no
+ *   norm and gives NaN); x_stride, z_stride: elements between tokens, >= groups * D and whole 16-byte units.
+ * w is fp32 [groups][D], or [D] for all groups with `shared`. Everything is computed in fp32 and rounded once to `dtype`. */
+enum replayssm_gate { REPLAYSSM_GATE_NONE = 0, REPLAYSSM_GATE_BEFORE = 1, REPLAYSSM_GATE_AFTER = 2 };
+typedef struct replayssm_gated_norm_config {
+  int32_t n_tokens;
+  int32_t groups;
+  int32_t D;
+  int32_t gate;   /* enum replayssm_gate */
+  int32_t shared; /* nonzero: one row of weights for all groups */
+  int32_t dtype;  /* of x, z, y and their gradients (enum replayssm_dtype) */
+  float eps;
+  int64_t x_stride;
+  int64_t z_stride;
+} replayssm_gated_norm_config;
+
+/* Bytes of the backward call's workspace. Host only. */
+int replayssm_gated_norm_sizes(const replayssm_gated_norm_config* cfg, int64_t* backward_bytes);
+
+/* x, z [n_tokens][groups][D] -> y, contiguous. */
+int replayssm_gated_norm(const replayssm_gated_norm_config* cfg, const void* x, const void* z, const float* w, void* y,
+                         void* stream);
+
+/* Gradients: from dy (like y) to dx and dz, contiguous like y, and dw like w (NULL: not wanted). workspace:
+ * replayssm_gated_norm_sizes bytes, used when dw is wanted. Sums over tokens have a fixed order: equal calls give equal bits. All
+ * n_tokens rows count in dw: where rows behind a packed batch's last token are not wanted, n_tokens ends in front of
+ * them, or their dy is zero (and x and z finite). */
+int replayssm_gated_norm_backward(const replayssm_gated_norm_config* cfg, const void* x, const void* z, const float* w,
+                                  const void* dy, void* dx, void* dz, float* dw, void* workspace, void* stream);
+
 /* ---- Kernel tiling (no effect on results) ----------------------------------------------
  * How the replay kernel (decode, verify, flush and the fused steps) maps the checkpoint onto
  * wavefronts when dk = 128, T_max <= 4 and dv is a multiple of 32: one 16-row tile

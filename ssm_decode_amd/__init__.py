@@ -16,4 +16,8 @@ from ._lib import (  # noqa: F401
     BF16, DELTA_BLOCK, DEVERR_RANGE, DeltaConfig, F16, F32, NORM_L2, NORM_RMS, QkNormConfig, Ragged, RaggedConfig,
     RaggedMaps, delta_prompt, delta_prompt_backward, delta_sizes, delta_step, make_delta_config, make_qk_norm_config, make_ragged_config, qk_norm, qk_norm_backward,
     qk_norm_sizes, ragged_maps, ragged_sizes,
+    ConvPromptConfig, GATE_AFTER, GATE_BEFORE, GATE_NONE, GatedNormConfig, LinearConfig, conv_prompt, conv_prompt_backward,
+    conv_prompt_sizes, conv_restore, gated_norm, gated_norm_backward, gated_norm_sizes, linear_prompt,
+    linear_prompt_backward, linear_segment, linear_sizes, linear_step, make_conv_prompt_config, make_gated_norm_config,
+    make_linear_config,
 )

@@ -35,7 +35,10 @@ DTYPES = {"f32": F32, "bf16": BF16, "f16": F16}
 TORCH_DTYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
 NORM_L2, NORM_RMS = 0, 1
 NORMS = {"l2": NORM_L2, "rms": NORM_RMS}
+GATE_NONE, GATE_BEFORE, GATE_AFTER = 0, 1, 2
+GATES = {"none": GATE_NONE, None: GATE_NONE, "before": GATE_BEFORE, "after": GATE_AFTER}
 DELTA_BLOCK = 64
+RAGGED_SEQS = 16384
 
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -89,6 +92,22 @@ class DeltaConfig(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class ConvPromptConfig(ctypes.Structure):
+    _fields_ = [("n_seqs", _i32), ("D", _i32), ("W", _i32), ("silu", _i32), ("dtype", _i32), ("n_tokens", _i64),
+                ("x_stride", _i64)]
+
+
+class LinearConfig(ctypes.Structure):
+    _fields_ = [("n_seqs", _i32), ("H", _i32), ("Hk", _i32), ("dk", _i32), ("dv", _i32), ("dtype", _i32),
+                ("n_tokens", _i64), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("scale", ctypes.c_float), ("segment", _i32)]
+
+
+class GatedNormConfig(ctypes.Structure):
+    _fields_ = [("n_tokens", _i32), ("groups", _i32), ("D", _i32), ("gate", _i32), ("shared", _i32), ("dtype", _i32),
+                ("eps", ctypes.c_float), ("x_stride", _i64), ("z_stride", _i64)]
+
+
 class ReplaySSMError(RuntimeError):
     def __init__(self, status: int, where: str, text: str):
         super().__init__(f"{where}: status {status} ({text})")
@@ -137,6 +156,18 @@ SIGNATURES = {
     "replayssm_delta_prompt": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(Ragged)] + [_vp] * 11,
     "replayssm_delta_prompt_backward": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(Ragged)] + [_vp] * 17,
     "replayssm_delta_sizes": [ctypes.POINTER(DeltaConfig), ctypes.POINTER(_i64), ctypes.POINTER(_i64)],
+    "replayssm_conv_prompt_sizes": [ctypes.POINTER(ConvPromptConfig), ctypes.POINTER(_i64)],
+    "replayssm_conv_prompt": [ctypes.POINTER(ConvPromptConfig), ctypes.POINTER(Ragged)] + [_vp] * 8,
+    "replayssm_conv_prompt_backward": [ctypes.POINTER(ConvPromptConfig), ctypes.POINTER(Ragged)] + [_vp] * 13,
+    "replayssm_conv_restore": [ctypes.POINTER(ConvConfig), ctypes.POINTER(ConvState), ctypes.c_int, _vp, _vp, _vp],
+    "replayssm_linear_segment": [ctypes.POINTER(LinearConfig), ctypes.POINTER(_i32)],
+    "replayssm_linear_sizes": [ctypes.POINTER(LinearConfig), ctypes.POINTER(_i64), ctypes.POINTER(_i64)],
+    "replayssm_linear_step": [ctypes.POINTER(LinearConfig), _vp, _vp, ctypes.c_int] + [_vp] * 11,
+    "replayssm_linear_prompt": [ctypes.POINTER(LinearConfig), ctypes.POINTER(Ragged)] + [_vp] * 12,
+    "replayssm_linear_prompt_backward": [ctypes.POINTER(LinearConfig), ctypes.POINTER(Ragged)] + [_vp] * 19,
+    "replayssm_gated_norm_sizes": [ctypes.POINTER(GatedNormConfig), ctypes.POINTER(_i64)],
+    "replayssm_gated_norm": [ctypes.POINTER(GatedNormConfig)] + [_vp] * 5,
+    "replayssm_gated_norm_backward": [ctypes.POINTER(GatedNormConfig)] + [_vp] * 9,
 }
 STRING_FUNCTIONS = {"replayssm_status_string": [ctypes.c_int], "replayssm_last_error": []}
 
@@ -672,3 +703,217 @@ def delta_prompt_backward(cfg, maps, q, k, v, g, beta, S0, dout, dS_out, dq, dk,
         _dev(dv, dev, t, values, "dv"), _dev(dg, dev, f32, (n, cfg.H), "dg"),
         _dev(dbeta, dev, f32, (n, cfg.H), "dbeta"), _dev(dS0, dev, f32, states, "dS0"),
         _workspace(workspace, dev, need), _dev(err, dev, torch.int32, None, "err"), s), "delta_prompt_backward")
+
+
+# ---- a Mamba-2 layer on whole sequences: convolution, linear attention, gated norm ----
+
+def make_conv_prompt_config(n_seqs, n_tokens, D, W=4, silu=True, dtype="bf16", x_stride=None) -> ConvPromptConfig:
+    """x_stride defaults to contiguous rows."""
+    return ConvPromptConfig(int(n_seqs), int(D), int(W), int(bool(silu)), DTYPES.get(dtype, dtype), int(n_tokens),
+                            int(D if x_stride is None else x_stride))
+
+
+def conv_prompt_sizes(cfg: ConvPromptConfig) -> int:
+    n = _i64(0)
+    _check(lib().replayssm_conv_prompt_sizes(ctypes.byref(cfg), ctypes.byref(n)), "conv_prompt_sizes")
+    return int(n.value)
+
+
+def _channel_rows(t, dev, dtype, shape, stride, what):
+    """Pointer of [tokens, channels] rows whose tokens lie `stride` elements apart."""
+    if t is None:
+        return None
+    if t.dim() != 2:
+        raise ValueError(f"{what}: shape {shape} expected, got {tuple(t.shape)}")
+    return _rows(t.unsqueeze(1), dev, dtype, (shape[0], 1, shape[1]), stride, what)
+
+
+def _table_room(cfg, maps):
+    """The room of a RaggedMaps in (tokens, blocks), checked against the batch; None for tables of the caller's own."""
+    room = getattr(maps, "room", None)
+    if room is None:
+        return None
+    if room[0] != cfg.n_seqs:
+        raise ValueError(f"cu_tokens: tables of {cfg.n_seqs} sequences expected, got {room[0]}")
+    return room[1:]
+
+
+def _conv_maps(cfg, maps):
+    """As _maps: tables with room for fewer tokens than the arrays hold tell the call so."""
+    room = _table_room(cfg, maps)
+    if room is not None and room[0] < cfg.n_tokens:
+        cfg = ConvPromptConfig.from_buffer_copy(cfg)
+        cfg.n_tokens = room[0]
+    return ctypes.byref(cfg), ctypes.byref(maps)
+
+
+def _conv_inputs(cfg, dev, x, w, bias, first):
+    f32, D, W = torch.float32, cfg.D, cfg.W
+    return (_channel_rows(x, dev, _torch_dtype(cfg.dtype, "conv_prompt"), (cfg.n_tokens, D), cfg.x_stride, "x"),
+            _dev(w, dev, f32, (D, W), "w"), _dev(bias, dev, f32, (D,), "bias"),
+            _dev(first, dev, f32, (cfg.n_seqs, W - 1, D), "first") if W > 1 else None)
+
+
+def conv_prompt(cfg, maps, x, w, bias, first, y, last, err, stream=None):
+    config, tables = _conv_maps(cfg, maps)
+    dev, s = _device_and_stream(stream)
+    _maps_device(maps, dev)
+    conv_prompt_sizes(cfg)
+    t, f32 = _torch_dtype(cfg.dtype, "conv_prompt"), torch.float32
+    _check(lib().replayssm_conv_prompt(
+        config, tables, *_conv_inputs(cfg, dev, x, w, bias, first), _dev(y, dev, t, (cfg.n_tokens, cfg.D), "y"),
+        _dev(last, dev, f32, (cfg.n_seqs, cfg.W - 1, cfg.D), "last") if cfg.W > 1 else None,
+        _dev(err, dev, torch.int32, None, "err"), s), "conv_prompt")
+
+
+def conv_prompt_backward(cfg, maps, x, w, bias, first, dy, dlast, dx, dw, dbias, dfirst, workspace, err, stream=None):
+    config, tables = _conv_maps(cfg, maps)
+    dev, s = _device_and_stream(stream)
+    _maps_device(maps, dev)
+    need = conv_prompt_sizes(cfg) if dw is not None or dbias is not None else 0
+    t, f32, D, W = _torch_dtype(cfg.dtype, "conv_prompt_backward"), torch.float32, cfg.D, cfg.W
+    window = (cfg.n_seqs, W - 1, D)
+    _check(lib().replayssm_conv_prompt_backward(
+        config, tables, *_conv_inputs(cfg, dev, x, w, bias, first), _dev(dy, dev, t, (cfg.n_tokens, D), "dy"),
+        _dev(dlast, dev, f32, window, "dlast") if W > 1 else None, _dev(dx, dev, t, (cfg.n_tokens, D), "dx"),
+        _dev(dw, dev, f32, (D, W), "dw"), _dev(dbias, dev, f32, (D,), "dbias"),
+        _dev(dfirst, dev, f32, window, "dfirst") if W > 1 else None, _workspace(workspace, dev, need),
+        _dev(err, dev, torch.int32, None, "err"), s), "conv_prompt_backward")
+
+
+def conv_restore(cfg, st, seqs, windows, stream=None):
+    """Starts sequences seqs of a ConvLayer from the windows that conv_prompt left."""
+    n = seqs.shape[0]
+    dev, s = _device_and_stream(stream)
+    _check(lib().replayssm_conv_restore(
+        ctypes.byref(cfg), ctypes.byref(st), int(n), _dev(seqs, dev, torch.int32, (n,), "seqs") if n else None,
+        _dev(windows, dev, torch.float32, (n, cfg.W - 1, cfg.D), "windows") if n and cfg.W > 1 else None, s), "conv_restore")
+
+
+def make_linear_config(n_seqs, n_tokens, H, Hk, dk, dv, dtype="bf16", scale=1.0, q_stride=None, k_stride=None,
+                       v_stride=None, segment=None) -> LinearConfig:
+    """Strides default to contiguous rows, segment to replayssm_linear_segment's (which refuses bad sizes)."""
+    cfg = LinearConfig(int(n_seqs), int(H), int(Hk), int(dk), int(dv), DTYPES.get(dtype, dtype), int(n_tokens),
+                       int(Hk * dk if q_stride is None else q_stride), int(Hk * dk if k_stride is None else k_stride),
+                       int(H * dv if v_stride is None else v_stride), float(scale), DELTA_BLOCK)
+    if segment is not None:
+        cfg.segment = int(segment)
+    elif cfg.n_seqs <= RAGGED_SEQS:  # (only the step takes more)
+        cfg.segment = linear_segment(cfg)
+    return cfg
+
+
+def linear_segment(cfg: LinearConfig) -> int:
+    n = _i32(0)
+    _check(lib().replayssm_linear_segment(ctypes.byref(cfg), ctypes.byref(n)), "linear_segment")
+    return int(n.value)
+
+
+def linear_sizes(cfg: LinearConfig):
+    """(bytes of linear_prompt's workspace, bytes of linear_prompt_backward's)"""
+    f, b = _i64(0), _i64(0)
+    _check(lib().replayssm_linear_sizes(ctypes.byref(cfg), ctypes.byref(f), ctypes.byref(b)), "linear_sizes")
+    return int(f.value), int(b.value)
+
+
+def _linear_inputs(cfg, dev, t, q, k, v, g, beta, skip):
+    n, f32 = cfg.n_tokens, torch.float32
+    return (_rows(q, dev, t, (n, cfg.Hk, cfg.dk), cfg.q_stride, "q"),
+            _rows(k, dev, t, (n, cfg.Hk, cfg.dk), cfg.k_stride, "k"),
+            _rows(v, dev, t, (n, cfg.H, cfg.dv), cfg.v_stride, "v"), _dev(g, dev, f32, (n, cfg.H), "g"),
+            _dev(beta, dev, f32, (n, cfg.H), "beta"), _dev(skip, dev, f32, (cfg.H,), "skip"))
+
+
+def _linear_maps(cfg, maps):
+    """As _maps, for tables whose blocks are the configuration's segments."""
+    room = _table_room(cfg, maps)
+    if room is not None:
+        tokens, blocks = room
+        if blocks != tokens // cfg.segment + cfg.n_seqs:
+            raise ValueError(f"block_seq: tables of blocks of {cfg.segment} expected")
+        if tokens < cfg.n_tokens:
+            cfg = LinearConfig.from_buffer_copy(cfg)
+            cfg.n_tokens = tokens
+    return ctypes.byref(cfg), ctypes.byref(maps)
+
+
+def linear_step(cfg, cu_tokens, slots, n_slots, q, k, v, g, beta, skip, S_in, S_out, out, err, stream=None):
+    dev, s = _device_and_stream(stream)
+    t, i32, n = _torch_dtype(cfg.dtype, "linear_step"), torch.int32, cfg.n_seqs
+    pool = (n_slots, cfg.H, cfg.dv, cfg.dk)
+    _check(lib().replayssm_linear_step(
+        ctypes.byref(cfg), _dev(cu_tokens, dev, i32, (n + 1,), "cu_tokens"), _dev(slots, dev, i32, (n,), "slots"),
+        int(n_slots), *_linear_inputs(cfg, dev, t, q, k, v, g, beta, skip), _dev(S_in, dev, torch.float32, pool, "S_in"),
+        _dev(S_out, dev, torch.float32, pool, "S_out"), _dev(out, dev, t, (cfg.n_tokens, cfg.H, cfg.dv), "out"),
+        _dev(err, dev, i32, None, "err"), s), "linear_step")
+
+
+def linear_prompt(cfg, maps, q, k, v, g, beta, skip, S0, out, S_out, workspace, err, stream=None):
+    dev, s = _device_and_stream(stream)
+    need = linear_sizes(cfg)[0]
+    config, tables = _linear_maps(cfg, maps)
+    _maps_device(maps, dev)
+    t, f32 = _torch_dtype(cfg.dtype, "linear_prompt"), torch.float32
+    states = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk)
+    _check(lib().replayssm_linear_prompt(
+        config, tables, *_linear_inputs(cfg, dev, t, q, k, v, g, beta, skip), _dev(S0, dev, f32, states, "S0"),
+        _dev(out, dev, t, (cfg.n_tokens, cfg.H, cfg.dv), "out"), _dev(S_out, dev, f32, states, "S_out"),
+        _workspace(workspace, dev, need), _dev(err, dev, torch.int32, None, "err"), s), "linear_prompt")
+
+
+def linear_prompt_backward(cfg, maps, q, k, v, g, beta, skip, S0, dout, dS_out, dq, dk, dv, dg, dbeta, dskip, dS0,
+                           workspace, err, stream=None):
+    dev, s = _device_and_stream(stream)
+    need = linear_sizes(cfg)[1]
+    config, tables = _linear_maps(cfg, maps)
+    _maps_device(maps, dev)
+    t, n, f32 = _torch_dtype(cfg.dtype, "linear_prompt_backward"), cfg.n_tokens, torch.float32
+    states, keys, values = (cfg.n_seqs, cfg.H, cfg.dv, cfg.dk), (n, cfg.Hk, cfg.dk), (n, cfg.H, cfg.dv)
+    _check(lib().replayssm_linear_prompt_backward(
+        config, tables, *_linear_inputs(cfg, dev, t, q, k, v, g, beta, skip), _dev(S0, dev, f32, states, "S0"),
+        _dev(dout, dev, t, values, "dout"), _dev(dS_out, dev, f32, states, "dS_out"), _dev(dq, dev, t, keys, "dq"),
+        _dev(dk, dev, t, keys, "dk"), _dev(dv, dev, t, values, "dv"), _dev(dg, dev, f32, (n, cfg.H), "dg"),
+        _dev(dbeta, dev, f32, (n, cfg.H), "dbeta"), _dev(dskip, dev, f32, (cfg.H,), "dskip"),
+        _dev(dS0, dev, f32, states, "dS0"), _workspace(workspace, dev, need), _dev(err, dev, torch.int32, None, "err"),
+        s), "linear_prompt_backward")
+
+
+def make_gated_norm_config(n_tokens, groups, D, gate="before", shared=False, eps=1e-5, dtype="bf16", x_stride=None,
+                           z_stride=None) -> GatedNormConfig:
+    """gate: "before" or "after" the norm, or "none". Strides default to contiguous rows."""
+    row = int(groups) * int(D)
+    return GatedNormConfig(int(n_tokens), int(groups), int(D), GATES.get(gate, gate), int(bool(shared)),
+                           DTYPES.get(dtype, dtype), float(eps), int(row if x_stride is None else x_stride),
+                           int(row if z_stride is None else z_stride))
+
+
+def gated_norm_sizes(cfg: GatedNormConfig) -> int:
+    n = _i64(0)
+    _check(lib().replayssm_gated_norm_sizes(ctypes.byref(cfg), ctypes.byref(n)), "gated_norm_sizes")
+    return int(n.value)
+
+
+def _norm_inputs(cfg, dev, x, z, w):
+    t, shape = _torch_dtype(cfg.dtype, "gated_norm"), (cfg.n_tokens, cfg.groups, cfg.D)
+    return (_rows(x, dev, t, shape, cfg.x_stride, "x"),
+            _rows(z, dev, t, shape, cfg.z_stride, "z") if cfg.gate != GATE_NONE else None,
+            _dev(w, dev, torch.float32, (cfg.D,) if cfg.shared else shape[1:], "w"))
+
+
+def gated_norm(cfg, x, z, w, y, stream=None):
+    dev, s = _device_and_stream(stream)
+    gated_norm_sizes(cfg)
+    t, shape = _torch_dtype(cfg.dtype, "gated_norm"), (cfg.n_tokens, cfg.groups, cfg.D)
+    _check(lib().replayssm_gated_norm(ctypes.byref(cfg), *_norm_inputs(cfg, dev, x, z, w), _dev(y, dev, t, shape, "y"), s),
+           "gated_norm")
+
+
+def gated_norm_backward(cfg, x, z, w, dy, dx, dz, dw=None, workspace=None, stream=None):
+    dev, s = _device_and_stream(stream)
+    need = gated_norm_sizes(cfg)
+    t, shape = _torch_dtype(cfg.dtype, "gated_norm"), (cfg.n_tokens, cfg.groups, cfg.D)
+    _check(lib().replayssm_gated_norm_backward(
+        ctypes.byref(cfg), *_norm_inputs(cfg, dev, x, z, w), _dev(dy, dev, t, shape, "dy"), _dev(dx, dev, t, shape, "dx"),
+        _dev(dz, dev, t, shape, "dz") if cfg.gate != GATE_NONE else None,
+        _dev(dw, dev, torch.float32, (cfg.D,) if cfg.shared else shape[1:], "dw"),
+        _workspace(workspace, dev, need if dw is not None else 0), s), "gated_norm_backward")

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libreplayssm.so")
 SOURCES = ["replay.hip", "ring.hip", "eager.hip", "probe.hip", "conv.hip", "ragged.hip", "qknorm.hip",
-           "delta_step.hip", "delta_prompt.hip", "delta_backward.hip", "api.cpp", "api_prompt.cpp"]
+           "delta_step.hip", "delta_prompt.hip", "delta_backward.hip", "conv_prompt.hip", "gatednorm.hip", "linear_prompt.hip",
+           "linear_backward.hip", "api.cpp", "api_prompt.cpp", "api_layer.cpp"]
 ARCH = "gfx950"
 
 

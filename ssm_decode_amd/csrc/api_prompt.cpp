@@ -9,23 +9,6 @@ using namespace rs::host;
 
 namespace {
 
-int element_bytes(int dtype) { return dtype == REPLAYSSM_F32 ? 4 : 2; }
-
-int check_dtype(int dtype, const char* name) {
-  if (dtype != REPLAYSSM_F32 && dtype != REPLAYSSM_BF16 && dtype != REPLAYSSM_F16)
-    return fail(REPLAYSSM_EINVAL, "%s %d unknown", name, dtype);
-  return REPLAYSSM_OK;
-}
-
-// Elements between tokens: at least the row, whole 16-byte units.
-int check_stride(int64_t stride, int64_t row, int dtype, const char* name) {
-  if (stride < row || stride > (int64_t)1 << 31)
-    return fail(REPLAYSSM_EINVAL, "%s=%lld outside %lld..2^31", name, (long long)stride, (long long)row);
-  if (stride * element_bytes(dtype) % 16 != 0)
-    return fail(REPLAYSSM_EINVAL, "%s=%lld is not a multiple of 16 bytes", name, (long long)stride);
-  return REPLAYSSM_OK;
-}
-
 int check_ragged(const replayssm_ragged_config* c) {
   if (c == nullptr) return fail(REPLAYSSM_EINVAL, "cfg is NULL");
   if (c->n_seqs < 1 || c->n_seqs > REPLAYSSM_RAGGED_SEQS)

@@ -1,0 +1,432 @@
+// The short causal convolution of a Mamba-2 layer's input side over a packed batch, and its gradients:
+//     s_t[c] = bias[c] + sum_{j<W} w[c][j] x_{t-W+1+j}[c],   y = act(s)
+// with the W - 1 inputs in front of each sequence from a window (or zero), and the last W - 1 inputs as the next window.
+//     e_t = dy_t act'(s_t),  dx_t = sum_n e_{t+n} w[W-1-n] (tokens of the sequence),  dw[j] = sum_t e_t x_{t-W+1+j}
+//
+// Bound by memory: x is read once and y written once. A thread owns eight channels (16 bytes of a 16-bit row) and walks
+// a run of tokens with the last W - 1 inputs in registers, the rows of the next kAhead tokens already asked for; a wavefront
+// covers 512 channels, so each of its loads is one KiB. A run reads the W - 1 rows in front of it again (and, backward, the W - 1
+// behind it). Runs are cut from the packed batch, whatever the sequences' lengths; where a run passes from one sequence to the
+// next its history is loaded anew, a branch that a whole wavefront takes. SiLU and its slope are computed again in the
+// backward pass from x, which costs less than storing s. Weights' gradients are summed over a run in registers, over a
+// workgroup's wavefronts in LDS and over workgroups by a second kernel, in a fixed order.
+#include "act.hpp"
+#include "layer.hpp"
+
+namespace rs {
+
+namespace {
+
+constexpr int kAhead = 8;        // tokens asked for at a time
+constexpr int kConvWaves = 4;    // of a workgroup, each with a run of its own
+constexpr int kConvThreads = kConvWaves * 64;
+
+// A sequence of the packed batch that holds token t, as the tables have it.
+struct ConvSeq {
+  int s, begin, end;
+};
+
+// (t is uniform over the wavefront, and so is everything read here.)
+__device__ __forceinline__ bool conv_seq(const ConvPromptArgs& a, int64_t t, ConvSeq& q) {
+  q.s = a.token_seq[t];
+  if (q.s < 0) return false;
+  bool ok = q.s < a.n_seqs;
+  if (ok) {
+    q.begin = a.cu_tokens[q.s];
+    q.end = a.cu_tokens[q.s + 1];
+    ok = q.begin >= 0 && (int64_t)q.begin <= t && t < (int64_t)q.end && (int64_t)q.end <= a.n_tokens;
+  }
+  if (!ok && (threadIdx.x & 63) == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
+  return ok;
+}
+
+template <typename T, int W>
+struct ConvThread {
+  const ConvPromptArgs& a;
+  const T* x;
+  int c;       // first channel
+  f32x8 w[W];  // w[j]: tap j of the eight channels
+  f32x8 bias;
+  __device__ __forceinline__ ConvThread(const ConvPromptArgs& args, int channel) : a(args), c(channel) {
+    x = static_cast<const T*>(a.x) + c;
+    float all[8 * W];
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) {
+      const f32x4 v = ld4(a.w + (int64_t)c * W + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) all[4 * i + e] = v[e];
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[j][e] = all[e * W + j];
+    bias = a.bias ? load8(a.bias + c) : f32x8{};
+  }
+  // The input at place p (negative: of the window) of a sequence.
+  __device__ __forceinline__ f32x8 input(const ConvSeq& q, int p) const {
+    if (p >= 0) return wide(raw8(x + ((int64_t)q.begin + p) * a.x_stride));
+    if (a.first == nullptr) return f32x8{};
+    return load8(a.first + ((int64_t)q.s * (W - 1) + W - 1 + p) * a.D + c);
+  }
+  // The W - 1 inputs in front of place p.
+  __device__ __forceinline__ void history(const ConvSeq& q, int p, f32x8 (&h)[W]) const {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) h[j] = input(q, p - (W - 1) + j);
+  }
+  // s of the newest input, h[W - 1]
+  __device__ __forceinline__ f32x8 mix(const f32x8 (&h)[W]) const {
+    f32x8 s = bias;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(w[j][e], h[j][e], s[e]);
+    return s;
+  }
+  __device__ __forceinline__ static void shift(f32x8 (&h)[W]) {
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) h[j] = h[j + 1];
+  }
+};
+
+// The last window: workgroups behind those of the runs, a wavefront per sequence and 512 channels.
+template <typename T, int W>
+__device__ __forceinline__ void conv_window(const ConvPromptArgs& a, int s, int unit) {
+  ConvSeq q{s, a.cu_tokens[s], a.cu_tokens[s + 1]};
+  if (q.begin < 0 || q.end < q.begin || (int64_t)q.end > a.n_tokens) {
+    if (unit == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
+    return;
+  }
+  if (a.last == nullptr || 8 * unit >= a.D) return;
+  const T* x = static_cast<const T*>(a.x) + 8 * unit;
+  for (int j = 0; j < W - 1; ++j) {
+    const int p = q.end - q.begin - (W - 1) + j;
+    f32x8 v{};
+    if (p >= 0)
+      v = wide(raw8(x + ((int64_t)q.begin + p) * a.x_stride));
+    else if (a.first)
+      v = load8(a.first + ((int64_t)s * (W - 1) + W - 1 + p) * a.D + 8 * unit);
+    store8(a.last + ((int64_t)s * (W - 1) + j) * a.D + 8 * unit, v);
+  }
+}
+
+// Grid: x over runs of kConvWaves wavefronts (then over sequences, for the windows), y over 512 channels.
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPromptArgs a, int run, int run_groups) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = blockIdx.y * 64 + (threadIdx.x & 63);
+  if ((int)blockIdx.x >= run_groups) {
+    const int s = ((int)blockIdx.x - run_groups) * kConvWaves + wave;
+    if (s < a.n_seqs) conv_window<T, W>(a, s, unit);
+    return;
+  }
+  const int64_t t0 = ((int64_t)blockIdx.x * kConvWaves + wave) * run;
+  const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
+  if (t0 >= t1) return;
+  const bool live = 8 * unit < a.D;
+  const ConvThread<T, W> th(a, live ? 8 * unit : a.D - 8);
+  T* y = static_cast<T*>(a.y) + th.c;
+  f32x8 h[W];
+  ConvSeq q;
+  bool ok = conv_seq(a, t0, q);
+  if (ok) th.history(q, (int)(t0 - q.begin), h);
+  Eight<T> next[kAhead];
+  const auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) next[i] = raw8(th.x + (t + i < a.n_tokens ? t + i : a.n_tokens - 1) * a.x_stride);
+  };
+  fetch(t0);
+  for (int64_t t = t0; t < t1; t += kAhead) {
+    Eight<T> now[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) now[i] = next[i];
+    if (t + kAhead < t1) fetch(t + kAhead);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (t + i < t1) {
+        if (t + i > t0 && (!ok || t + i >= q.end)) {
+          ok = conv_seq(a, t + i, q);
+          if (ok) th.history(q, (int)(t + i - q.begin), h);
+        }
+        if (ok) {
+          h[W - 1] = wide(now[i]);
+          f32x8 s = th.mix(h);
+          if (SILU) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] *= sigmoid<sizeof(T) == 4>(s[e]);
+          }
+          if (live) store8(y + (t + i) * a.D, s);
+          th.shift(h);
+        }
+      }
+    }
+  }
+}
+
+// The gradient of a sequence's first window: what the first W - 1 tokens take from it, and what of it is still in the last one.
+template <typename T, int W, bool SILU>
+__device__ __forceinline__ void conv_dfirst(const ConvPromptArgs& a, int s, int unit) {
+  const ConvSeq q{s, a.cu_tokens[s], a.cu_tokens[s + 1]};
+  if (q.begin < 0 || q.end < q.begin || (int64_t)q.end > a.n_tokens) {
+    if (unit == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
+    return;
+  }
+  if (a.dfirst == nullptr || 8 * unit >= a.D) return;
+  const ConvThread<T, W> th(a, 8 * unit);
+  const T* dy = static_cast<const T*>(a.dy) + th.c;
+  const int n = q.end - q.begin;
+  f32x8 d[W], h[W];
+#pragma unroll
+  for (int r = 0; r < W; ++r) d[r] = f32x8{};
+  th.history(q, 0, h);
+#pragma unroll
+  for (int p = 0; p < W - 1; ++p) {
+    if (p < n) {
+      h[W - 1] = th.input(q, p);
+      f32x8 e = wide(raw8(dy + ((int64_t)q.begin + p) * a.D));
+      if (SILU) {
+        const f32x8 z = th.mix(h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] *= silu<sizeof(T) == 4>(z[i]).slope;
+      }
+      th.shift(h);
+#pragma unroll
+      for (int r = p; r < W - 1; ++r) d[r] += e * th.w[r - p];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < W - 1; ++r) {
+    if (a.dlast && r >= n) d[r] += load8(a.dlast + ((int64_t)s * (W - 1) + r - n) * a.D + th.c);
+    store8(a.dfirst + ((int64_t)s * (W - 1) + r) * a.D + th.c, d[r]);
+  }
+}
+
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(const ConvPromptArgs a, int run, int run_groups) {
+  __shared__ __align__(16) float sums[kConvWaves][64 * 8];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = blockIdx.y * 64 + lane;
+  if ((int)blockIdx.x >= run_groups) {
+    const int s = ((int)blockIdx.x - run_groups) * kConvWaves + wave;
+    if (s < a.n_seqs) conv_dfirst<T, W, SILU>(a, s, unit);
+    return;
+  }
+  const bool live = 8 * unit < a.D;
+  const ConvThread<T, W> th(a, live ? 8 * unit : a.D - 8);
+  const T* dy = static_cast<const T*>(a.dy) + th.c;
+  T* dx = static_cast<T*>(a.dx) + th.c;
+  f32x8 dw[W], db{};
+#pragma unroll
+  for (int j = 0; j < W; ++j) dw[j] = f32x8{};
+  // runs of this wavefront
+  for (int64_t t0 = ((int64_t)blockIdx.x * kConvWaves + wave) * run; t0 < a.n_tokens; t0 += (int64_t)run_groups * kConvWaves * run) {
+    const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
+    int64_t at = t0;
+    while (at < t1) {
+      ConvSeq q;
+      if (!conv_seq(a, at, q)) {
+        ++at;
+        continue;
+      }
+      // tokens at .. to - 1 of sequence q: their dx, and their part of the weights' gradients
+      const int64_t to = t1 < q.end ? t1 : q.end;
+      f32x8 h[W], e[W];  // e[W - 1]: of the newest token
+      th.history(q, (int)(at - q.begin), h);
+#pragma unroll
+      for (int j = 0; j < W; ++j) e[j] = f32x8{};
+      Eight<T> xn[kAhead], dn[kAhead];
+      const auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int64_t r = t + i < a.n_tokens ? t + i : a.n_tokens - 1;
+          xn[i] = raw8(th.x + r * a.x_stride);
+          dn[i] = raw8(dy + r * a.D);
+        }
+      };
+      fetch(at);
+      const int64_t stop = to + W - 1;
+      for (int64_t t = at; t < stop; t += kAhead) {
+        Eight<T> xs[kAhead], ds[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          xs[i] = xn[i];
+          ds[i] = dn[i];
+        }
+        if (t + kAhead < stop) fetch(t + kAhead);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (t + i < stop) {
+            f32x8 g{};
+            if (t + i < q.end) {
+              h[W - 1] = wide(xs[i]);
+              g = wide(ds[i]);
+              if (SILU) {
+                const f32x8 z = th.mix(h);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) g[c] *= silu<sizeof(T) == 4>(z[c]).slope;
+              }
+              if (t + i < to) {
+                db += g;
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) dw[j][c] = __builtin_fmaf(g[c], h[j][c], dw[j][c]);
+              }
+              th.shift(h);
+            }
+            th.shift(e);
+            e[W - 1] = g;
+            const int64_t done = t + i - (W - 1);
+            if (done >= at) {
+              f32x8 d{};
+#pragma unroll
+              for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] = __builtin_fmaf(e[j][c], th.w[W - 1 - j][c], d[c]);
+              const int row = (int)(done - q.end) + W - 1;  // of the last window
+              if (a.dlast && row >= 0) d += load8(a.dlast + ((int64_t)q.s * (W - 1) + row) * a.D + th.c);
+              if (live) store8(dx + done * a.D, d);
+            }
+          }
+        }
+      }
+      at = to;
+    }
+  }
+  if (a.partial == nullptr) return;
+  float* part = a.partial + (int64_t)blockIdx.x * (W + 1) * a.D;
+#pragma unroll
+  for (int j = 0; j <= W; ++j) {
+    store8(&sums[wave][lane * 8], j < W ? dw[j < W ? j : 0] : db);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 512; c += kConvThreads) {
+      const int channel = blockIdx.y * 512 + c;
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < kConvWaves; ++v) s += sums[v][c];
+      if (channel < a.D) part[(int64_t)j * a.D + channel] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// dw and dbias from the workgroups' sums.
+__global__ void __launch_bounds__(256) conv_weights_kernel(const ConvPromptArgs a, int parts) {
+  __shared__ float sums[16][17];
+  const int i = blockIdx.x * 16 + (threadIdx.x & 15), r = threadIdx.x >> 4;
+  const int columns = (a.W + 1) * a.D;
+  float s = 0.f;
+  if (i < columns)
+    for (int p = r; p < parts; p += 16) s += a.partial[(int64_t)p * columns + i];
+  sums[r][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (r == 0 && i < columns) {
+    float total = 0.f;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) total += sums[p][threadIdx.x];
+    const int j = i / a.D, c = i - j * a.D;
+    if (j < a.W) {
+      if (a.dw) a.dw[(int64_t)c * a.W + j] = total;
+    } else if (a.dbias) {
+      a.dbias[c] = total;
+    }
+  }
+}
+
+struct ConvPlan {
+  int run, groups;  // tokens of a run; workgroups of kConvWaves runs
+};
+
+// Tokens a wavefront walks: 32 where that still leaves four wavefronts a SIMD, so that the rows read twice are a tenth; eight
+// where the batch is small and every wavefront counts.
+ConvPlan conv_plan(int64_t n_tokens, int D) {
+  const int64_t columns = (D + 511) / 512;
+  ConvPlan p;
+  p.run = n_tokens / 32 * columns >= 4096 ? 32 : kAhead;
+  p.groups = (int)((n_tokens + p.run * kConvWaves - 1) / (p.run * kConvWaves));
+  return p;
+}
+
+// Backward: at most two thousand workgroups in all, each of which writes one row of weights' gradients per channel.
+ConvPlan conv_backward_plan(int64_t n_tokens, int D) {
+  const int64_t columns = (D + 511) / 512;
+  ConvPlan p;
+  p.run = n_tokens / 64 * columns >= 2048 ? 64 : n_tokens / 32 * columns >= 2048 ? 32 : kAhead;
+  const int64_t all = (n_tokens + p.run * kConvWaves - 1) / (p.run * kConvWaves);
+  int64_t most = 2048 / columns;
+  if (most < 1) most = 1;
+  p.groups = (int)(all < most ? all : most);
+  return p;
+}
+
+template <typename T, int W, bool SILU>
+hipError_t conv_start(const ConvPromptArgs& a, bool backward, hipStream_t s) {
+  const ConvPlan p = backward ? conv_backward_plan(a.n_tokens, a.D) : conv_plan(a.n_tokens, a.D);
+  const dim3 grid((unsigned)(p.groups + (a.n_seqs + kConvWaves - 1) / kConvWaves), (unsigned)((a.D + 511) / 512));
+  if (!backward) {
+    conv_prompt_kernel<T, W, SILU><<<grid, dim3(kConvThreads), 0, s>>>(a, p.run, p.groups);
+    return hipGetLastError();
+  }
+  conv_prompt_backward_kernel<T, W, SILU><<<grid, dim3(kConvThreads), 0, s>>>(a, p.run, p.groups);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.partial == nullptr) return e;
+  conv_weights_kernel<<<dim3((unsigned)(((W + 1) * a.D + 15) / 16)), dim3(256), 0, s>>>(a, p.groups);
+  return hipGetLastError();
+}
+
+template <typename T, int W>
+hipError_t conv_act(const ConvPromptArgs& a, bool backward, hipStream_t s) {
+  return a.silu ? conv_start<T, W, true>(a, backward, s) : conv_start<T, W, false>(a, backward, s);
+}
+
+template <typename T>
+hipError_t conv_width(const ConvPromptArgs& a, bool backward, hipStream_t s) {
+  switch (a.W) {
+    case 1: return conv_act<T, 1>(a, backward, s);
+    case 2: return conv_act<T, 2>(a, backward, s);
+    case 3: return conv_act<T, 3>(a, backward, s);
+    default: return conv_act<T, 4>(a, backward, s);
+  }
+}
+
+hipError_t conv_prompt(const ConvPromptArgs& a, bool backward, hipStream_t s) {
+  switch (a.dtype) {
+    case REPLAYSSM_BF16: return conv_width<__bf16>(a, backward, s);
+    case REPLAYSSM_F16: return conv_width<_Float16>(a, backward, s);
+    default: return conv_width<float>(a, backward, s);
+  }
+}
+
+// A decode ring's sequences from windows: the W - 1 inputs at the ring's first slots, nothing pending.
+__global__ void __launch_bounds__(256) conv_restore_kernel(const ConvRestoreArgs a) {
+  const int b = a.seqs[blockIdx.y];
+  if (b < 0 || b >= a.B) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, REPLAYSSM_DEVERR_INDEX);
+    return;
+  }
+  const int64_t size = (int64_t)(a.W - 1) * a.D;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i < size) st4(a.ring + (int64_t)b * a.Cc * a.D + i, ld4(a.windows + blockIdx.y * size + i));
+  if (i == 0) {
+    a.start[b] = 0;
+    a.pend[b] = 0;
+  }
+}
+
+}  // namespace
+
+int64_t conv_prompt_backward_bytes(const replayssm_conv_prompt_config& c) {
+  return (int64_t)conv_backward_plan(c.n_tokens, c.D).groups * (c.W + 1) * c.D * 4;
+}
+
+hipError_t launch_conv_prompt(const ConvPromptArgs& a, hipStream_t s) { return conv_prompt(a, false, s); }
+hipError_t launch_conv_prompt_backward(const ConvPromptArgs& a, hipStream_t s) { return conv_prompt(a, true, s); }
+
+hipError_t launch_conv_restore(const ConvRestoreArgs& a, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  const int64_t size = (int64_t)(a.W - 1) * a.D / 4;
+  const int64_t blocks = size > 0 ? (size + 255) / 256 : 1;
+  conv_restore_kernel<<<dim3((unsigned)blocks, (unsigned)a.n), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace rs

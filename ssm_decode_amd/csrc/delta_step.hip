@@ -1,5 +1,5 @@
-// The gated delta rule token by token, on a pool of states:
-//     S_t = e^g S_{t-1} + u k^T,   u = beta (v - e^g S_{t-1} k),   o = scale S_t q
+// The gated delta rule and linear attention token by token, on a pool of states:
+//     S_t = e^g S_{t-1} + u k^T,   u = beta (v - e^g S_{t-1} k)  or  beta v,   o = scale S_t q [+ skip v]
 // for the few new tokens (usually one) of every sequence of a packed batch.
 //
 // With one token per sequence it reads and writes each state once (128 KB per head at
@@ -41,7 +41,8 @@ __device__ __forceinline__ void load_row(const T* p, float (&x)[N]) {
   }
 }
 
-template <typename T, int DK>
+// DELTA: the delta rule; otherwise linear attention, whose beta may be missing (1) and which adds skip v.
+template <typename T, int DK, bool DELTA>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArgs a) {
   using Sh = StepShape<DK>;
   const int slices = (a.dv + Sh::kRows - 1) / Sh::kRows;
@@ -95,12 +96,13 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
   const T* k = static_cast<const T*>(a.k) + (int64_t)hk * DK + sub * Sh::kFloats;
   const T* v = static_cast<const T*>(a.v) + (int64_t)h * a.dv + row0;
   T* out = static_cast<T*>(a.out) + (int64_t)h * a.dv + row0;
+  const float skip = !DELTA && a.skip ? a.skip[h] : 0.f;
   for (int64_t t = begin; t < end; ++t) {
     float qr[Sh::kFloats], kr[Sh::kFloats];
     load_row<Sh::kFloats>(q + t * a.q_stride, qr);
     load_row<Sh::kFloats>(k + t * a.k_stride, kr);
     const float decay = expf(a.g[t * a.H + h]);
-    const float beta = a.beta[t * a.H + h];
+    const float beta = DELTA || a.beta ? a.beta[t * a.H + h] : 1.f;
 #pragma unroll
     for (int i = 0; i < Sh::kIter; ++i) {
       const float vv = (float)v[t * a.v_stride + i];
@@ -108,9 +110,9 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
 #pragma unroll
       for (int e = 0; e < Sh::kFloats; ++e) {
         S[i][e] *= decay;
-        sk = __builtin_fmaf(S[i][e], kr[e], sk);
+        if (DELTA) sk = __builtin_fmaf(S[i][e], kr[e], sk);
       }
-      const float u = beta * (vv - sum_width<Sh::kLanes>(sk));
+      const float u = beta * (DELTA ? vv - sum_width<Sh::kLanes>(sk) : vv);
       float sq = 0.f;
 #pragma unroll
       for (int e = 0; e < Sh::kFloats; ++e) {
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
         sq = __builtin_fmaf(S[i][e], qr[e], sq);
       }
       sq = sum_width<Sh::kLanes>(sq) * a.scale;
+      if (!DELTA) sq = __builtin_fmaf(skip, vv, sq);
       if (sub == 0) out[t * a.H * a.dv + i] = (T)sq;
     }
   }
@@ -130,31 +133,35 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaArg
                  f32x4{S[i][4 * c], S[i][4 * c + 1], S[i][4 * c + 2], S[i][4 * c + 3]});
 }
 
-template <typename T, int DK>
+template <typename T, int DK, bool DELTA>
 hipError_t launch_step(const DeltaArgs& a, hipStream_t s) {
   const int slices = (a.dv + StepShape<DK>::kRows - 1) / StepShape<DK>::kRows;
-  delta_step_kernel<T, DK><<<dim3((unsigned)((int64_t)a.n_seqs * a.H * slices)), dim3(kStepThreads), 0, s>>>(a);
+  delta_step_kernel<T, DK, DELTA><<<dim3((unsigned)((int64_t)a.n_seqs * a.H * slices)), dim3(kStepThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool DELTA>
 hipError_t launch_dk(const DeltaArgs& a, hipStream_t s) {
   switch (a.dk) {
-    case 16: return launch_step<T, 16>(a, s);
-    case 32: return launch_step<T, 32>(a, s);
-    case 64: return launch_step<T, 64>(a, s);
-    default: return launch_step<T, 128>(a, s);
+    case 16: return launch_step<T, 16, DELTA>(a, s);
+    case 32: return launch_step<T, 32, DELTA>(a, s);
+    case 64: return launch_step<T, 64, DELTA>(a, s);
+    default: return launch_step<T, 128, DELTA>(a, s);
+  }
+}
+
+template <bool DELTA>
+hipError_t launch_type(const DeltaArgs& a, hipStream_t s) {
+  switch (a.dtype) {
+    case REPLAYSSM_BF16: return launch_dk<__bf16, DELTA>(a, s);
+    case REPLAYSSM_F16: return launch_dk<_Float16, DELTA>(a, s);
+    default: return launch_dk<float, DELTA>(a, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t s) {
-  switch (a.dtype) {
-    case REPLAYSSM_BF16: return launch_dk<__bf16>(a, s);
-    case REPLAYSSM_F16: return launch_dk<_Float16>(a, s);
-    default: return launch_dk<float>(a, s);
-  }
-}
+hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t s) { return launch_type<true>(a, s); }
+hipError_t launch_linear_step(const DeltaArgs& a, hipStream_t s) { return launch_type<false>(a, s); }
 
 }  // namespace rs

@@ -1,4 +1,4 @@
-// What the C entry points share on the host: status text, pointer checks (not installed).
+// What the C entry points share on the host: status text, checks of pointers, types and strides (not installed).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -30,6 +30,23 @@ inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s);
     if ((ptr) == nullptr) return fail(REPLAYSSM_EINVAL, "%s is NULL", #ptr);        \
     if (!aligned(ptr)) return fail(REPLAYSSM_EINVAL, "%s is not 16-byte aligned", #ptr); \
   } while (0)
+
+inline int element_bytes(int dtype) { return dtype == REPLAYSSM_F32 ? 4 : 2; }
+
+inline int check_dtype(int dtype, const char* name) {
+  if (dtype != REPLAYSSM_F32 && dtype != REPLAYSSM_BF16 && dtype != REPLAYSSM_F16)
+    return fail(REPLAYSSM_EINVAL, "%s %d unknown", name, dtype);
+  return REPLAYSSM_OK;
+}
+
+// Elements between tokens: at least the row, whole 16-byte units.
+inline int check_stride(int64_t stride, int64_t row, int dtype, const char* name) {
+  if (stride < row || stride > (int64_t)1 << 31)
+    return fail(REPLAYSSM_EINVAL, "%s=%lld outside %lld..2^31", name, (long long)stride, (long long)row);
+  if (stride * element_bytes(dtype) % 16 != 0)
+    return fail(REPLAYSSM_EINVAL, "%s=%lld is not a multiple of 16 bytes", name, (long long)stride);
+  return REPLAYSSM_OK;
+}
 
 }  // namespace host
 }  // namespace rs

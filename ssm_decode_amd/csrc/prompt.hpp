@@ -48,7 +48,8 @@ struct DeltaArgs {
   const void* k;
   const void* v;      // rows [H][dv] per token
   const float* g;     // [n_tokens][H]
-  const float* beta;  // [n_tokens][H]
+  const float* beta;  // [n_tokens][H] (linear attention: or NULL)
+  const float* skip;  // linear attention: [H] or NULL
   const float* S0;    // [n_seqs][H][dv][dk] or NULL
   void* out;          // [n_tokens][H][dv]
   float* S_out;       // like S0, or NULL
@@ -82,6 +83,8 @@ hipError_t launch_qk_norm_backward(const QkNormArgs& a, hipStream_t s);
 // Workgroups of the backward kernel that write a row of partial weight gradients each.
 int qk_norm_partials(int n_tokens, int Hq, int Hk, int D);
 hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t s);
+// Linear attention's step (a delta rule's arguments, without its correction).
+hipError_t launch_linear_step(const DeltaArgs& a, hipStream_t s);
 int64_t delta_forward_bytes(const replayssm_delta_config& c, int max_blocks);
 int64_t delta_backward_bytes(const replayssm_delta_config& c, int max_blocks);
 hipError_t launch_delta_prompt(const DeltaArgs& a, hipStream_t s);
