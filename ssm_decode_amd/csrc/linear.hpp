@@ -22,6 +22,8 @@
 // differences of long sums.
 #pragma once
 
+#include <type_traits>
+
 #include "chunk.hpp"
 #include "layer.hpp"
 
@@ -31,11 +33,13 @@ namespace {
 
 constexpr int kRows = kBlock;
 
-// Tiles of 16 state rows (dv) that a wavefront holds: its slice of a head.
+// State rows (dv) that a wavefront holds, its slice of a head: two tiles of 16. (With four, which would share a block's scores among
+// twice the rows, the state and a block's results left the scheduler no registers at two wavefronts a SIMD, and it spilled.)
+constexpr int kTiles = 2;
+constexpr int kSlice = kTiles * 16;
+// Wavefronts of a workgroup, which share their key head's rows: all that fit LDS beside them.
 template <typename T>
-constexpr int kTiles = sizeof(T) == 2 && Parts<T>::in == 1 ? 4 : 2;
-template <typename T>
-constexpr int kSlice = kTiles<T> * 16;
+constexpr int kWaves = sizeof(T) == 4 ? 4 : 8;
 
 // A segment of a sequence: its tokens, its place, and whether the tables are sound.
 struct Segment {
@@ -108,66 +112,251 @@ struct Blocks {
   __device__ __forceinline__ int64_t token(int r) const { return reverse ? t0 + n - 1 - r : t0 + r; }
 };
 
+// 2^t with the fp32 remainder of t to first order: two ulp whatever the size of t, where 2^(float)t would be off by |t| 2^-24.
+__device__ __forceinline__ float decay_of(double t) {
+  const float hi = (float)t, lo = (float)(t - (double)hi);
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return __builtin_fmaf(e, lo * 0.69314718055994531f, e);
+}
+constexpr double kLog2e = 1.4426950408889634;
+
 // A block's scalars of one head, by row.
 struct RowScalars {
-  double G[kRows];     // running decay exponent
+  double G[kRows];     // running decay exponent, to base 2
   float first[kRows];  // e^{G_r}
   float last[kRows];   // e^{G_end - G_r} times z's weight
-  float col[kRows];    // z's weight
   float row[kRows];    // the results' weight (0 behind the last row)
 };
 
-// One wavefront fills them, lane r for row r, and returns G_end.
-__device__ __forceinline__ double row_scalars(const LinearArgs& a, const Side& d, const Blocks& b, int seq_end, int h, RowScalars* out) {
-  const int lane = threadIdx.x & 63;
-  const bool live = lane < b.n;
-  const int64_t t = live ? b.token(lane) : b.t0;
-  // backwards the decay between a token and the one walked before it is that one's own
-  const int64_t tg = d.reverse ? t + 1 : t;
-  double sum = live && tg < seq_end ? (double)closed_gate(a.g[tg * a.H + h]) : 0.0;
-  const float col = !live ? 0.f : d.beta ? d.beta[t * a.H + h] : d.weight;
-  const float row = !live ? 0.f : d.row ? d.row[t * a.H + h] : d.row_weight;
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const double up = __shfl_up(sum, s);
-    if (lane >= s) sum += up;
-  }
-  const double end = __shfl(sum, 63);
-  out->G[lane] = sum;
-  out->first[lane] = expf((float)sum);
-  out->last[lane] = expf((float)(end - sum)) * col;
-  out->col[lane] = col;
-  out->row[lane] = row;
-  return end;
+// The weights of a block's pairs, e^{G_r - G_c} col_c for c <= r, without an exponential for each and without a factor
+// above one, which could overflow: pairs of different eights of rows pass by the end of c's eight,
+//     e^{G_r - G_{8 c/8 + 7}} * tail[c],  tail[c] = e^{G_{8 c/8 + 7} - G_c} col_c,
+// pairs of one eight are in a table of their own (zero for c > r).
+struct PairScalars : RowScalars {
+  float tail[kRows];
+  float near[kRows][8];
+};
+
+// x of the lane d in front in its row of 16, 0 in front of the row.
+template <int D>
+__device__ __forceinline__ double row_shift(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x110 + D, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x110 + D, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sums of the lanes up to each.
+__device__ __forceinline__ double running_sum(double x) {
+  x += row_shift<1>(x);
+  x += row_shift<2>(x);
+  x += row_shift<4>(x);
+  x += row_shift<8>(x);
+  const double a = lane_value(x, 15), b = a + lane_value(x, 31), c = b + lane_value(x, 47);
+  const int row = (threadIdx.x & 63) >> 4;
+  return x + (row == 0 ? 0.0 : row == 1 ? a : row == 2 ? b : c);
 }
 
-// Rows of one block into a tile in parts, by all `threads` threads: W columns of which DK exist.
-template <typename T, int DK, int W>
-__device__ __forceinline__ void stage_rows(const Tile<W, Parts<T>::in>& tile, const T* p, int64_t stride, const Blocks& b, int threads) {
-  constexpr int kUnits = kRows * (W / 8);
-  const T* base = p + b.token(0) * stride;
-  const int64_t step = b.reverse ? -stride : stride;
-  for (int u0 = threadIdx.x; u0 < kUnits; u0 += 4 * threads) {
-    Raw8<T> x[4];
+// Makes them for one wavefront's head, lane r for row r: what they are made of is asked for a block ahead.
+struct ScalarFeed {
+  const float *g, *col_from, *row_from;  // of the head
+  int64_t step;                          // tokens lie so many entries apart
+  float col_weight, row_weight;
+  int end;  // the sequence's
+  bool reverse;
+  float gate, col, row;
+  __device__ __forceinline__ ScalarFeed(const LinearArgs& a, const Side& d, int h, int seq_end)
+      : g(a.g + h), col_from(d.beta ? d.beta + h : nullptr), row_from(d.row ? d.row + h : nullptr), step(a.H), col_weight(d.weight),
+        row_weight(d.row_weight), end(seq_end), reverse(d.reverse) {}
+  __device__ __forceinline__ void load(const Blocks& b) {
+    const int lane = threadIdx.x & 63;
+    const bool live = lane < b.n;
+    const int64_t t = live ? b.token(lane) : b.t0;
+    // backwards the decay between a token and the one walked before it is that one's own
+    const int64_t tg = reverse ? t + 1 : t;
+    gate = live && tg < end ? g[tg * step] : 0.f;
+    col = !live ? 0.f : col_from ? col_from[t * step] : col_weight;
+    row = !live ? 0.f : row_from ? row_from[t * step] : row_weight;
+  }
+  // returns the block's whole exponent
+  template <typename Scalars>
+  __device__ __forceinline__ double make(Scalars* out) const {
+    const int lane = threadIdx.x & 63;
+    const double sum = running_sum((double)closed_gate(gate) * kLog2e);
+    const double whole = lane_value(sum, 63);
+    out->G[lane] = sum;
+    out->first[lane] = decay_of(sum);
+    out->last[lane] = decay_of(whole - sum) * col;
+    out->row[lane] = row;
+    if constexpr (std::is_same_v<Scalars, PairScalars>) {
+      // (the pairs' table first holds the columns' weights)
+      out->tail[lane] = col;
+      const double* G = out->G + (lane & ~7);
+      const f32x8 cols = load8(out->tail + (lane & ~7));
+      f32x8 near;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = u0 + i * threads, row = u / (W / 8), chunk = u % (W / 8);
-      if (u < kUnits && row < b.n && chunk * 8 < DK)
-        x[i].load(base + row * step + chunk * 8);
-      else
-        x[i].zero();
+      for (int e = 0; e < 8; ++e) {
+        const float w = decay_of(sum - G[e]) * cols[e];
+        near[e] = e <= (lane & 7) ? w : 0.f;
+      }
+      store8(out->near[lane], near);
+      out->tail[lane] = decay_of(G[7] - sum) * col;
     }
+    return whole;
+  }
+};
+
+// The eight weights of row r = 16 rt + n and columns 32 ks + 8 g .., up to the factor that pair_scale gives.
+__device__ __forceinline__ f32x8 pair_weights(const PairScalars* s, int rt, int ks, int n, int g) {
+  const int r = 16 * rt + n, eight = 4 * ks + g;
+  return load8(eight == r >> 3 ? s->near[r] : s->tail + 8 * eight);
+}
+// Gr: G of row r
+__device__ __forceinline__ float pair_scale(const PairScalars* s, double Gr, int rt, int ks, int n, int g) {
+  const int mine = (16 * rt + n) >> 3, eight = 4 * ks + g;
+  const float far = decay_of(Gr - s->G[8 * eight + 7]);
+  return eight == mine ? 1.f : eight < mine ? far : 0.f;
+}
+
+// Nothing is moved across it: in these unrolled kernels the scheduler would otherwise ask for the operands of many steps at once,
+// which does not fit the registers beside a state.
+__device__ __forceinline__ void step_ends() { __builtin_amdgcn_sched_barrier(0); }
+
+// x, of which the compiler forgets that it does not change: what is computed from it in a loop stays in the loop. (Of the hundred
+// addresses in LDS that a block takes, each one exclusive-or away from a lane's few, it would keep every one in a register.)
+__device__ __forceinline__ void fresh(int& x) { asm volatile("" : "+v"(x)); }
+
+// A lane's places in a tile of parts, from which each operand is one exclusive-or and a constant away: the tile's key touches the
+// same bits of an address as the column does.
+template <int W, int N>
+struct Reader {
+  using T = Tile<W, N>;
+  static constexpr int kRow = T::kRowBytes;
+  const char* base;
+  int row_[2], dealt_[2], col_[2];
+  __device__ __forceinline__ Reader(const T& t, int lane) : base(t.base) {
+    const int n = lane & 15, g = lane >> 4, e = (lane >> 2) & 3, c = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = u0 + i * threads;
-      if (u < kUnits) tile.put(u / (W / 8), u % (W / 8), x[i].split());
+    for (int i = 0; i < 2; ++i) {
+      row_[i] = T::at(16 * i + n, g);
+      dealt_[i] = T::at(8 * (n >> 2) + 4 * i + (n & 3), g);
+      col_[i] = T::at(8 * g + e + 4 * i, c);
     }
   }
+  __device__ __forceinline__ void at(const T& t) { base = t.base; }
+  // at the top of a loop: the places that its operands use
+  __device__ __forceinline__ void rows() { fresh(row_[0]), fresh(row_[1]); }
+  __device__ __forceinline__ void dealts() { fresh(dealt_[0]), fresh(dealt_[1]); }
+  __device__ __forceinline__ void columns() { fresh(col_[0]), fresh(col_[1]); }
+  __device__ __forceinline__ Split<N> read(int at) const {
+    Split<N> s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s.p[i] = *reinterpret_cast<const bf16x8*>(base + at + i * T::kPlane);
+    return s;
+  }
+  // as Tile::row8 of row 16 rt + n, and of row dealt(t, n)
+  __device__ __forceinline__ Split<N> row(int rt, int k) const { return read((row_[rt & 1] ^ (k << 6)) + (rt >> 1) * 32 * kRow); }
+  __device__ __forceinline__ Split<N> dealt_row(int t, int k) const { return read((dealt_[t & 1] ^ (k << 6)) + (t >> 1) * 32 * kRow); }
+  // as Tile::col8<true>(t, ks)
+  __device__ __forceinline__ Split<N> column(int t, int ks) const {
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    const int more = (t & 1) * 8 + ks * 32 * kRow;
+    const char* lo = base + (col_[0] ^ ((t >> 1) << 6)) + more;
+    const char* hi = base + (col_[1] ^ ((t >> 1) << 6)) + more;
+    Split<N> s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lo + i * T::kPlane));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(hi + i * T::kPlane));
+      s.p[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    return s;
+  }
+};
+
+// 16 bytes of every lane straight into LDS, to `to` (uniform) + 16 lane.
+__device__ __forceinline__ void copy16(const void* from, char* to) {
+  typedef __attribute__((address_space(1))) const void* global_ptr;
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
 }
+// A wavefront's copies have landed.
+__device__ __forceinline__ void copies_landed() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// bf16 rows are copied straight into LDS, the lanes' source chunks exchanged as the tile's are; a block's missing rows, and types
+// and widths that change on the way, go through registers.
+template <typename T, int DK>
+constexpr bool kCopied = sizeof(T) == 2 && Parts<T>::in == 1 && DK >= 32;
+
+// A lane's part in copying rows of W bf16 columns: a wavefront's instruction takes a piece of kStep rows. (The key of row kStep j
+// + r is that of kStep j exclusive-or that of r.)
+template <int W>
+struct Copier {
+  static constexpr int kChunks = W / 8, kStep = 64 / kChunks, kPieces = kRows / kStep;
+  int64_t offset;  // of the lane's row in the piece, in bytes
+  int chunk;
+  __device__ __forceinline__ Copier(int64_t step) {
+    const int lane = threadIdx.x & 63, row = lane / kChunks;
+    offset = row * step * 2;
+    chunk = ((lane % kChunks) ^ Tile<W, 1>::key(row)) * 16;
+  }
+  // base: row 0; step: elements from row to row
+  __device__ __forceinline__ void copy(const void* base, int64_t step, int piece, char* tile) const {
+    const char* p = static_cast<const char*>(base) + (int64_t)(piece * kStep) * step * 2 + offset;
+    copy16(p + (chunk ^ (Tile<W, 1>::key(piece * kStep) * 16)), tile + piece * 1024);
+  }
+};
+
+// Rows of one block into a tile in parts, by a workgroup of `threads` threads: W columns of which DK exist. step: elements
+// from row to row in walking order.
+template <typename T, int DK>
+struct RowFeed {
+  static constexpr int W = kWide<DK>;
+  using Rows = Tile<W, Parts<T>::in>;
+  const T* p;
+  int64_t stride, step;
+  Copier<W> copier;
+  __device__ __forceinline__ RowFeed(const T* rows, int64_t s, bool reverse) : p(rows), stride(s), step(reverse ? -s : s), copier(step) {}
+  __device__ __forceinline__ void stage(const Rows& tile, const Blocks& b, int wave, int threads) {
+    const T* base = p + b.token(0) * stride;
+    if constexpr (kCopied<T, DK>) {
+      if (b.n == kRows) {
+        fresh(copier.chunk);
+        for (int i = wave; i < Copier<W>::kPieces; i += threads / 64) copier.copy(base, step, i, tile.base);
+        return;
+      }
+    }
+    // (a few at a time: in front of the copies' path registers are dear)
+    constexpr int kChunks = W / 8, kUnits = kRows * kChunks, kBatch = kCopied<T, DK> ? 1 : 4;
+    int u0 = threadIdx.x;
+    fresh(u0);
+#pragma unroll 1
+    for (; u0 < kUnits; u0 += kBatch * threads) {
+      Raw8<T> x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = u0 + i * threads, row = u / kChunks, chunk = u % kChunks;
+        if (u < kUnits && row < b.n && chunk * 8 < DK)
+          x[i].load(base + row * step + chunk * 8);
+        else
+          x[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = u0 + i * threads;
+        if (u < kUnits) tile.put(u / kChunks, u % kChunks, x[i].split());
+      }
+    }
+  }
+};
 
 // A wavefront's own rows of z (a slice of a head's channels, `columns` of which exist) in their own type.
 template <typename T>
-using Values = ColumnTile<T, kSlice<T>>;
+using Values = ColumnTile<T, kSlice>;
 
 template <typename T>
 __device__ __forceinline__ void put_value(const Values<T>& v, int row, int chunk, const Raw8<T>& x) {
@@ -190,27 +379,85 @@ __device__ __forceinline__ Raw8<T> value_row(const Values<T>& v, int row, int ks
   return x;
 }
 
+// Brings a wavefront's rows of z, `columns` of whose kSlice exist.
 template <typename T>
-__device__ __forceinline__ void stage_values(const Values<T>& v, const T* p, int64_t stride, const Blocks& b, int columns) {
-  constexpr int kChunks = kSlice<T> / 8, kPer = kRows * kChunks / 64;
-  const int lane = threadIdx.x & 63;
-  const T* base = p + b.token(0) * stride;
-  const int64_t step = b.reverse ? -stride : stride;
-  Raw8<T> x[kPer];
+struct ValueFeed {
+  const T* p;
+  int64_t stride, step;
+  int columns;
+  Copier<kSlice> copier;  // (bf16)
+  __device__ __forceinline__ ValueFeed(const T* rows, int64_t s, bool reverse, int c)
+      : p(rows), stride(s), step(reverse ? -s : s), columns(c), copier(step) {}
+  __device__ __forceinline__ void stage(const Values<T>& tile, const Blocks& b) {
+    const T* base = p + b.token(0) * stride;
+    if constexpr (kCopied<T, 32>) {
+      if (b.n == kRows && columns == kSlice) {
+        fresh(copier.chunk);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int u = i * 64 + lane, row = u / kChunks, chunk = u % kChunks;
-    if (row < b.n && chunk * 8 < columns)
-      x[i].load(base + row * step + chunk * 8);
+        for (int i = 0; i < Copier<kSlice>::kPieces; ++i) copier.copy(base, step, i, tile.tile.base);
+        return;
+      }
+    }
+    constexpr int kChunks = kSlice / 8, kUnits = kRows * kChunks, kBatch = kCopied<T, 32> ? 1 : 4;
+    int u0 = threadIdx.x & 63;
+    fresh(u0);
+#pragma unroll 1
+    for (; u0 < kUnits; u0 += kBatch * 64) {
+      Raw8<T> x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = u0 + i * 64, row = u / kChunks, chunk = u % kChunks;
+        if (row < b.n && chunk * 8 < columns)
+          x[i].load(base + row * step + chunk * 8);
+        else
+          x[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) put_value<T>(tile, (u0 + i * 64) / kChunks, (u0 + i * 64) % kChunks, x[i]);
+    }
+  }
+};
+
+// The same for a wavefront's rows of z: eight tokens 32 ks + 8 g .. of column 16 m + n (as ColumnTile::read<false>).
+template <typename T>
+struct ValueReader {
+  const char* base;
+  int col_[2];
+  __device__ __forceinline__ ValueReader(const Values<T>& v, int lane) {
+    if constexpr (sizeof(T) == 2) {
+      base = v.tile.base;
+      const int g = lane >> 4, e = (lane >> 2) & 3, c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) col_[i] = Tile<kSlice, 1>::at(8 * g + e + 4 * i, c >> 1) + (c & 1) * 8;
+    } else {
+      base = reinterpret_cast<const char*>(v.base);
+      col_[0] = col_[1] = (8 * (lane >> 4) * Values<T>::kLdRow + (lane & 15)) * 4;
+    }
+  }
+  __device__ __forceinline__ void at(const Values<T>& v) {
+    if constexpr (sizeof(T) == 2)
+      base = v.tile.base;
     else
-      x[i].zero();
+      base = reinterpret_cast<const char*>(v.base);
   }
+  __device__ __forceinline__ void columns() { fresh(col_[0]), fresh(col_[1]); }
+  __device__ __forceinline__ Raw8<T> column(int m, int ks) const {
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 2) {
+      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+      typedef T vec __attribute__((ext_vector_type(8)));
+      constexpr int kRow = Tile<kSlice, 1>::kRowBytes;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(base + (col_[0] ^ (m << 5)) + ks * 32 * kRow));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(base + (col_[1] ^ (m << 5)) + ks * 32 * kRow));
+      r.x = __builtin_bit_cast(vec, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const float* c = reinterpret_cast<const float*>(base + col_[0]) + 32 * ks * Values<T>::kLdRow + 16 * m;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int u = i * 64 + lane;
-    put_value<T>(v, u / kChunks, u % kChunks, x[i]);
+      for (int e = 0; e < 8; ++e) r.x[e] = c[e * Values<T>::kLdRow];
+    }
+    return r;
   }
-}
+};
 
 // What the wavefronts of a workgroup hold: `items` neighbouring (head, slice) pairs of one key head.
 struct Place {
@@ -223,14 +470,14 @@ __host__ __device__ __forceinline__ int slices_of(int dv, int slice) { return (d
 // Item `i` of key head hk.
 template <typename T>
 __device__ __forceinline__ Place place_of(const LinearArgs& a, int hk, int i) {
-  const int slices = slices_of(a.dv, kSlice<T>), group = a.H / a.Hk;
+  const int slices = slices_of(a.dv, kSlice), group = a.H / a.Hk;
   Place p;
   p.hk = hk;
   p.live = i < group * slices;
   if (!p.live) i = group * slices - 1;
   p.head = hk * group + i / slices;
-  p.row0 = (i % slices) * kSlice<T>;
-  p.columns = a.dv - p.row0 < kSlice<T> ? a.dv - p.row0 : kSlice<T>;
+  p.row0 = (i % slices) * kSlice;
+  p.columns = a.dv - p.row0 < kSlice ? a.dv - p.row0 : kSlice;
   return p;
 }
 
@@ -243,7 +490,7 @@ __device__ __forceinline__ Split<kMid> weighted(const Raw8<T>& z, const float* w
 // States in registers as [dk][dv]: S[i][m] is the tile of dk indices dealt(i, .) by dv columns 16 m + n.
 template <typename T, int DK>
 struct KeyMajor {
-  static constexpr int kI = kWide<DK> / 16, kM = kTiles<T>;
+  static constexpr int kI = kWide<DK> / 16, kM = kTiles;
   f32x4 S[kI][kM];
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -259,7 +506,7 @@ struct KeyMajor {
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const int k = dealt(i, 4 * g);
-        S[i][m] = k < DK && 16 * m + n < columns ? ld4(p + (16 * m + n) * DK + k) : f32x4{};
+        S[i][m] = (DK >= 32 || k < DK) && 16 * m < columns ? ld4(p + (16 * m + n) * DK + k) : f32x4{};
       }
   }
   __device__ __forceinline__ void store(float* p, int columns, float scale) const {
@@ -269,19 +516,36 @@ struct KeyMajor {
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const int k = dealt(i, 4 * g);
-        if (k < DK && 16 * m + n < columns) st4(p + (16 * m + n) * DK + k, S[i][m] * scale);
+        if ((DK >= 32 || k < DK) && 16 * m < columns) st4(p + (16 * m + n) * DK + k, S[i][m] * scale);
       }
   }
-  // S[.][m] <- whole S[.][m] + Y^T (weighted z)
+  // S <- whole S + Y^T (weighted z), z's weighted rows in N parts. A half of the block's rows at a time, so that the weighted
+  // rows of one half are live and Y is read once.
   template <int N>
-  __device__ __forceinline__ void update(int m, float whole, const Tile<kWide<DK>, Parts<T>::in>& Y, const Split<N> (&z)[2]) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void update(float whole, const Reader<kWide<DK>, Parts<T>::in>& Y, const ValueReader<T>& Z, const float* weights) {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      f32x4 s = S[i][m] * whole;
+    for (int ks = 0; ks < 2; ++ks) {
+      step_ends();
+      const f32x8 w = load8(weights + 32 * ks + 8 * g);
+      Split<N> zs[kM];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) s = mma(Y.template col8<true>(i, ks, lane), z[ks], s);
-      S[i][m] = s;
+      for (int m = 0; m < kM; ++m) zs[m] = split8<N>(Z.column(m, ks).f32() * w);
+      auto y = Y.column(0, ks);
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        step_ends();
+        const auto now = y;
+        if (i + 1 < kI) y = Y.column(i + 1, ks);
+        if (ks == 0) {
+#pragma unroll
+          for (int m = 0; m < kM; ++m) S[i][m] *= whole;
+        }
+        products<Parts<T>::in, N>([&](int pi, int pj) {
+#pragma unroll
+          for (int m = 0; m < kM; ++m) S[i][m] = mfma(now.p[pi], zs[m].p[pj], S[i][m]);
+        });
+      }
     }
   }
 };

@@ -23,8 +23,7 @@ namespace rs {
 
 namespace {
 
-template <typename T>
-constexpr int kMaxWaves = 128 / kTiles<T> / 8;  // 4 or 8: a head of 256 rows
+constexpr int kMaxWaves = 8;  // a head of 256 rows
 
 // What linear_keys leaves per token, head and slice: pairs with tokens in front of its block, and inside it.
 struct Pairs {
@@ -54,11 +53,11 @@ struct KeysArgs {
 template <typename T, int DK>
 struct KeysLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
-  // tiles of 16 rows whose results are summed over the wavefronts at a time (fp32, whose rows fill LDS, takes two)
-  static constexpr int kSumTiles = sizeof(T) == 4 ? 2 : 4;
+  // tiles of 16 rows whose results are summed over the wavefronts at a time (fp32, whose rows fill LDS, takes one)
+  static constexpr int kSumTiles = sizeof(T) == 4 ? 1 : 4;
   // a wavefront's results of 16 channels, and, when those have been read, its three sums per row
   static constexpr int kSum = kSumTiles * 64 * 16;
-  static constexpr int kWave = Values<T>::kBytes + (int)sizeof(RowScalars) + kSum;
+  static constexpr int kWave = Values<T>::kBytes + (int)sizeof(PairScalars) + kSum;
   static_assert(3 * kRows * 4 <= kSum, "room for both");
   static constexpr int y = 0, waves = Rows::kBytes;
   static int total(int n) { return waves + n * kWave; }
@@ -69,7 +68,7 @@ __device__ __forceinline__ int pair_frag(int rt, int ks) { return rt < 2 ? rt : 
 // States in registers as [dv][dk]: S[m][i] is the tile of rows dealt(m, .) by dk columns 16 i + n.
 template <typename T, int DK>
 struct ValueMajor {
-  static constexpr int kI = DK / 16, kM = kTiles<T>;
+  static constexpr int kI = DK / 16, kM = kTiles;
   f32x4 S[kM][kI];
   __device__ __forceinline__ void load(const float* p, int columns) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -101,9 +100,9 @@ struct ValueMajor {
 };
 
 template <typename T, int DK, bool BACK>
-__global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const LinearArgs a, const KeysArgs p) {
+__global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const LinearArgs a, const KeysArgs p) {
   constexpr int in = Parts<T>::in, low = Parts<T>::low;
-  constexpr int kK = kWide<DK> / 32, kV = kTiles<T> / 2;
+  constexpr int kK = kWide<DK> / 32, kV = kTiles / 2;
   constexpr int kWhole = 2 * in - 1 > kMid ? kMid : 2 * in - 1;  // products of inputs on the way to dg and dbeta: all (fp32: to 24 bits)
   using L = KeysLds<T, DK>;
   using State = ValueMajor<T, DK>;
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const Li
   const Segment seg = linear_segment(a, b);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int slices = slices_of(a.dv, kSlice<T>), slice = wave % slices;
+  const int slices = slices_of(a.dv, kSlice), slice = wave % slices;
   const Place at = place_of<T>(a, hk, part * p.waves + wave);
   if (!seg.ok) {
     if (!BACK && p.skips && at.live && lane == 0) p.skips[((int64_t)slice * a.max_segments + b) * a.H + at.head] = 0.f;
@@ -122,8 +121,8 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const Li
   char* mine = lds + L::waves + wave * L::kWave;
   const typename L::Rows Y(lds + L::y);
   const Values<T> W(mine);
-  RowScalars* rows = reinterpret_cast<RowScalars*>(mine + Values<T>::kBytes);
-  const int sum_at = L::waves + Values<T>::kBytes + (int)sizeof(RowScalars);  // of wavefront 0
+  PairScalars* rows = reinterpret_cast<PairScalars*>(mine + Values<T>::kBytes);
+  const int sum_at = L::waves + Values<T>::kBytes + (int)sizeof(PairScalars);  // of wavefront 0
   const auto sum_of = [&](int w) { return reinterpret_cast<f32x4*>(lds + sum_at + w * L::kWave); };
   const auto red_of = [&](int w) { return reinterpret_cast<float*>(lds + sum_at + w * L::kWave); };
   const T* y = static_cast<const T*>(d.y) + (int64_t)hk * DK;
@@ -140,13 +139,18 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const Li
     for (int s = 0; s < slices; ++s) rho += (double)p.rho[((int64_t)s * a.max_segments + b) * a.H + at.head];
   }
   float skips = 0.f;
+  RowFeed<T, DK> yf(y, d.y_stride, BACK);
+  ValueFeed<T> wf(w, p.w_stride, BACK, at.columns);
+  ScalarFeed scalars(a, d, at.head, seg.end);
   for (Blocks blk(seg, BACK); blk.more(); blk.next()) {
     __syncthreads();
-    stage_rows<T, DK>(Y, y, d.y_stride, blk, p.waves * 64);
-    stage_values<T>(W, w, p.w_stride, blk, at.columns);
-    const double end = row_scalars(a, d, blk, seg.end, at.head, rows);
+    yf.stage(Y, blk, wave, p.waves * 64);
+    wf.stage(W, blk);
+    scalars.load(blk);
+    const double end = scalars.make(rows);
+    copies_landed();
     __syncthreads();
-    const float whole = expf((float)end);
+    const float whole = decay_of(end);
     // this wavefront's rows u, as operands
     Split<in> U[4][kV];
     const int64_t u_step = BACK ? -p.u_stride : p.u_stride, e_step = BACK ? -p.e_stride : p.e_stride;
@@ -191,14 +195,19 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const Li
           t1 = mma_to<kWhole>(Y.row8(dealt(2 * ks + 1, n), k, g), er, t1);
         }
         f32x8 dp = join(p0, p1);
-        const f32x8 tt = join(t0, t1);
+        const f32x8 tt = join(t0, t1), w8 = pair_weights(rows, rt, ks, n, g) * pair_scale(rows, Gr, rt, ks, n, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int c = 32 * ks + 8 * g + i;
-          if (c == r) skips += dp[i];
-          const float x = c <= r ? dp[i] * (expf((float)(Gr - rows->G[c])) * rows->col[c]) : 0.f;
-          if (c < r) inner[rt] = __builtin_fmaf(x, tt[i], inner[rt]);
-          if (c == r) diag[rt] = x * tt[i];
+          const float x = dp[i] * w8[i];
+          if (ks == rt / 2) {
+            skips += c == r ? dp[i] : 0.f;
+            const float both = x * tt[i];
+            diag[rt] += c == r ? both : 0.f;
+            inner[rt] += c < r ? both : 0.f;
+          } else {
+            inner[rt] = __builtin_fmaf(x, tt[i], inner[rt]);
+          }
           dp[i] = x;
         }
         D[pair_frag(rt, ks)] = split8<low>(dp);
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const Li
     if (BACK && blk.final()) break;
     // the state behind the block
 #pragma unroll
-    for (int m = 0; m < kTiles<T>; ++m)
+    for (int m = 0; m < kTiles; ++m)
       if (16 * (m & ~1) < at.columns) {
         Split<kMid> z[2];
 #pragma unroll
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64) linear_keys_kernel(const Li
   float product = 0.f;
   if (behind) {
     product = state.dot(behind, at.columns);
-    if (seg.t1 < seg.end) product *= expf((float)closed_gate(a.g[seg.t1 * a.H + at.head]));
+    if (seg.t1 < seg.end) product *= expf(closed_gate(a.g[seg.t1 * a.H + at.head]));
   }
   skips = sum_width<64>(skips);
   if (lane == 0 && at.live) {
@@ -372,10 +381,8 @@ int64_t padded(int64_t bytes) { return (bytes + 255) & ~(int64_t)255; }
 
 KeysPlan keys_plan(const replayssm_linear_config& c, int max_segments) {
   KeysPlan p;
-  const int slice = c.dtype == REPLAYSSM_BF16 ? kSlice<__bf16> : kSlice<float>, most = c.dtype == REPLAYSSM_BF16 ? kMaxWaves<__bf16> : kMaxWaves<float>;
-  static_assert(kSlice<_Float16> == kSlice<float> && kMaxWaves<_Float16> == kMaxWaves<float>, "one shape for both");
-  p.slices = slices_of(c.dv, slice);
-  const int group = c.H / c.Hk;
+  p.slices = slices_of(c.dv, kSlice);
+  const int group = c.H / c.Hk, most = kMaxWaves;
   p.heads = most / p.slices < group ? most / p.slices : group;
   p.waves = p.heads * p.slices;
   p.parts = (group + p.heads - 1) / p.heads;
@@ -406,7 +413,7 @@ replayssm_linear_config config_of(const LinearArgs& a) {
 template <typename T, int DK, bool BACK>
 hipError_t start_keys(const LinearArgs& a, const KeysArgs& p, hipStream_t s) {
   const int bytes = KeysLds<T, DK>::total(p.waves);
-  static_assert(KeysLds<T, DK>::waves + kMaxWaves<T> * KeysLds<T, DK>::kWave <= 160 * 1024, "the LDS of a compute unit");
+  static_assert(KeysLds<T, DK>::waves + kMaxWaves * KeysLds<T, DK>::kWave <= 160 * 1024, "the LDS of a compute unit");
   constexpr auto kernel = linear_keys_kernel<T, DK, BACK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(160 * 1024);
   if (e != hipSuccess) return e;

@@ -7,55 +7,75 @@ namespace rs {
 
 namespace {
 
-constexpr int kWaves = 4;  // of a workgroup, which share their key head's rows
-constexpr int kThreads = kWaves * 64;
-
 // ---- what each segment adds to the state --------------------------------------
+
+// Rows in LDS: bf16 in two buffers, of which the copies fill one while the other is computed with; types that change on their way
+// in one.
+template <typename T, int DK>
+constexpr int kBuffers = kCopied<T, DK> ? 2 : 1;
 
 template <typename T, int DK>
 struct StatesLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
-  static constexpr int y = 0, z = y + Rows::kBytes, scalars = z + kWaves * Values<T>::kBytes,
-                       total = scalars + kWaves * (int)sizeof(RowScalars);
+  static constexpr int kBuffer(int n) { return Rows::kBytes + n * Values<T>::kBytes; }
+  static constexpr int scalars(int n) { return kBuffers<T, DK> * kBuffer(n); }
+  static constexpr int total(int n) { return scalars(n) + n * (int)sizeof(RowScalars); }
+  static_assert(total(kWaves<T>) <= 160 * 1024, "the LDS of a compute unit");
 };
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kThreads) linear_states_kernel(const LinearArgs a, const Side d, int chunks) {
+__global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_states_kernel(const LinearArgs a, const Side d, int chunks) {
   using L = StatesLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
   const int chunk = blockIdx.x % chunks, hk = blockIdx.x / chunks % a.Hk, b = blockIdx.x / chunks / a.Hk;
   const Segment seg = linear_segment(a, b);
   if (!seg.ok || seg.index == (d.reverse ? 0 : seg.count - 1)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
-  const Place at = place_of<T>(a, hk, chunk * kWaves + wave);
-  const typename L::Rows Y(lds + L::y);
-  const Values<T> Z(lds + L::z + wave * Values<T>::kBytes);
-  RowScalars* rows = reinterpret_cast<RowScalars*>(lds + L::scalars) + wave;
-  const T* y = static_cast<const T*>(d.y) + (int64_t)hk * DK;
-  const T* z = static_cast<const T*>(d.z) + (int64_t)at.head * a.dv + at.row0;
+  const int threads = blockDim.x, waves = threads / 64;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place at = place_of<T>(a, hk, chunk * waves + wave);
+  char* now = lds;
+  char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
+  const auto Y = [&](char* p) { return typename L::Rows(p); };
+  const auto Z = [&](char* p) { return Values<T>(p + L::Rows::kBytes + wave * Values<T>::kBytes); };
+  RowScalars* rows = reinterpret_cast<RowScalars*>(lds + L::scalars(waves)) + wave;
   KeyMajor<T, DK> state;
   state.zero();
   double all = 0.0;
-  for (Blocks blk(seg, d.reverse); blk.more(); blk.next()) {
+  Reader<kWide<DK>, Parts<T>::in> yr(Y(now), lane);
+  ValueReader<T> zr(Z(now), lane);
+  RowFeed<T, DK> yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, d.reverse);
+  ValueFeed<T> zf(static_cast<const T*>(d.z) + (int64_t)at.head * a.dv + at.row0, d.z_stride, d.reverse, at.columns);
+  ScalarFeed scalars(a, d, at.head, seg.end);
+  Blocks blk(seg, d.reverse);
+  const auto bring = [&](char* to) {
+    yf.stage(Y(to), blk, wave, threads);
+    zf.stage(Z(to), blk);
+    scalars.load(blk);
+  };
+  bring(now);
+  while (true) {
+    copies_landed();
     __syncthreads();
-    stage_rows<T, DK>(Y, y, d.y_stride, blk, kThreads);
-    stage_values<T>(Z, z, d.z_stride, blk, at.columns);
-    const double end = row_scalars(a, d, blk, seg.end, at.head, rows);
-    all += end;
-    __syncthreads();
-    const float whole = expf((float)end);
-#pragma unroll
-    for (int m = 0; m < kTiles<T>; ++m)
-      if (16 * m < at.columns) {
-        Split<kMid> w[2];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) w[ks] = weighted<T>(Z.template read<false>(m, ks, lane), rows->last, ks, g);
-        state.update(m, whole, Y, w);
-      }
+    const double whole = scalars.make(rows);
+    all += whole;
+    blk.next();
+    const bool more = blk.more();
+    if (kBuffers<T, DK> == 2 && more) bring(other);
+    yr.at(Y(now)), zr.at(Z(now)), yr.columns(), zr.columns();
+    state.template update<kMid>(decay_of(whole), yr, zr, rows->last);
+    if (!more) break;
+    if (kBuffers<T, DK> == 1) {
+      __syncthreads();
+      bring(now);
+    } else {
+      char* t = now;
+      now = other;
+      other = t;
+    }
   }
   if (!at.live) return;
   state.store(d.starts + (((int64_t)b * a.H + at.head) * a.dv + at.row0) * DK, at.columns, 1.f);
-  if (lane == 0 && at.row0 == 0) d.decays[(int64_t)b * a.H + at.head] = expf((float)all);
+  if (lane == 0 && at.row0 == 0) d.decays[(int64_t)b * a.H + at.head] = decay_of(all);
 }
 
 // ---- the states in front of the segments ------------------------------------------
@@ -87,13 +107,11 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
 template <typename T, int DK>
 struct OutLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
-  static constexpr int x = 0, y = x + Rows::kBytes, z = y + Rows::kBytes, scalars = z + kWaves * Values<T>::kBytes,
-                       total = scalars + kWaves * (int)sizeof(RowScalars);
-  static_assert(total <= 160 * 1024, "the LDS of a compute unit");
+  static constexpr int kBuffer(int n) { return 2 * Rows::kBytes + n * Values<T>::kBytes; }
+  static constexpr int scalars(int n) { return kBuffers<T, DK> * kBuffer(n); }
+  static constexpr int total(int n) { return scalars(n) + n * (int)sizeof(PairScalars); }
+  static_assert(total(kWaves<T>) <= 160 * 1024, "the LDS of a compute unit");
 };
-
-// Frag of P^T for rows 16 rt + n and columns 32 ks + 8 g ..: which of the six it is (ks <= rt / 2).
-__device__ __forceinline__ constexpr int p_frag(int rt, int ks) { return rt < 2 ? rt : 2 + 2 * (rt - 2) + ks; }
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const f32x4& x) {
@@ -111,7 +129,7 @@ __device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d,
     return;
   }
   if (seq.count != 0 || d.last == nullptr || d.last == d.first) return;
-  const Place at = place_of<T>(a, hk, chunk * kWaves + (threadIdx.x >> 6));
+  const Place at = place_of<T>(a, hk, chunk * (blockDim.x / 64) + (threadIdx.x >> 6));
   if (!at.live) return;
   const int64_t base = (((int64_t)s * a.H + at.head) * a.dv + at.row0) * a.dk;
   for (int i = (threadIdx.x & 63) * 4; i < at.columns * a.dk; i += 256)
@@ -119,29 +137,44 @@ __device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d,
 }
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kThreads) linear_out_kernel(const LinearArgs a, const Side d, const void* xs, int64_t x_stride, void* outs,
-                                                              int chunks) {
+__global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const LinearArgs a, const Side d, const void* xs, int64_t x_stride,
+                                                                       void* outs, int chunks) {
   constexpr int in = Parts<T>::in, low = Parts<T>::low;
-  constexpr int kK = kWide<DK> / 32;
+  constexpr int kK = kWide<DK> / 32, kM = kTiles;
   using L = OutLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
   const int chunk = blockIdx.x % chunks, hk = blockIdx.x / chunks % a.Hk, b = blockIdx.x / chunks / a.Hk;
   if (b >= a.max_segments) return linear_empty<T>(a, d, b - a.max_segments, hk, chunk);
   const Segment seg = linear_segment(a, b);
   if (!seg.ok) return;
+  const int threads = blockDim.x, waves = threads / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Place at = place_of<T>(a, hk, chunk * kWaves + wave);
-  const typename L::Rows X(lds + L::x), Y(lds + L::y);
-  const Values<T> Z(lds + L::z + wave * Values<T>::kBytes);
-  RowScalars* rows = reinterpret_cast<RowScalars*>(lds + L::scalars) + wave;
-  const T* x = static_cast<const T*>(xs) + (int64_t)hk * DK;
-  const T* y = static_cast<const T*>(d.y) + (int64_t)hk * DK;
+  const Place at = place_of<T>(a, hk, chunk * waves + wave);
+  char* now = lds;
+  char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
+  const auto X = [&](char* p) { return typename L::Rows(p); };
+  const auto Y = [&](char* p) { return typename L::Rows(p + L::Rows::kBytes); };
+  const auto Z = [&](char* p) { return Values<T>(p + 2 * L::Rows::kBytes + wave * Values<T>::kBytes); };
+  PairScalars* rows = reinterpret_cast<PairScalars*>(lds + L::scalars(waves)) + wave;
   const int64_t head = (int64_t)at.head * a.dv + at.row0;
-  const T* z = static_cast<const T*>(d.z) + head;
   T* out = static_cast<T*>(outs) + head;
   const float skip = a.skip ? a.skip[at.head] : 0.f;
   const bool closes = seg.index == (d.reverse ? 0 : seg.count - 1);
+  Reader<kWide<DK>, in> xr(X(now), lane), yr(Y(now), lane);
+  ValueReader<T> zr(Z(now), lane);
+  RowFeed<T, DK> xf(static_cast<const T*>(xs) + (int64_t)hk * DK, x_stride, d.reverse),
+      yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, d.reverse);
+  ValueFeed<T> zf(static_cast<const T*>(d.z) + head, d.z_stride, d.reverse, at.columns);
+  ScalarFeed scalars(a, d, at.head, seg.end);
+  Blocks blk(seg, d.reverse);
+  const auto bring = [&](char* to) {
+    xf.stage(X(to), blk, wave, threads);
+    yf.stage(Y(to), blk, wave, threads);
+    zf.stage(Z(to), blk);
+    scalars.load(blk);
+  };
+  bring(now);
   KeyMajor<T, DK> state;
   {
     const int64_t one = (int64_t)a.H * a.dv * DK, off = head * DK;
@@ -153,106 +186,129 @@ __global__ void __launch_bounds__(kThreads) linear_out_kernel(const LinearArgs a
       state.zero();
   }
   const bool keep = closes && d.last != nullptr;
-  for (Blocks blk(seg, d.reverse); blk.more(); blk.next()) {
+  const int64_t out_row = (int64_t)a.H * a.dv, out_step = d.reverse ? -out_row : out_row, out_lane = n * out_step + 4 * g;
+  int diagonal = n - 8 * g;  // of the 16 rows of an even tile: the column e of a lane's eight that is its row's own
+  while (true) {
+    copies_landed();
     __syncthreads();
-    stage_rows<T, DK>(X, x, x_stride, blk, kThreads);
-    stage_rows<T, DK>(Y, y, d.y_stride, blk, kThreads);
-    stage_values<T>(Z, z, d.z_stride, blk, at.columns);
-    const double end = row_scalars(a, d, blk, seg.end, at.head, rows);
-    __syncthreads();
-    const float whole = expf((float)end);
-    // P[r][c] = row_r col_c e^{G_r - G_c} (x_r . y_c), with the skip weight on the diagonal
-    Split<low> P[6];
+    const double end = scalars.make(rows);
+    const int live = blk.n;
+    T* to_rows = out + blk.token(0) * out_row + out_lane;
+    blk.next();
+    const bool more = blk.more();
+    if (kBuffers<T, DK> == 2 && more) bring(other);
+    xr.at(X(now)), yr.at(Y(now)), zr.at(Z(now));
+    xr.rows(), yr.dealts(), yr.columns(), zr.columns(), fresh(diagonal);
+    // what the state gives
+    f32x4 acc[kM][4];
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) acc[m][rt] = f32x4{};
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      step_ends();
+      Split<in> x[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) x[rt] = xr.row(rt, k);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const Split<low> s = split8<low>(join(state.S[2 * k][m], state.S[2 * k + 1][m]));
+        products<low, in>([&](int i, int j) {
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) acc[m][rt] = mfma(s.p[i], x[rt].p[j], acc[m][rt]);
+        });
+      }
+    }
+    // what the block's own rows give: P[r][c] = row_r col_c e^{G_r - G_c} (x_r . y_c), with the skip weight on the diagonal
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       const int r = 16 * rt + n;
       const double Gr = rows->G[r];
-      const float row = rows->row[r];
+      const float row = rows->row[r], first = rows->first[r] * row;
+#pragma unroll
+      for (int m = 0; m < kM; ++m) acc[m][rt] *= first;
 #pragma unroll
       for (int ks = 0; ks <= rt / 2; ++ks) {
+        step_ends();
         f32x4 t0{}, t1{};
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-          const Split<in> xr = X.row8(r, k, g);
-          t0 = mma(Y.row8(dealt(2 * ks, n), k, g), xr, t0);
-          t1 = mma(Y.row8(dealt(2 * ks + 1, n), k, g), xr, t1);
+          const Split<in> x = xr.row(rt, k);
+          t0 = mma(yr.dealt_row(2 * ks, k), x, t0);
+          t1 = mma(yr.dealt_row(2 * ks + 1, k), x, t1);
         }
-        f32x8 p = join(t0, t1);
+        f32x8 p = join(t0, t1) * (pair_weights(rows, rt, ks, n, g) * (pair_scale(rows, Gr, rt, ks, n, g) * row));
+        if (ks == rt / 2) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = 32 * ks + 8 * g + e;
-          const float w = expf((float)(Gr - rows->G[c])) * rows->col[c] * row;
-          p[e] = c <= r ? p[e] * w : 0.f;
-          if (c == r) p[e] += skip;
+          for (int e = 0; e < 8; ++e) p[e] += e == diagonal + 16 * (rt & 1) ? skip : 0.f;
         }
-        P[p_frag(rt, ks)] = split8<low>(p);
+        const Split<low> P = split8<low>(p);
+#pragma unroll
+        for (int m = 0; m < kM; ++m) acc[m][rt] = mma(zr.column(m, ks).split(), P, acc[m][rt]);
+      }
+      if (at.live && r < live) {
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+          if (16 * m < at.columns) store4(to_rows + 16 * rt * out_step + 16 * m, acc[m][rt]);
       }
     }
-    const bool update = keep || !blk.final();
-#pragma unroll
-    for (int m = 0; m < kTiles<T>; ++m) {
-      if (16 * m < at.columns) {
-        f32x4 acc[4];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{};
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          const Split<low> s = split8<low>(join(state.S[2 * k][m], state.S[2 * k + 1][m]));
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt) acc[rt] = mma(s, X.row8(16 * rt + n, k, g), acc[rt]);
-        }
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) acc[rt] *= rows->first[16 * rt + n] * rows->row[16 * rt + n];
-        Raw8<T> v[2];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) v[ks] = Z.template read<false>(m, ks, lane);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const Split<in> vs = v[ks].split();
-#pragma unroll
-          for (int rt = 2 * ks; rt < 4; ++rt) acc[rt] = mma(vs, P[p_frag(rt, ks)], acc[rt]);
-        }
-        if (at.live) {
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt)
-            if (16 * rt + n < blk.n) store4(out + blk.token(16 * rt + n) * a.H * a.dv + 16 * m + 4 * g, acc[rt]);
-        }
-        if (update) {
-          Split<kMid> w[2];
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) w[ks] = weighted<T>(v[ks], rows->last, ks, g);
-          state.update(m, whole, Y, w);
-        }
-      }
+    // The state behind the block: in 24 bits where it is a result, in those of the outputs otherwise.
+    const float whole = decay_of(end);
+    if (keep)
+      state.template update<kMid>(whole, yr, zr, rows->last);
+    else if (more)
+      state.template update<low>(whole, yr, zr, rows->last);
+    if (!more) break;
+    if (kBuffers<T, DK> == 1) {
+      __syncthreads();
+      bring(now);
+    } else {
+      char* t = now;
+      now = other;
+      other = t;
     }
   }
   if (keep && at.live) {
     // backwards the first token's own decay lies between it and the state in front of it
-    const float decay = d.reverse ? expf((float)closed_gate(a.g[(int64_t)seg.begin * a.H + at.head])) : 1.f;
+    const float decay = d.reverse ? expf(closed_gate(a.g[(int64_t)seg.begin * a.H + at.head])) : 1.f;
     state.store(d.last + ((int64_t)seg.s * a.H * a.dv + head) * DK, at.columns, decay);
   }
 }
 
-int item_chunks(const LinearArgs& a, int slice) { return (a.H / a.Hk * slices_of(a.dv, slice) + kWaves - 1) / kWaves; }
+// Wavefronts of a workgroup, and workgroups of a key head.
+struct Items {
+  int waves, chunks;
+};
+
+Items items_of(const LinearArgs& a, int most) {
+  const int items = a.H / a.Hk * slices_of(a.dv, kSlice);
+  Items r;
+  r.chunks = (items + most - 1) / most;
+  r.waves = (items + r.chunks - 1) / r.chunks;
+  return r;
+}
 
 template <typename T, int DK>
 hipError_t start_states(const LinearArgs& a, const Side& d, hipStream_t s) {
-  const int chunks = item_chunks(a, kSlice<T>);
+  using L = StatesLds<T, DK>;
+  const Items it = items_of(a, kWaves<T>);
   constexpr auto kernel = linear_states_kernel<T, DK>;
-  const hipError_t e = allow_lds<decltype(kernel), kernel>(StatesLds<T, DK>::total);
+  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total(kWaves<T>));
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * chunks)), dim3(kThreads), StatesLds<T, DK>::total, s>>>(a, d, chunks);
+  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * it.chunks)), dim3(it.waves * 64), L::total(it.waves), s>>>(a, d, it.chunks);
   return hipGetLastError();
 }
 
 template <typename T, int DK>
 hipError_t start_out(const LinearArgs& a, const Side& d, const void* x, int64_t x_stride, void* out, hipStream_t s) {
-  const int chunks = item_chunks(a, kSlice<T>);
+  using L = OutLds<T, DK>;
+  const Items it = items_of(a, kWaves<T>);
   constexpr auto kernel = linear_out_kernel<T, DK>;
-  const hipError_t e = allow_lds<decltype(kernel), kernel>(OutLds<T, DK>::total);
+  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total(kWaves<T>));
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)((a.max_segments + a.n_seqs) * a.Hk * chunks)), dim3(kThreads), OutLds<T, DK>::total, s>>>(
-      a, d, x, x_stride, out, chunks);
+  kernel<<<dim3((unsigned)((a.max_segments + a.n_seqs) * a.Hk * it.chunks)), dim3(it.waves * 64), L::total(it.waves), s>>>(a, d, x, x_stride, out,
+                                                                                                                        it.chunks);
   return hipGetLastError();
 }
 
@@ -292,8 +348,7 @@ hipError_t linear_out(const LinearArgs& a, const Side& d, const void* x, int64_t
 // Blocks of 64 tokens are dealt so that about two thousand wavefronts (two a SIMD) each walk one segment: shorter ones cost
 // memory for the states between them, longer ones leave compute units idle.
 int linear_segment_for(const replayssm_linear_config& c) {
-  const int slice = c.dtype == REPLAYSSM_BF16 ? kSlice<__bf16> : kSlice<float>;
-  const int64_t work = (c.n_tokens + kRows - 1) / kRows * c.H * slices_of(c.dv, slice);
+  const int64_t work = (c.n_tokens + kRows - 1) / kRows * c.H * slices_of(c.dv, kSlice);
   int blocks = 4;
   while (blocks < 64 && work >= (int64_t)blocks * 2 * 2048) blocks *= 2;
   while (blocks < 1024 && c.H * (c.n_tokens / (blocks * kRows) + c.n_seqs) * ((c.dv + 31) / 32) > (int64_t)1 << 23) blocks *= 2;
