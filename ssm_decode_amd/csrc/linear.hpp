@@ -112,6 +112,10 @@ struct Blocks {
   __device__ __forceinline__ int64_t token(int r) const { return reverse ? t0 + n - 1 - r : t0 + r; }
 };
 
+// x, of which the compiler forgets that it does not change: what is computed from it in a loop stays in the loop. (Of the hundred
+// addresses in LDS that a block takes, each one exclusive-or away from a lane's few, it would keep every one in a register.)
+__device__ __forceinline__ void fresh(int& x) { asm volatile("" : "+v"(x)); }
+
 // 2^t with the fp32 remainder of t to first order: two ulp whatever the size of t, where 2^(float)t would be off by |t| 2^-24.
 __device__ __forceinline__ float decay_of(double t) {
   const float hi = (float)t, lo = (float)(t - (double)hi);
@@ -168,7 +172,9 @@ struct ScalarFeed {
   float col_weight, row_weight;
   int end;  // the sequence's
   bool reverse;
-  float gate, col, row;
+  struct Gates {
+    float gate, col, row;
+  } gates;
   __device__ __forceinline__ ScalarFeed(const LinearArgs& a, const Side& d, int h, int seq_end)
       : g(a.g + h), col_from(d.beta ? d.beta + h : nullptr), row_from(d.row ? d.row + h : nullptr), step(a.H), col_weight(d.weight),
         row_weight(d.row_weight), end(seq_end), reverse(d.reverse) {}
@@ -178,13 +184,14 @@ struct ScalarFeed {
     const int64_t t = live ? b.token(lane) : b.t0;
     // backwards the decay between a token and the one walked before it is that one's own
     const int64_t tg = reverse ? t + 1 : t;
-    gate = live && tg < end ? g[tg * step] : 0.f;
-    col = !live ? 0.f : col_from ? col_from[t * step] : col_weight;
-    row = !live ? 0.f : row_from ? row_from[t * step] : row_weight;
+    gates.gate = live && tg < end ? g[tg * step] : 0.f;
+    gates.col = !live ? 0.f : col_from ? col_from[t * step] : col_weight;
+    gates.row = !live ? 0.f : row_from ? row_from[t * step] : row_weight;
   }
   // returns the block's whole exponent
   template <typename Scalars>
-  __device__ __forceinline__ double make(Scalars* out) const {
+  __device__ __forceinline__ static double make(const Gates& from, Scalars* out) {
+    const float gate = from.gate, col = from.col, row = from.row;
     const int lane = threadIdx.x & 63;
     const double sum = running_sum((double)closed_gate(gate) * kLog2e);
     const double whole = lane_value(sum, 63);
@@ -193,18 +200,23 @@ struct ScalarFeed {
     out->last[lane] = decay_of(whole - sum) * col;
     out->row[lane] = row;
     if constexpr (std::is_same_v<Scalars, PairScalars>) {
-      // (the pairs' table first holds the columns' weights)
+      // (the pairs' tables first hold the columns' weights and the tokens' own decays)
       out->tail[lane] = col;
-      const double* G = out->G + (lane & ~7);
-      const f32x8 cols = load8(out->tail + (lane & ~7));
+      out->near[0][lane] = decay_of((double)closed_gate(gate) * kLog2e);
+      int eight = lane & ~7, place = lane & 7;
+      fresh(place);
+      const f32x8 cols = load8(out->tail + eight), decays = load8(out->near[0] + eight);
+      const double end = out->G[eight + 7];
       f32x8 near;
+      float w = 1.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float w = decay_of(sum - G[e]) * cols[e];
-        near[e] = e <= (lane & 7) ? w : 0.f;
+      for (int e = 7; e >= 0; --e) {
+        // decays of the tokens behind column e up to the row
+        if (e < 7) w = e < place ? w * decays[e + 1 > 7 ? 7 : e + 1] : 1.f;
+        near[e] = e <= place ? w * cols[e] : 0.f;
       }
       store8(out->near[lane], near);
-      out->tail[lane] = decay_of(G[7] - sum) * col;
+      out->tail[lane] = decay_of(end - sum) * col;
     }
     return whole;
   }
@@ -225,10 +237,6 @@ __device__ __forceinline__ float pair_scale(const PairScalars* s, double Gr, int
 // Nothing is moved across it: in these unrolled kernels the scheduler would otherwise ask for the operands of many steps at once,
 // which does not fit the registers beside a state.
 __device__ __forceinline__ void step_ends() { __builtin_amdgcn_sched_barrier(0); }
-
-// x, of which the compiler forgets that it does not change: what is computed from it in a loop stays in the loop. (Of the hundred
-// addresses in LDS that a block takes, each one exclusive-or away from a lane's few, it would keep every one in a register.)
-__device__ __forceinline__ void fresh(int& x) { asm volatile("" : "+v"(x)); }
 
 // A lane's places in a tile of parts, from which each operand is one exclusive-or and a constant away: the tile's key touches the
 // same bits of an address as the column does.
@@ -259,8 +267,8 @@ struct Reader {
     return s;
   }
   // as Tile::row8 of row 16 rt + n, and of row dealt(t, n)
-  __device__ __forceinline__ Split<N> row(int rt, int k) const { return read((row_[rt & 1] ^ (k << 6)) + (rt >> 1) * 32 * kRow); }
-  __device__ __forceinline__ Split<N> dealt_row(int t, int k) const { return read((dealt_[t & 1] ^ (k << 6)) + (t >> 1) * 32 * kRow); }
+  __device__ __forceinline__ Split<N> row(int rt, int k) const { return read(((rt & 1 ? row_[1] : row_[0]) ^ (k << 6)) + (rt >> 1) * 32 * kRow); }
+  __device__ __forceinline__ Split<N> dealt_row(int t, int k) const { return read(((t & 1 ? dealt_[1] : dealt_[0]) ^ (k << 6)) + (t >> 1) * 32 * kRow); }
   // as Tile::col8<true>(t, ks)
   __device__ __forceinline__ Split<N> column(int t, int ks) const {
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
@@ -277,6 +285,15 @@ struct Reader {
     return s;
   }
 };
+
+// Of the two wavefronts on a SIMD one goes first, so that one's matrix instructions run while the other converts operands: with
+// equal priority they go through a block's phases together and wait for the same unit.
+__device__ __forceinline__ void take_turns(int wave) {
+  if (wave & 4)
+    __builtin_amdgcn_s_setprio(0);
+  else
+    __builtin_amdgcn_s_setprio(2);
+}
 
 // 16 bytes of every lane straight into LDS, to `to` (uniform) + 16 lane.
 __device__ __forceinline__ void copy16(const void* from, char* to) {
@@ -459,32 +476,55 @@ struct ValueReader {
   }
 };
 
-// What the wavefronts of a workgroup hold: `items` neighbouring (head, slice) pairs of one key head.
-struct Place {
-  int hk, head, row0, columns;  // key head, value head, first state row, state rows that exist
-  bool live;
+// How a key head's value heads and their slices are dealt to workgroups: a workgroup takes `heads` whole heads, a wavefront a slice,
+// or, where a head has more slices than a workgroup wavefronts, one of `parts` parts of a head.
+struct Deal {
+  int slices, heads, waves, parts, chunks;  // chunks: workgroups of a key head
 };
 
-__host__ __device__ __forceinline__ int slices_of(int dv, int slice) { return (dv + slice - 1) / slice; }
-
-// Item `i` of key head hk.
-template <typename T>
-__device__ __forceinline__ Place place_of(const LinearArgs& a, int hk, int i) {
-  const int slices = slices_of(a.dv, kSlice), group = a.H / a.Hk;
-  Place p;
-  p.hk = hk;
-  p.live = i < group * slices;
-  if (!p.live) i = group * slices - 1;
-  p.head = hk * group + i / slices;
-  p.row0 = (i % slices) * kSlice;
-  p.columns = a.dv - p.row0 < kSlice ? a.dv - p.row0 : kSlice;
-  return p;
+inline Deal deal(int dv, int group, int most_waves, int most_heads) {
+  Deal d;
+  d.slices = (dv + kSlice - 1) / kSlice;
+  d.parts = (d.slices + most_waves - 1) / most_waves;
+  if (d.parts > 1) {
+    d.heads = 1;
+    d.waves = (d.slices + d.parts - 1) / d.parts;
+    d.chunks = group * d.parts;
+    return d;
+  }
+  d.heads = most_waves / d.slices < most_heads ? most_waves / d.slices : most_heads;
+  if (d.heads > group) d.heads = group;
+  d.chunks = (group + d.heads - 1) / d.heads;
+  d.heads = (group + d.chunks - 1) / d.chunks;  // (as even as they come)
+  d.waves = d.heads * d.slices;
+  return d;
 }
 
-// The weighted z of eight tokens c = 32 ks + 8 g .. + 7 for one column, as an operand of the states' products.
-template <typename T>
-__device__ __forceinline__ Split<kMid> weighted(const Raw8<T>& z, const float* w, int ks, int g) {
-  return split8<kMid>(z.f32() * load8(w + 32 * ks + 8 * g));
+struct Place {
+  int head, slot, slice;  // value head, which of the workgroup's it is, which slice of it
+  int row0, columns;      // first state row, state rows that exist
+  bool live;              // (a wavefront without a slice computes with another's and writes nothing)
+};
+
+__device__ __forceinline__ Place place_of(const LinearArgs& a, const Deal& d, int hk, int chunk, int wave) {
+  const int group = a.H / a.Hk;
+  Place p;
+  int head, slice;
+  if (d.parts > 1) {
+    head = chunk / d.parts;
+    p.slot = 0;
+    slice = chunk % d.parts * d.waves + wave;
+  } else {
+    p.slot = wave / d.slices;
+    head = chunk * d.heads + p.slot;
+    slice = wave % d.slices;
+  }
+  p.live = head < group && slice < d.slices;
+  p.slice = slice < d.slices ? slice : d.slices - 1;
+  p.head = hk * group + (head < group ? head : group - 1);
+  p.row0 = p.slice * kSlice;
+  p.columns = a.dv - p.row0 < kSlice ? a.dv - p.row0 : kSlice;
+  return p;
 }
 
 // States in registers as [dk][dv]: S[i][m] is the tile of dk indices dealt(i, .) by dv columns 16 m + n.
@@ -519,32 +559,35 @@ struct KeyMajor {
         if ((DK >= 32 || k < DK) && 16 * m < columns) st4(p + (16 * m + n) * DK + k, S[i][m] * scale);
       }
   }
-  // S <- whole S + Y^T (weighted z), z's weighted rows in N parts. A half of the block's rows at a time, so that the weighted
-  // rows of one half are live and Y is read once.
+  // S <- whole S + Y^T (weighted z), z's weighted rows in N parts; z[m][ks]: its columns. A half of the block's rows at a time.
   template <int N>
-  __device__ __forceinline__ void update(float whole, const Reader<kWide<DK>, Parts<T>::in>& Y, const ValueReader<T>& Z, const float* weights) {
+  __device__ __forceinline__ void update(float whole, const Reader<kWide<DK>, Parts<T>::in>& Y, const Raw8<T> (&z)[kM][2], const float* weights) {
     const int g = (threadIdx.x & 63) >> 4;
+    constexpr int kIn = Parts<T>::in, kGroup = kIn == 1 && kI >= 4 ? 4 : 2;  // operands asked for together
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      step_ends();
       const f32x8 w = load8(weights + 32 * ks + 8 * g);
       Split<N> zs[kM];
 #pragma unroll
-      for (int m = 0; m < kM; ++m) zs[m] = split8<N>(Z.column(m, ks).f32() * w);
-      auto y = Y.column(0, ks);
+      for (int m = 0; m < kM; ++m) zs[m] = split8<N>(z[m][ks].f32() * w);
 #pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        step_ends();
-        const auto now = y;
-        if (i + 1 < kI) y = Y.column(i + 1, ks);
+      for (int i0 = 0; i0 < kI; i0 += kGroup) {
+        Split<kIn> y[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) y[i] = Y.column(i0 + i, ks);
         if (ks == 0) {
 #pragma unroll
-          for (int m = 0; m < kM; ++m) S[i][m] *= whole;
-        }
-        products<Parts<T>::in, N>([&](int pi, int pj) {
+          for (int i = 0; i < kGroup; ++i)
 #pragma unroll
-          for (int m = 0; m < kM; ++m) S[i][m] = mfma(now.p[pi], zs[m].p[pj], S[i][m]);
+            for (int m = 0; m < kM; ++m) S[i0 + i][m] *= whole;
+        }
+        products<kIn, N>([&](int pi, int pj) {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+            for (int m = 0; m < kM; ++m) S[i0 + i][m] = mfma(y[i].p[pi], zs[m].p[pj], S[i0 + i][m]);
         });
+        if (i0 & kGroup) step_ends();
       }
     }
   }

@@ -45,9 +45,7 @@ struct KeysArgs {
   float* skips;  // [slices][segments][H]: sums of u . w, or NULL
   float* dg;
   float* dbeta;
-  int heads;     // value heads of a workgroup
-  int waves;     // its wavefronts: heads * slices
-  int parts;     // workgroups of a key head
+  Deal deal;
 };
 
 template <typename T, int DK>
@@ -108,12 +106,12 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
   using State = ValueMajor<T, DK>;
   extern __shared__ __align__(16) char lds[];
   const Side& d = p.d;
-  const int part = blockIdx.x % p.parts, hk = blockIdx.x / p.parts % a.Hk, b = blockIdx.x / p.parts / a.Hk;
+  const int part = blockIdx.x % p.deal.chunks, hk = blockIdx.x / p.deal.chunks % a.Hk, b = blockIdx.x / p.deal.chunks / a.Hk;
   const Segment seg = linear_segment(a, b);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int slices = slices_of(a.dv, kSlice), slice = wave % slices;
-  const Place at = place_of<T>(a, hk, part * p.waves + wave);
+  const Place at = place_of(a, p.deal, hk, part, wave);
+  const int slices = p.deal.slices, slice = at.slice;
   if (!seg.ok) {
     if (!BACK && p.skips && at.live && lane == 0) p.skips[((int64_t)slice * a.max_segments + b) * a.H + at.head] = 0.f;
     return;
@@ -144,10 +142,10 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
   ScalarFeed scalars(a, d, at.head, seg.end);
   for (Blocks blk(seg, BACK); blk.more(); blk.next()) {
     __syncthreads();
-    yf.stage(Y, blk, wave, p.waves * 64);
+    yf.stage(Y, blk, wave, p.deal.waves * 64);
     wf.stage(W, blk);
     scalars.load(blk);
-    const double end = scalars.make(rows);
+    const double end = scalars.make(scalars.gates, rows);
     copies_landed();
     __syncthreads();
     const float whole = decay_of(end);
@@ -247,9 +245,9 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
 #pragma unroll
         for (int rt = 0; rt < L::kSumTiles; ++rt) sum_of(wave)[rt * 64 + lane] = at.live ? acc[r0 + rt] : f32x4{};
         __syncthreads();
-        for (int v = threadIdx.x; v < L::kSumTiles * 64; v += p.waves * 64) {
+        for (int v = threadIdx.x; v < L::kSumTiles * 64; v += p.deal.waves * 64) {
           f32x4 s = sum_of(0)[v];
-          for (int k = 1; k < p.waves; ++k) s += sum_of(k)[v];
+          for (int k = 1; k < p.deal.waves; ++k) s += sum_of(k)[v];
           const int r = 16 * (r0 + (v >> 6)) + (v & 15), c = 16 * i + 4 * ((v >> 4) & 3);
           if (r < blk.n) {
             const int64_t to = (blk.token(r) * a.Hk + hk) * DK + c;
@@ -319,7 +317,7 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
       if (16 * (m & ~1) < at.columns) {
         Split<kMid> z[2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) z[ks] = weighted<T>(W.template read<true>(m, ks, lane), rows->last, ks, g);
+        for (int ks = 0; ks < 2; ++ks) z[ks] = split8<kMid>(W.template read<true>(m, ks, lane).f32() * load8(rows->last + 32 * ks + 8 * g));
 #pragma unroll
         for (int i = 0; i < DK / 16; ++i) {
           f32x4 s = state.S[m][i] * whole;
@@ -373,7 +371,7 @@ __global__ void __launch_bounds__(256) linear_skip_kernel(const LinearArgs a, co
 
 // How the value heads of a key head are dealt to workgroups, and what lies where in the workspace.
 struct KeysPlan {
-  int slices, heads, waves, parts;
+  Deal deal;
   int64_t forward, reverse, pairs, rho, skips, partial, total;
 };
 
@@ -381,19 +379,15 @@ int64_t padded(int64_t bytes) { return (bytes + 255) & ~(int64_t)255; }
 
 KeysPlan keys_plan(const replayssm_linear_config& c, int max_segments) {
   KeysPlan p;
-  p.slices = slices_of(c.dv, kSlice);
-  const int group = c.H / c.Hk, most = kMaxWaves;
-  p.heads = most / p.slices < group ? most / p.slices : group;
-  p.waves = p.heads * p.slices;
-  p.parts = (group + p.heads - 1) / p.heads;
-  const int64_t side = linear_side_bytes(c, max_segments), per = padded((int64_t)p.slices * max_segments * c.H * 4);
+  p.deal = deal(c.dv, c.H / c.Hk, kMaxWaves, kMaxWaves);
+  const int64_t side = linear_side_bytes(c, max_segments), per = padded((int64_t)p.deal.slices * max_segments * c.H * 4);
   p.forward = 0;
   p.reverse = side;
   p.pairs = p.reverse + side;
-  p.rho = p.pairs + padded((int64_t)p.slices * c.n_tokens * c.H * sizeof(Pairs));
+  p.rho = p.pairs + padded((int64_t)p.deal.slices * c.n_tokens * c.H * sizeof(Pairs));
   p.skips = p.rho + per;
   p.partial = p.skips + per;
-  p.total = p.partial + (p.parts > 1 ? padded((int64_t)p.parts * c.n_tokens * c.Hk * c.dk * 4) : 0);
+  p.total = p.partial + (p.deal.chunks > 1 ? padded((int64_t)p.deal.chunks * c.n_tokens * c.Hk * c.dk * 4) : 0);
   return p;
 }
 
@@ -412,12 +406,12 @@ replayssm_linear_config config_of(const LinearArgs& a) {
 
 template <typename T, int DK, bool BACK>
 hipError_t start_keys(const LinearArgs& a, const KeysArgs& p, hipStream_t s) {
-  const int bytes = KeysLds<T, DK>::total(p.waves);
+  const int bytes = KeysLds<T, DK>::total(p.deal.waves);
   static_assert(KeysLds<T, DK>::waves + kMaxWaves * KeysLds<T, DK>::kWave <= 160 * 1024, "the LDS of a compute unit");
   constexpr auto kernel = linear_keys_kernel<T, DK, BACK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(160 * 1024);
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * p.parts)), dim3(p.waves * 64), bytes, s>>>(a, p);
+  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * p.deal.chunks)), dim3(p.deal.waves * 64), bytes, s>>>(a, p);
   return hipGetLastError();
 }
 
@@ -432,7 +426,7 @@ hipError_t keys(const LinearArgs& a, const KeysArgs& p, hipStream_t s) {
   }
   if (e != hipSuccess || p.partial == nullptr) return e;
   const int64_t units = ((int64_t)a.segment * a.Hk * a.dk + 2047) / 2048;
-  linear_sum_kernel<T><<<dim3((unsigned)(units < 1024 ? units : 1024), (unsigned)a.max_segments), dim3(256), 0, s>>>(a, p.partial, p.parts,
+  linear_sum_kernel<T><<<dim3((unsigned)(units < 1024 ? units : 1024), (unsigned)a.max_segments), dim3(256), 0, s>>>(a, p.partial, p.deal.chunks,
                                                                                                                   static_cast<T*>(p.out));
   return hipGetLastError();
 }
@@ -482,10 +476,8 @@ hipError_t launch_linear_prompt_backward(const LinearArgs& a, hipStream_t s) {
   if (e == hipSuccess) e = linear_starts(a, r, s);
   if (e != hipSuccess) return e;
   KeysArgs p{};
-  p.heads = plan.heads;
-  p.waves = plan.waves;
-  p.parts = plan.parts;
-  p.partial = plan.parts > 1 ? reinterpret_cast<float*>(ws + plan.partial) : nullptr;
+  p.deal = plan.deal;
+  p.partial = plan.deal.chunks > 1 ? reinterpret_cast<float*>(ws + plan.partial) : nullptr;
   p.pairs = reinterpret_cast<Pairs*>(ws + plan.pairs);
   p.rho = reinterpret_cast<float*>(ws + plan.rho);
   p.skips = a.dskip ? reinterpret_cast<float*>(ws + plan.skips) : nullptr;
@@ -515,7 +507,7 @@ hipError_t launch_linear_prompt_backward(const LinearArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   e = linear_out(a, r, a.k, a.k_stride, a.dv_, s);
   if (e != hipSuccess || a.dskip == nullptr) return e;
-  linear_skip_kernel<<<dim3((unsigned)a.H), dim3(256), 0, s>>>(a, p.skips, plan.slices * a.max_segments);
+  linear_skip_kernel<<<dim3((unsigned)a.H), dim3(256), 0, s>>>(a, p.skips, plan.deal.slices * a.max_segments);
   return hipGetLastError();
 }
 

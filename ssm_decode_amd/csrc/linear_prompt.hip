@@ -24,15 +24,15 @@ struct StatesLds {
 };
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_states_kernel(const LinearArgs a, const Side d, int chunks) {
+__global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_states_kernel(const LinearArgs a, const Side d, const Deal deal) {
   using L = StatesLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
-  const int chunk = blockIdx.x % chunks, hk = blockIdx.x / chunks % a.Hk, b = blockIdx.x / chunks / a.Hk;
+  const int chunk = blockIdx.x % deal.chunks, hk = blockIdx.x / deal.chunks % a.Hk, b = blockIdx.x / deal.chunks / a.Hk;
   const Segment seg = linear_segment(a, b);
   if (!seg.ok || seg.index == (d.reverse ? 0 : seg.count - 1)) return;
-  const int threads = blockDim.x, waves = threads / 64;
+  const int waves = deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place at = place_of<T>(a, hk, chunk * waves + wave);
+  const Place at = place_of(a, deal, hk, chunk, wave);
   char* now = lds;
   char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
   const auto Y = [&](char* p) { return typename L::Rows(p); };
@@ -53,16 +53,23 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_states_kernel(const 
     scalars.load(blk);
   };
   bring(now);
+  take_turns(wave);
   while (true) {
     copies_landed();
     __syncthreads();
-    const double whole = scalars.make(rows);
-    all += whole;
     blk.next();
     const bool more = blk.more();
+    const ScalarFeed::Gates gates = scalars.gates;
     if (kBuffers<T, DK> == 2 && more) bring(other);
+    const double whole = scalars.make(gates, rows);
+    all += whole;
     yr.at(Y(now)), zr.at(Z(now)), yr.columns(), zr.columns();
-    state.template update<kMid>(decay_of(whole), yr, zr, rows->last);
+    Raw8<T> z[kTiles][2];
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) z[m][ks] = zr.column(m, ks);
+    state.template update<kMid>(decay_of(whole), yr, z, rows->last);
     if (!more) break;
     if (kBuffers<T, DK> == 1) {
       __syncthreads();
@@ -108,10 +115,21 @@ template <typename T, int DK>
 struct OutLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
   static constexpr int kBuffer(int n) { return 2 * Rows::kBytes + n * Values<T>::kBytes; }
-  static constexpr int scalars(int n) { return kBuffers<T, DK> * kBuffer(n); }
-  static constexpr int total(int n) { return scalars(n) + n * (int)sizeof(PairScalars); }
-  static_assert(total(kWaves<T>) <= 160 * 1024, "the LDS of a compute unit");
+  static constexpr int kScores = 12 * 1024;  // of the key head, fp32
+  static constexpr int scores(int n) { return kBuffers<T, DK> * kBuffer(n); }
+  static constexpr int scalars(int n) { return scores(n) + kScores; }
+  static constexpr int total(int n, int heads) { return scalars(n) + heads * (int)sizeof(PairScalars); }
+  // value heads of a workgroup: most that fit
+  static constexpr int heads() {
+    int n = kWaves<T>;
+    while (total(n, n) > 160 * 1024) --n;
+    return n;
+  }
+  static_assert(total(kWaves<T>, kWaves<T> / 2) <= 160 * 1024, "heads of several slices fill the workgroup");
 };
+
+// The tiles of the scores, [c][rt] with 16 c <= 16 rt + 15 in pairs of c: which of the twelve.
+__device__ __forceinline__ constexpr int score_tile(int c, int rt) { return c < 2 ? 4 * c + rt : 8 + 2 * (c - 2) + rt - 2; }
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const f32x4& x) {
@@ -120,8 +138,7 @@ __device__ __forceinline__ void store4(T* p, const f32x4& x) {
 }
 
 // Sequences without tokens, and the flag of those whose tables are bad.
-template <typename T>
-__device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d, int s, int hk, int chunk) {
+__device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d, const Deal& deal, int s, int hk, int chunk) {
   int b0;
   const Segment seq = linear_sequence(a, s, &b0);
   if (!seq.ok) {
@@ -129,7 +146,7 @@ __device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d,
     return;
   }
   if (seq.count != 0 || d.last == nullptr || d.last == d.first) return;
-  const Place at = place_of<T>(a, hk, chunk * (blockDim.x / 64) + (threadIdx.x >> 6));
+  const Place at = place_of(a, deal, hk, chunk, threadIdx.x >> 6);
   if (!at.live) return;
   const int64_t base = (((int64_t)s * a.H + at.head) * a.dv + at.row0) * a.dk;
   for (int i = (threadIdx.x & 63) * 4; i < at.columns * a.dk; i += 256)
@@ -138,25 +155,28 @@ __device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d,
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const LinearArgs a, const Side d, const void* xs, int64_t x_stride,
-                                                                       void* outs, int chunks) {
+                                                                       void* outs, const Deal deal) {
   constexpr int in = Parts<T>::in, low = Parts<T>::low;
   constexpr int kK = kWide<DK> / 32, kM = kTiles;
   using L = OutLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
-  const int chunk = blockIdx.x % chunks, hk = blockIdx.x / chunks % a.Hk, b = blockIdx.x / chunks / a.Hk;
-  if (b >= a.max_segments) return linear_empty<T>(a, d, b - a.max_segments, hk, chunk);
+  const int chunk = blockIdx.x % deal.chunks, hk = blockIdx.x / deal.chunks % a.Hk, b = blockIdx.x / deal.chunks / a.Hk;
+  if (b >= a.max_segments) return linear_empty(a, d, deal, b - a.max_segments, hk, chunk);
   const Segment seg = linear_segment(a, b);
   if (!seg.ok) return;
-  const int threads = blockDim.x, waves = threads / 64;
+  const int waves = deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Place at = place_of<T>(a, hk, chunk * waves + wave);
+  const Place at = place_of(a, deal, hk, chunk, wave);
   char* now = lds;
   char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
   const auto X = [&](char* p) { return typename L::Rows(p); };
   const auto Y = [&](char* p) { return typename L::Rows(p + L::Rows::kBytes); };
   const auto Z = [&](char* p) { return Values<T>(p + 2 * L::Rows::kBytes + wave * Values<T>::kBytes); };
-  PairScalars* rows = reinterpret_cast<PairScalars*>(lds + L::scalars(waves)) + wave;
+  float* scores = reinterpret_cast<float*>(lds + L::scores(waves));
+  PairScalars* rows = reinterpret_cast<PairScalars*>(lds + L::scalars(waves)) + at.slot;
+  // this wavefront makes its head's tables (those of a workgroup's heads on different SIMDs)
+  const bool makes = deal.parts > 1 ? wave == 0 : wave - at.slot * deal.slices == at.slot * deal.slices / 4 % deal.slices;
   const int64_t head = (int64_t)at.head * a.dv + at.row0;
   T* out = static_cast<T*>(outs) + head;
   const float skip = a.skip ? a.skip[at.head] : 0.f;
@@ -175,6 +195,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
     scalars.load(blk);
   };
   bring(now);
+  take_turns(wave);
   KeyMajor<T, DK> state;
   {
     const int64_t one = (int64_t)a.H * a.dv * DK, off = head * DK;
@@ -191,14 +212,23 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   while (true) {
     copies_landed();
     __syncthreads();
-    const double end = scalars.make(rows);
     const int live = blk.n;
     T* to_rows = out + blk.token(0) * out_row + out_lane;
     blk.next();
     const bool more = blk.more();
+    const ScalarFeed::Gates gates = scalars.gates;
     if (kBuffers<T, DK> == 2 && more) bring(other);
+    if (makes) scalars.make(gates, rows);
     xr.at(X(now)), yr.at(Y(now)), zr.at(Z(now));
     xr.rows(), yr.dealts(), yr.columns(), zr.columns(), fresh(diagonal);
+    // the scores of the key head, t[c][r] = y_c . x_r: the same for all wavefronts, which share the work
+    for (int q = wave; q < 12; q += waves) {
+      const int c = q < 8 ? q >> 2 : 2 + ((q - 8) >> 1), rt = q < 8 ? q & 3 : 2 + ((q - 8) & 1);
+      f32x4 t{};
+#pragma unroll
+      for (int k = 0; k < kK; ++k) t = mma(yr.dealt_row(c, k), xr.row(rt, k), t);
+      st4(scores + (q * 64 + lane) * 4, t);
+    }
     // what the state gives
     f32x4 acc[kM][4];
 #pragma unroll
@@ -207,58 +237,60 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
       for (int rt = 0; rt < 4; ++rt) acc[m][rt] = f32x4{};
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
-      step_ends();
       Split<in> x[4];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) x[rt] = xr.row(rt, k);
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const Split<low> s = split8<low>(join(state.S[2 * k][m], state.S[2 * k + 1][m]));
-        products<low, in>([&](int i, int j) {
+        products<low, in>([&](int pi, int pj) {
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) acc[m][rt] = mfma(s.p[i], x[rt].p[j], acc[m][rt]);
+          for (int rt = 0; rt < 4; ++rt) acc[m][rt] = mfma(s.p[pi], x[rt].p[pj], acc[m][rt]);
         });
       }
+      if (k & 1) step_ends();
     }
-    // what the block's own rows give: P[r][c] = row_r col_c e^{G_r - G_c} (x_r . y_c), with the skip weight on the diagonal
+    __syncthreads();
+    // what the block's own rows give, by P[r][c] = row_r col_c e^{G_r - G_c} t[c][r] with the skip weight on the diagonal
+    const double end = rows->G[kRows - 1];
+    Raw8<T> z[kM][2];
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) z[m][ks] = zr.column(m, ks);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      const int r = 16 * rt + n;
-      const double Gr = rows->G[r];
-      const float row = rows->row[r], first = rows->first[r] * row;
+      const double Gr = rows->G[16 * rt + n];
+      const float row = rows->row[16 * rt + n], first = rows->first[16 * rt + n] * row;
 #pragma unroll
       for (int m = 0; m < kM; ++m) acc[m][rt] *= first;
 #pragma unroll
       for (int ks = 0; ks <= rt / 2; ++ks) {
-        step_ends();
-        f32x4 t0{}, t1{};
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          const Split<in> x = xr.row(rt, k);
-          t0 = mma(yr.dealt_row(2 * ks, k), x, t0);
-          t1 = mma(yr.dealt_row(2 * ks + 1, k), x, t1);
-        }
-        f32x8 p = join(t0, t1) * (pair_weights(rows, rt, ks, n, g) * (pair_scale(rows, Gr, rt, ks, n, g) * row));
-        if (ks == rt / 2) {
+        const f32x8 t = join(ld4(scores + (score_tile(2 * ks, rt) * 64 + lane) * 4), ld4(scores + (score_tile(2 * ks + 1, rt) * 64 + lane) * 4));
+        f32x8 p = t * (pair_weights(rows, rt, ks, n, g) * (pair_scale(rows, Gr, rt, ks, n, g) * row));
+        if (ks == rt / 2 && skip != 0.f) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) p[e] += e == diagonal + 16 * (rt & 1) ? skip : 0.f;
         }
         const Split<low> P = split8<low>(p);
 #pragma unroll
-        for (int m = 0; m < kM; ++m) acc[m][rt] = mma(zr.column(m, ks).split(), P, acc[m][rt]);
+        for (int m = 0; m < kM; ++m) acc[m][rt] = mma(z[m][ks].split(), P, acc[m][rt]);
       }
-      if (at.live && r < live) {
+      if (rt & 1) step_ends();
+    }
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+      if (at.live && 16 * rt + n < live) {
 #pragma unroll
         for (int m = 0; m < kM; ++m)
           if (16 * m < at.columns) store4(to_rows + 16 * rt * out_step + 16 * m, acc[m][rt]);
       }
-    }
     // The state behind the block: in 24 bits where it is a result, in those of the outputs otherwise.
     const float whole = decay_of(end);
     if (keep)
-      state.template update<kMid>(whole, yr, zr, rows->last);
+      state.template update<kMid>(whole, yr, z, rows->last);
     else if (more)
-      state.template update<low>(whole, yr, zr, rows->last);
+      state.template update<low>(whole, yr, z, rows->last);
     if (!more) break;
     if (kBuffers<T, DK> == 1) {
       __syncthreads();
@@ -276,39 +308,26 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   }
 }
 
-// Wavefronts of a workgroup, and workgroups of a key head.
-struct Items {
-  int waves, chunks;
-};
-
-Items items_of(const LinearArgs& a, int most) {
-  const int items = a.H / a.Hk * slices_of(a.dv, kSlice);
-  Items r;
-  r.chunks = (items + most - 1) / most;
-  r.waves = (items + r.chunks - 1) / r.chunks;
-  return r;
-}
-
 template <typename T, int DK>
 hipError_t start_states(const LinearArgs& a, const Side& d, hipStream_t s) {
   using L = StatesLds<T, DK>;
-  const Items it = items_of(a, kWaves<T>);
+  const Deal way = deal(a.dv, a.H / a.Hk, kWaves<T>, kWaves<T>);
   constexpr auto kernel = linear_states_kernel<T, DK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total(kWaves<T>));
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * it.chunks)), dim3(it.waves * 64), L::total(it.waves), s>>>(a, d, it.chunks);
+  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * way.chunks)), dim3(way.waves * 64), L::total(way.waves), s>>>(a, d, way);
   return hipGetLastError();
 }
 
 template <typename T, int DK>
 hipError_t start_out(const LinearArgs& a, const Side& d, const void* x, int64_t x_stride, void* out, hipStream_t s) {
   using L = OutLds<T, DK>;
-  const Items it = items_of(a, kWaves<T>);
+  const Deal way = deal(a.dv, a.H / a.Hk, kWaves<T>, L::heads());
   constexpr auto kernel = linear_out_kernel<T, DK>;
-  const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total(kWaves<T>));
+  const hipError_t e = allow_lds<decltype(kernel), kernel>(160 * 1024);
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)((a.max_segments + a.n_seqs) * a.Hk * it.chunks)), dim3(it.waves * 64), L::total(it.waves), s>>>(a, d, x, x_stride, out,
-                                                                                                                        it.chunks);
+  kernel<<<dim3((unsigned)((a.max_segments + a.n_seqs) * a.Hk * way.chunks)), dim3(way.waves * 64), L::total(way.waves, way.heads), s>>>(
+      a, d, x, x_stride, out, way);
   return hipGetLastError();
 }
 
@@ -348,7 +367,7 @@ hipError_t linear_out(const LinearArgs& a, const Side& d, const void* x, int64_t
 // Blocks of 64 tokens are dealt so that about two thousand wavefronts (two a SIMD) each walk one segment: shorter ones cost
 // memory for the states between them, longer ones leave compute units idle.
 int linear_segment_for(const replayssm_linear_config& c) {
-  const int64_t work = (c.n_tokens + kRows - 1) / kRows * c.H * slices_of(c.dv, kSlice);
+  const int64_t work = (c.n_tokens + kRows - 1) / kRows * c.H * ((c.dv + kSlice - 1) / kSlice);
   int blocks = 4;
   while (blocks < 64 && work >= (int64_t)blocks * 2 * 2048) blocks *= 2;
   while (blocks < 1024 && c.H * (c.n_tokens / (blocks * kRows) + c.n_seqs) * ((c.dv + 31) / 32) > (int64_t)1 << 23) blocks *= 2;
