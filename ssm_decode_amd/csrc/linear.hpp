@@ -115,6 +115,8 @@ struct Blocks {
 // x, of which the compiler forgets that it does not change: what is computed from it in a loop stays in the loop. (Of the hundred
 // addresses in LDS that a block takes, each one exclusive-or away from a lane's few, it would keep every one in a register.)
 __device__ __forceinline__ void fresh(int& x) { asm volatile("" : "+v"(x)); }
+// x is computed here, and not where it is used, with all that it is made of kept until then.
+__device__ __forceinline__ void done(float& x) { asm volatile("" : "+v"(x)); }
 
 // 2^t with the fp32 remainder of t to first order: two ulp whatever the size of t, where 2^(float)t would be off by |t| 2^-24.
 __device__ __forceinline__ float decay_of(double t) {
@@ -222,10 +224,62 @@ struct ScalarFeed {
   }
 };
 
+// Eight values as two results of the matrix cores: unlike a vector of eight they need no eight registers in a row, which the
+// kernels here, close to all registers as they are, would pay for with memory.
+struct Eights {
+  f32x4 lo, hi;
+  __device__ __forceinline__ float operator[](int e) const { return e < 4 ? lo[e & 3] : hi[e & 3]; }
+};
+__device__ __forceinline__ Eights eights(const float* p) { return Eights{ld4(p), ld4(p + 4)}; }
+__device__ __forceinline__ Eights operator*(const Eights& a, const Eights& b) { return Eights{a.lo * b.lo, a.hi * b.hi}; }
+__device__ __forceinline__ Eights operator*(const Eights& a, float b) { return Eights{a.lo * b, a.hi * b}; }
+
+// As split8, bit for bit.
+template <int N>
+__device__ __forceinline__ Split<N> parts(const Eights& x) {
+#pragma clang fp contract(off)
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  Split<N> s;
+  u32x4 packed[N];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a = x[2 * e], b = x[2 * e + 1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t pair = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+      packed[i][e] = pair;
+      a -= bf16_lo(pair);
+      b -= bf16_hi(pair);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) s.p[i] = __builtin_bit_cast(bf16x8, packed[i]);
+  return s;
+}
+template <typename T>
+__device__ __forceinline__ Eights widened(const Raw8<T>& r) {
+  Eights x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x.lo[e] = (float)r.x[e];
+    x.hi[e] = (float)r.x[4 + e];
+  }
+  return x;
+}
+// As Raw8::split.
+template <typename T>
+__device__ __forceinline__ Split<Parts<T>::in> parts_of(const Raw8<T>& r) {
+  if constexpr (Parts<T>::in == 1)
+    return r.split();
+  else
+    return parts<Parts<T>::in>(widened(r));
+}
+
 // The eight weights of row r = 16 rt + n and columns 32 ks + 8 g .., up to the factor that pair_scale gives.
-__device__ __forceinline__ f32x8 pair_weights(const PairScalars* s, int rt, int ks, int n, int g) {
+__device__ __forceinline__ Eights pair_weights(const PairScalars* s, int rt, int ks, int n, int g) {
   const int r = 16 * rt + n, eight = 4 * ks + g;
-  return load8(eight == r >> 3 ? s->near[r] : s->tail + 8 * eight);
+  return eights(eight == r >> 3 ? s->near[r] : s->tail + 8 * eight);
 }
 // Gr: G of row r
 __device__ __forceinline__ float pair_scale(const PairScalars* s, double Gr, int rt, int ks, int n, int g) {
@@ -245,14 +299,16 @@ struct Reader {
   using T = Tile<W, N>;
   static constexpr int kRow = T::kRowBytes;
   const char* base;
-  int row_[2], dealt_[2], col_[2];
+  int row_[2], dealt_[2], col_[2], plain_[2], four_[2];
   __device__ __forceinline__ Reader(const T& t, int lane) : base(t.base) {
     const int n = lane & 15, g = lane >> 4, e = (lane >> 2) & 3, c = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       row_[i] = T::at(16 * i + n, g);
+      four_[i] = T::at(16 * i + n, g >> 1) + (g & 1) * 8;
       dealt_[i] = T::at(8 * (n >> 2) + 4 * i + (n & 3), g);
       col_[i] = T::at(8 * g + e + 4 * i, c);
+      plain_[i] = T::at(8 * g + e + 4 * i, c >> 1) + (c & 1) * 8;
     }
   }
   __device__ __forceinline__ void at(const T& t) { base = t.base; }
@@ -260,6 +316,8 @@ struct Reader {
   __device__ __forceinline__ void rows() { fresh(row_[0]), fresh(row_[1]); }
   __device__ __forceinline__ void dealts() { fresh(dealt_[0]), fresh(dealt_[1]); }
   __device__ __forceinline__ void columns() { fresh(col_[0]), fresh(col_[1]); }
+  __device__ __forceinline__ void plain_columns() { fresh(plain_[0]), fresh(plain_[1]); }
+  __device__ __forceinline__ void fours() { fresh(four_[0]), fresh(four_[1]); }
   __device__ __forceinline__ Split<N> read(int at) const {
     Split<N> s;
 #pragma unroll
@@ -269,12 +327,23 @@ struct Reader {
   // as Tile::row8 of row 16 rt + n, and of row dealt(t, n)
   __device__ __forceinline__ Split<N> row(int rt, int k) const { return read(((rt & 1 ? row_[1] : row_[0]) ^ (k << 6)) + (rt >> 1) * 32 * kRow); }
   __device__ __forceinline__ Split<N> dealt_row(int t, int k) const { return read(((t & 1 ? dealt_[1] : dealt_[0]) ^ (k << 6)) + (t >> 1) * 32 * kRow); }
+  // the values of row 16 rt + n, columns 16 i + 4 g ..
+  __device__ __forceinline__ f32x4 four(int rt, int i) const {
+    typedef __bf16 vec __attribute__((ext_vector_type(4)));
+    const char* p = base + ((rt & 1 ? four_[1] : four_[0]) ^ (i << 5)) + (rt >> 1) * 32 * kRow;
+    f32x4 x = __builtin_convertvector(*reinterpret_cast<const vec*>(p), f32x4);
+#pragma unroll
+    for (int q = 1; q < N; ++q) x += __builtin_convertvector(*reinterpret_cast<const vec*>(p + q * T::kPlane), f32x4);
+    return x;
+  }
   // as Tile::col8<true>(t, ks)
-  __device__ __forceinline__ Split<N> column(int t, int ks) const {
+  __device__ __forceinline__ Split<N> column(int t, int ks) const { return transposed(col_, (t >> 1) << 6, (t & 1) * 8 + ks * 32 * kRow); }
+  // as Tile::col8<false>(t, ks)
+  __device__ __forceinline__ Split<N> plain_column(int t, int ks) const { return transposed(plain_, t << 5, ks * 32 * kRow); }
+  __device__ __forceinline__ Split<N> transposed(const int (&at)[2], int turn, int more) const {
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-    const int more = (t & 1) * 8 + ks * 32 * kRow;
-    const char* lo = base + (col_[0] ^ ((t >> 1) << 6)) + more;
-    const char* hi = base + (col_[1] ^ ((t >> 1) << 6)) + more;
+    const char* lo = base + (at[0] ^ turn) + more;
+    const char* hi = base + (at[1] ^ turn) + more;
     Split<N> s;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -308,6 +377,20 @@ __device__ __forceinline__ void copies_landed() { __builtin_amdgcn_s_waitcnt(0x0
 // and widths that change on the way, go through registers.
 template <typename T, int DK>
 constexpr bool kCopied = sizeof(T) == 2 && Parts<T>::in == 1 && DK >= 32;
+
+// Rows in LDS: bf16 in two buffers, of which the copies fill one while the other is computed with; types that change on their way
+// in one.
+template <typename T, int DK>
+constexpr int kBuffers = kCopied<T, DK> ? 2 : 1;
+
+// The tiles of the scores, [c][rt] with 16 c <= 16 rt + 15 in pairs of c: which of the twelve.
+__device__ __forceinline__ constexpr int score_tile(int c, int rt) { return c < 2 ? 4 * c + rt : 8 + 2 * (c - 2) + rt - 2; }
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const f32x4& x) {
+  typedef T vec __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<vec*>(p) = __builtin_convertvector(x, vec);
+}
 
 // A lane's part in copying rows of W bf16 columns: a wavefront's instruction takes a piece of kStep rows. (The key of row kStep j
 // + r is that of kStep j exclusive-or that of r.)
@@ -566,10 +649,10 @@ struct KeyMajor {
     constexpr int kIn = Parts<T>::in, kGroup = kIn == 1 && kI >= 4 ? 4 : 2;  // operands asked for together
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const f32x8 w = load8(weights + 32 * ks + 8 * g);
+      const Eights w = eights(weights + 32 * ks + 8 * g);
       Split<N> zs[kM];
 #pragma unroll
-      for (int m = 0; m < kM; ++m) zs[m] = split8<N>(z[m][ks].f32() * w);
+      for (int m = 0; m < kM; ++m) zs[m] = parts<N>(widened(z[m][ks]) * w);
 #pragma unroll
       for (int i0 = 0; i0 < kI; i0 += kGroup) {
         Split<kIn> y[kGroup];

@@ -37,7 +37,7 @@ struct KeysArgs {
   const void* e;  // [Hk][dk] rows per token
   int64_t u_stride, w_stride, e_stride;
   void* out;       // [n_tokens][Hk][dk], or
-  float* partial;  // [parts][n_tokens][Hk][dk] where a key head has several workgroups
+  float* partial;  // [chunks][n_tokens][Hk][dk] where a key head has several workgroups
   Pairs* pairs;    // [slices][n_tokens][H]: written forwards, read backwards
   float* rho;      // [slices][segments][H]: written forwards, read backwards
   const float* other;  // forwards: the other side's starts
@@ -48,20 +48,27 @@ struct KeysArgs {
   Deal deal;
 };
 
+// LDS: e and the ring once, y and w twice where they are copied (e's next rows come when the ring is done with these). fp32, whose
+// rows would not fit, reads e from memory.
 template <typename T, int DK>
 struct KeysLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
-  // tiles of 16 rows whose results are summed over the wavefronts at a time (fp32, whose rows fill LDS, takes one)
-  static constexpr int kSumTiles = sizeof(T) == 4 ? 1 : 4;
-  // a wavefront's results of 16 channels, and, when those have been read, its three sums per row
-  static constexpr int kSum = kSumTiles * 64 * 16;
-  static constexpr int kWave = Values<T>::kBytes + (int)sizeof(PairScalars) + kSum;
-  static_assert(3 * kRows * 4 <= kSum, "room for both");
-  static constexpr int y = 0, waves = Rows::kBytes;
-  static int total(int n) { return waves + n * kWave; }
+  static constexpr bool kHasE = sizeof(T) == 2;
+  static constexpr int kTile = 4 * 64 * 16;  // 16 channels of 64 results
+  static constexpr int kRing = 32 * 1024;    // the results of eight tiles; before them the scores, behind them the sums per row
+  static constexpr int ring = 0, e = ring + kRing, y = e + (kHasE ? Rows::kBytes : 0);
+  static constexpr int kBuffer(int waves) { return Rows::kBytes + waves * Values<T>::kBytes; }
+  static constexpr int scalars(int waves) { return y + kBuffers<T, DK> * kBuffer(waves); }
+  static constexpr int total(int waves, int heads) { return scalars(waves) + heads * (int)sizeof(PairScalars); }
+  static_assert(DK / 16 * kTile <= kRing && 12 * 1024 <= kRing && kMaxWaves * 3 * kRows * 4 <= kRing, "what shares the ring's place");
+  // value heads of a workgroup, if a head has `slices`: most that fit
+  static constexpr int heads(int slices) {
+    int n = kMaxWaves / slices;
+    while (n > 1 && total(n * slices, n) > 160 * 1024) --n;
+    return n;
+  }
+  static_assert(total(kMaxWaves, 1) <= 160 * 1024, "a head of eight slices");
 };
-
-__device__ __forceinline__ int pair_frag(int rt, int ks) { return rt < 2 ? rt : 2 + 2 * (rt - 2) + ks; }
 
 // States in registers as [dv][dk]: S[m][i] is the tile of rows dealt(m, .) by dk columns 16 i + n.
 template <typename T, int DK>
@@ -97,10 +104,23 @@ struct ValueMajor {
   }
 };
 
+// f(integral constant i) for the i that is `which` (uniform), i < N.
+template <int N, typename F>
+__device__ __forceinline__ void for_one(int which, const F& f) {
+  if constexpr (N > 0) {
+    if (which == N - 1)
+      f(std::integral_constant<int, N - 1>());
+    else
+      for_one<N - 1>(which, f);
+  }
+}
+
+// The results of 16 key channels are summed over the wavefronts in a ring: at every step each wavefront takes another tile of
+// channels, adds its own to what the ones before it left in LDS, and hands it on. A tile passes the wavefronts in a fixed order.
 template <typename T, int DK, bool BACK>
-__global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const LinearArgs a, const KeysArgs p) {
+__global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const LinearArgs a, const KeysArgs p) {
   constexpr int in = Parts<T>::in, low = Parts<T>::low;
-  constexpr int kK = kWide<DK> / 32, kV = kTiles / 2;
+  constexpr int kK = kWide<DK> / 32, kI = DK / 16;
   constexpr int kWhole = 2 * in - 1 > kMid ? kMid : 2 * in - 1;  // products of inputs on the way to dg and dbeta: all (fp32: to 24 bits)
   using L = KeysLds<T, DK>;
   using State = ValueMajor<T, DK>;
@@ -108,6 +128,7 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
   const Side& d = p.d;
   const int part = blockIdx.x % p.deal.chunks, hk = blockIdx.x / p.deal.chunks % a.Hk, b = blockIdx.x / p.deal.chunks / a.Hk;
   const Segment seg = linear_segment(a, b);
+  const int waves = p.deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const Place at = place_of(a, p.deal, hk, part, wave);
@@ -116,18 +137,43 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
     if (!BACK && p.skips && at.live && lane == 0) p.skips[((int64_t)slice * a.max_segments + b) * a.H + at.head] = 0.f;
     return;
   }
-  char* mine = lds + L::waves + wave * L::kWave;
-  const typename L::Rows Y(lds + L::y);
-  const Values<T> W(mine);
-  PairScalars* rows = reinterpret_cast<PairScalars*>(mine + Values<T>::kBytes);
-  const int sum_at = L::waves + Values<T>::kBytes + (int)sizeof(PairScalars);  // of wavefront 0
-  const auto sum_of = [&](int w) { return reinterpret_cast<f32x4*>(lds + sum_at + w * L::kWave); };
-  const auto red_of = [&](int w) { return reinterpret_cast<float*>(lds + sum_at + w * L::kWave); };
-  const T* y = static_cast<const T*>(d.y) + (int64_t)hk * DK;
-  const T* e = static_cast<const T*>(p.e) + (int64_t)hk * DK;
+  float* ring = reinterpret_cast<float*>(lds + L::ring);
+  const typename L::Rows E(lds + L::e);
+  char* now = lds + L::y;
+  char* other = now + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
+  const auto Y = [&](char* q) { return typename L::Rows(q); };
+  const auto W = [&](char* q) { return Values<T>(q + L::Rows::kBytes + wave * Values<T>::kBytes); };
+  PairScalars* rows = reinterpret_cast<PairScalars*>(lds + L::scalars(waves)) + at.slot;
+  const bool makes = wave - at.slot * slices == at.slot * slices / 4 % slices;  // its head's tables (different heads' on different SIMDs)
   const int64_t head = (int64_t)at.head * a.dv + at.row0;
+  const T* e = static_cast<const T*>(p.e) + (int64_t)hk * DK;
   const T* u = static_cast<const T*>(p.u) + head;
-  const T* w = static_cast<const T*>(p.w) + head;
+  Reader<kWide<DK>, in> er(E, lane), yr(Y(now), lane);
+  RowFeed<T, DK> ef(e, p.e_stride, BACK), yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, BACK);
+  ValueFeed<T> wf(static_cast<const T*>(p.w) + head, p.w_stride, BACK, at.columns);
+  ScalarFeed scalars(a, d, at.head, seg.end);
+  Blocks blk(seg, BACK);
+  const int64_t u_step = BACK ? -p.u_stride : p.u_stride, e_step = BACK ? -p.e_stride : p.e_stride, u_lane = n * u_step;
+  // this wavefront's rows u of the block to come, as operands
+  Raw8<T> un[4];
+  const auto bring = [&](char* to) __attribute__((always_inline)) {
+    yf.stage(Y(to), blk, wave, threads);
+    wf.stage(W(to), blk);
+    scalars.load(blk);
+  };
+  const auto bring_u = [&]() __attribute__((always_inline)) {
+    const T* u0 = u + blk.token(0) * p.u_stride;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      if (16 * rt + n < blk.n && 8 * g < at.columns)
+        un[rt].load(u0 + 16 * rt * u_step + u_lane + 8 * g);
+      else
+        un[rt].zero();
+    }
+  };
+  bring(now);
+  bring_u();
+  if (L::kHasE) ef.stage(E, blk, wave, threads);
   const int64_t one = (int64_t)a.H * a.dv * DK, off = head * DK;
   State state;
   state.load(seg.count > 1 ? d.starts + b * one + off : d.first ? d.first + seg.s * one + off : nullptr, at.columns);
@@ -137,133 +183,159 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
     for (int s = 0; s < slices; ++s) rho += (double)p.rho[((int64_t)s * a.max_segments + b) * a.H + at.head];
   }
   float skips = 0.f;
-  RowFeed<T, DK> yf(y, d.y_stride, BACK);
-  ValueFeed<T> wf(w, p.w_stride, BACK, at.columns);
-  ScalarFeed scalars(a, d, at.head, seg.end);
-  for (Blocks blk(seg, BACK); blk.more(); blk.next()) {
-    __syncthreads();
-    yf.stage(Y, blk, wave, p.deal.waves * 64);
-    wf.stage(W, blk);
-    scalars.load(blk);
-    const double end = scalars.make(scalars.gates, rows);
+  const int64_t key_row = (int64_t)a.Hk * DK;
+  const int key_step = BACK ? -(int)key_row : (int)key_row;
+  float* partial = p.partial ? p.partial + part * (a.n_tokens * key_row) : nullptr;
+  while (true) {
     copies_landed();
     __syncthreads();
-    const float whole = decay_of(end);
-    // this wavefront's rows u, as operands
-    Split<in> U[4][kV];
-    const int64_t u_step = BACK ? -p.u_stride : p.u_stride, e_step = BACK ? -p.e_stride : p.e_stride;
-    const T* u0 = u + blk.token(0) * p.u_stride;
-    const T* e0 = e + blk.token(0) * p.e_stride;
+    const Blocks cur = blk;
+    blk.next();
+    const bool more = blk.more();
+    const ScalarFeed::Gates gates = scalars.gates;
+    Split<in> U[4];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
+    for (int rt = 0; rt < 4; ++rt) U[rt] = parts_of(un[rt]);
+    if (kBuffers<T, DK> == 2 && more) bring(other);
+    if (makes) scalars.make(gates, rows);
+    er.at(E), yr.at(Y(now));
+    er.rows(), yr.dealts(), yr.plain_columns();
+    const Values<T> Wn = W(now);
+    const T* e0 = e + cur.token(0) * p.e_stride;
+    // the scores of the key head, t[c][r] = y_c . e_r: the same for all wavefronts, which share the work
+    for (int q = wave; q < 12; q += waves) {
+      const int c = q < 8 ? q >> 2 : 2 + ((q - 8) >> 1), rt = q < 8 ? q & 3 : 2 + ((q - 8) & 1);
+      f32x4 t{};
 #pragma unroll
-      for (int ks = 0; ks < kV; ++ks) {
-        Raw8<T> x;
-        if (16 * rt + n < blk.n && 32 * ks + 8 * g < at.columns)
-          x.load(u0 + (16 * rt + n) * u_step + 32 * ks + 8 * g);
-        else
-          x.zero();
-        U[rt][ks] = x.split();
+      for (int k = 0; k < kK; ++k) {
+        Split<in> x;
+        if constexpr (L::kHasE) {
+          x = er.row(rt, k);
+        } else {
+          Raw8<T> raw;
+          if (16 * rt + n < cur.n && 32 * k + 8 * g < DK)
+            raw.load(e0 + (16 * rt + n) * e_step + 32 * k + 8 * g);
+          else
+            raw.zero();
+          x = parts_of(raw);
+        }
+        t = mma_to<kWhole>(yr.dealt_row(c, k), x, t);
       }
-    // pairs inside the block: D[r][c] = col_c e^{G_r - G_c} u_r . w_c, and their sums with e_r . y_c
+      st4(ring + (q * 64 + lane) * 4, t);
+    }
+    __syncthreads();
+    const double end = rows->G[kRows - 1];
+    // D[r][c] = col_c e^{G_r - G_c} u_r . w_c, and its sums with the scores
     Split<low> D[6];
     float inner[4], diag[4], outer[4];
+    int lane_now = lane;
+    fresh(lane_now);
+    const int n_now = lane_now & 15, g_now = lane_now >> 4, diagonal = n_now - 8 * g_now;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       inner[rt] = diag[rt] = outer[rt] = 0.f;
-      const int r = 16 * rt + n;
-      const double Gr = rows->G[r];
+      const double Gr = rows->G[16 * rt + n_now];
 #pragma unroll
       for (int ks = 0; ks <= rt / 2; ++ks) {
-        f32x4 p0{}, p1{}, t0{}, t1{};
-#pragma unroll
-        for (int k = 0; k < kV; ++k) {
-          p0 = mma_to<kWhole>(value_row<T>(W, dealt(2 * ks, n), k, g).split(), U[rt][k], p0);
-          p1 = mma_to<kWhole>(value_row<T>(W, dealt(2 * ks + 1, n), k, g).split(), U[rt][k], p1);
-        }
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          Raw8<T> x;
-          if (r < blk.n && 32 * k + 8 * g < DK)
-            x.load(e0 + r * e_step + 32 * k + 8 * g);
-          else
-            x.zero();
-          const Split<in> er = x.split();
-          t0 = mma_to<kWhole>(Y.row8(dealt(2 * ks, n), k, g), er, t0);
-          t1 = mma_to<kWhole>(Y.row8(dealt(2 * ks + 1, n), k, g), er, t1);
-        }
-        f32x8 dp = join(p0, p1);
-        const f32x8 tt = join(t0, t1), w8 = pair_weights(rows, rt, ks, n, g) * pair_scale(rows, Gr, rt, ks, n, g);
+        const Eights raw{mma_to<kWhole>(parts_of(value_row<T>(Wn, dealt(2 * ks, n_now), 0, g_now)), U[rt], f32x4{}),
+                               mma_to<kWhole>(parts_of(value_row<T>(Wn, dealt(2 * ks + 1, n_now), 0, g_now)), U[rt], f32x4{})};
+        const Eights tt{ld4(ring + (score_tile(2 * ks, rt) * 64 + lane_now) * 4), ld4(ring + (score_tile(2 * ks + 1, rt) * 64 + lane_now) * 4)};
+        const Eights x = raw * (pair_weights(rows, rt, ks, n_now, g_now) * pair_scale(rows, Gr, rt, ks, n_now, g_now));
+        const Eights both = x * tt;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int c = 32 * ks + 8 * g + i;
-          const float x = dp[i] * w8[i];
           if (ks == rt / 2) {
-            skips += c == r ? dp[i] : 0.f;
-            const float both = x * tt[i];
-            diag[rt] += c == r ? both : 0.f;
-            inner[rt] += c < r ? both : 0.f;
+            const bool own = i == diagonal + 16 * (rt & 1);
+            if (!BACK) skips += own ? raw[i] : 0.f;
+            diag[rt] += own ? both[i] : 0.f;
+            inner[rt] += own ? 0.f : both[i];  // (behind the diagonal the weights are 0)
           } else {
-            inner[rt] = __builtin_fmaf(x, tt[i], inner[rt]);
+            inner[rt] += both[i];
           }
-          dp[i] = x;
         }
-        D[pair_frag(rt, ks)] = split8<low>(dp);
+        D[rt < 2 ? rt : 2 + 2 * (rt - 2) + ks] = parts<low>(x);
+        done(inner[rt]), done(diag[rt]);
+        if (!BACK) done(skips);
+        step_ends();
       }
     }
-    // sixteen key channels at a time: their results, summed over the wavefronts, and their columns of the state
+    __syncthreads();  // the scores have been read
+    const float whole = decay_of(end);
+    float first[4], row[4];
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i) {
-      f32x4 acc[4];
+    for (int rt = 0; rt < 4; ++rt) {
+      first[rt] = rows->first[16 * rt + n];
+      row[rt] = rows->row[16 * rt + n];
+    }
+    // the ring
+    // (64 rows of keys lie within 2^31 elements)
+    const int64_t to_block = (cur.token(0) * a.Hk + hk) * DK;
+    const int turns = kI > waves ? kI : waves;
+#pragma unroll 1
+    for (int s = 0; s < turns; ++s) {
+      er.fours(), yr.plain_columns();
+      int lane_row = n, lane_at = lane * 4;
+      fresh(lane_row), fresh(lane_at);
+      int tile = wave + s;
+      if (tile >= turns) tile -= turns;
+      const bool opens = tile < waves ? wave == tile : wave == waves - 1;
+      const bool closes = tile < waves - 1 ? wave == tile + 1 : wave == 0;
+      for_one<kI>(tile, [&](auto which) __attribute__((always_inline)) {
+        constexpr int i = decltype(which)::value;
+        f32x4 acc[4];
+        const Split<kMid> sp = parts<kMid>(Eights{state.S[0][i], state.S[1][i]});
+        Split<in> ys[2];
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{};
-#pragma unroll
-      for (int ks = 0; ks < kV; ++ks)
-        if (32 * ks < at.columns) {
-          const Split<kMid> s = split8<kMid>(join(state.S[2 * ks][i], state.S[2 * ks + 1][i]));
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt) acc[rt] = mma(s, U[rt][ks], acc[rt]);
+        for (int ks = 0; ks < 2; ++ks) {
+          // column 16 i + n of rows 32 ks + 8 g ..
+          ys[ks] = yr.plain_column(i, ks);
         }
-      Split<in> ys[2];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) ys[ks] = Y.template col8<false>(i, ks, lane);
+        for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{};
+        products<kMid, in>([&](int x, int y) {
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const int r = 16 * rt + n;
-        acc[rt] *= rows->first[r];
-        if (r < blk.n) {
-          const T* er = e0 + r * e_step + 16 * i + 4 * g;
+          for (int rt = 0; rt < 4; ++rt) acc[rt] = mfma(sp.p[x], U[rt].p[y], acc[rt]);
+        });
 #pragma unroll
-          for (int j = 0; j < 4; ++j) outer[rt] = __builtin_fmaf(acc[rt][j], (float)er[j], outer[rt]);
+        for (int rt = 0; rt < 4; ++rt) {
+          acc[rt] *= first[rt];
+          f32x4 el;
+          if constexpr (L::kHasE)
+            el = er.four(rt, i);
+          else
+            el = 16 * rt + lane_row < cur.n ? ld4(reinterpret_cast<const float*>(e0 + (16 * rt + lane_row) * e_step + 16 * i + 4 * g)) : f32x4{};
+          outer[rt] = fma4(acc[rt], el, outer[rt]);
         }
+        products<in, low>([&](int x, int y) {
 #pragma unroll
-        for (int ks = 0; ks <= rt / 2; ++ks) acc[rt] = mma(ys[ks], D[pair_frag(rt, ks)], acc[rt]);
-        acc[rt] *= rows->row[r];
-      }
+          for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-      for (int r0 = 0; r0 < 4; r0 += L::kSumTiles) {
+            for (int ks = 0; ks <= rt / 2; ++ks) acc[rt] = mfma(ys[ks].p[x], D[rt < 2 ? rt : 2 + 2 * (rt - 2) + ks].p[y], acc[rt]);
+        });
+        float* slot = ring + i * (L::kTile / 4) + lane_at;
 #pragma unroll
-        for (int rt = 0; rt < L::kSumTiles; ++rt) sum_of(wave)[rt * 64 + lane] = at.live ? acc[r0 + rt] : f32x4{};
-        __syncthreads();
-        for (int v = threadIdx.x; v < L::kSumTiles * 64; v += p.deal.waves * 64) {
-          f32x4 s = sum_of(0)[v];
-          for (int k = 1; k < p.deal.waves; ++k) s += sum_of(k)[v];
-          const int r = 16 * (r0 + (v >> 6)) + (v & 15), c = 16 * i + 4 * ((v >> 4) & 3);
-          if (r < blk.n) {
-            const int64_t to = (blk.token(r) * a.Hk + hk) * DK + c;
-            if (p.partial) {
-              st4(p.partial + part * (a.n_tokens * a.Hk * DK) + to, s);
-            } else {
-              typedef T vec __attribute__((ext_vector_type(4)));
-              *reinterpret_cast<vec*>(static_cast<T*>(p.out) + to) = __builtin_convertvector(s, vec);
-            }
+        for (int rt = 0; rt < 4; ++rt) {
+          f32x4 o = at.live ? acc[rt] * row[rt] : f32x4{};
+          if (!opens) o += ld4(slot + rt * 256);
+          if (!closes) {
+            st4(slot + rt * 256, o);
+          } else if (16 * rt + lane_row < cur.n) {
+            const int to = (16 * rt + lane_row) * key_step + 16 * i + 4 * g;
+            if (p.partial)
+              st4(partial + to_block + to, o);
+            else
+              store4(static_cast<T*>(p.out) + to_block + to, o);
           }
         }
-        __syncthreads();
-      }
+      });
+      __syncthreads();
+    }
+    if (kBuffers<T, DK> == 2 && more) {
+      if (L::kHasE) ef.stage(E, blk, wave, threads);
+      bring_u();
     }
     // sums per row, over this head's slices
-    float* red = red_of(wave);
+    float* red = ring + wave * 3 * kRows;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       const float o = sum_groups(outer[rt]), s = sum_groups(inner[rt]), q = sum_groups(diag[rt]);
@@ -275,16 +347,16 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
     }
     __syncthreads();
     if (!BACK) {
-      if (at.live && lane < blk.n)
-        p.pairs[((int64_t)slice * a.n_tokens + blk.token(lane)) * a.H + at.head] =
+      if (at.live && lane < cur.n)
+        p.pairs[((int64_t)slice * a.n_tokens + cur.token(lane)) * a.H + at.head] =
             Pairs{red[lane] * rows->row[lane], red[kRows + lane] * rows->row[lane]};
     } else if (slice == 0) {
       float o = 0.f, s = 0.f, q = 0.f;
       double x = 0.0, within = 0.0;
-      const bool here = lane < blk.n;
-      const int64_t to = (here ? blk.token(lane) : blk.t0) * a.H + at.head;
+      const bool here = lane < cur.n;
+      const int64_t to = (here ? cur.token(lane) : cur.t0) * a.H + at.head;
       for (int k = 0; k < slices; ++k) {
-        const float* r = red_of(wave + k);
+        const float* r = ring + (wave + k) * 3 * kRows;
         o += r[lane];
         s += r[kRows + lane];
         q += r[2 * kRows + lane];
@@ -294,38 +366,49 @@ __global__ void __launch_bounds__(kMaxWaves * 64) linear_keys_kernel(const Linea
           within += (double)f.inner;
         }
       }
-      const double row = rows->row[lane], z = row * o;
-      double sum = here ? x + within - z - row * s : 0.0, span = here ? x - z : 0.0;
-#pragma unroll
-      for (int k = 1; k < 64; k <<= 1) {
-        const double up = __shfl_up(sum, k), wide = __shfl_up(span, k);
-        if (lane >= k) {
-          sum += up;
-          span += wide;
-        }
-      }
+      const double weight = rows->row[lane], z = weight * o;
+      const double sum = running_sum(here ? x + within - z - weight * s : 0.0), span = running_sum(here ? x - z : 0.0);
       if (here && at.live) {
         p.dg[to] = (float)(rho + sum);
         if (p.dbeta) p.dbeta[to] = o + s + q;
       }
-      rho += __shfl(span, 63);
+      rho += lane_value(span, 63);
     }
-    if (BACK && blk.final()) break;
     // the state behind the block
+    fresh(lane_now);
+    if (!BACK || more) {
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-      if (16 * (m & ~1) < at.columns) {
-        Split<kMid> z[2];
+      for (int ks = 0; ks < 2; ++ks) {
+        Split<kMid> z[kTiles];
+        const Eights weight = eights(rows->last + 32 * ks + 8 * (lane_now >> 4));
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) z[ks] = split8<kMid>(W.template read<true>(m, ks, lane).f32() * load8(rows->last + 32 * ks + 8 * g));
+        for (int m = 0; m < kTiles; ++m) z[m] = parts<kMid>(widened(Wn.template read<true>(m, ks, lane_now)) * weight);
 #pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-          f32x4 s = state.S[m][i] * whole;
+        for (int i = 0; i < kI; ++i) {
+          const Split<in> y = yr.plain_column(i, ks);
+          if (ks == 0) {
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) s = mma(z[ks], Y.template col8<false>(i, ks, lane), s);
-          state.S[m][i] = s;
+            for (int m = 0; m < kTiles; ++m) state.S[m][i] *= whole;
+          }
+          products<kMid, in>([&](int x, int v) {
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) state.S[m][i] = mfma(z[m].p[x], y.p[v], state.S[m][i]);
+          });
+          if (i & 1) step_ends();
         }
       }
+    }
+    if (!more) break;
+    if (kBuffers<T, DK> == 1) {
+      __syncthreads();
+      bring(now);
+      bring_u();
+      if (L::kHasE) ef.stage(E, blk, wave, threads);
+    } else {
+      char* t = now;
+      now = other;
+      other = t;
+    }
   }
   if (BACK) return;
   // what the pairs over the segment's end begin with, and the skip weight's gradient
@@ -377,9 +460,27 @@ struct KeysPlan {
 
 int64_t padded(int64_t bytes) { return (bytes + 255) & ~(int64_t)255; }
 
+template <typename T>
+int keys_heads_of(int dk, int slices) {
+  switch (dk) {
+    case 16: return KeysLds<T, 16>::heads(slices);
+    case 32: return KeysLds<T, 32>::heads(slices);
+    case 64: return KeysLds<T, 64>::heads(slices);
+    default: return KeysLds<T, 128>::heads(slices);
+  }
+}
+int keys_heads(const replayssm_linear_config& c, int slices) {
+  switch (c.dtype) {
+    case REPLAYSSM_BF16: return keys_heads_of<__bf16>(c.dk, slices);
+    case REPLAYSSM_F16: return keys_heads_of<_Float16>(c.dk, slices);
+    default: return keys_heads_of<float>(c.dk, slices);
+  }
+}
+
 KeysPlan keys_plan(const replayssm_linear_config& c, int max_segments) {
   KeysPlan p;
-  p.deal = deal(c.dv, c.H / c.Hk, kMaxWaves, kMaxWaves);
+  const int slices = (c.dv + kSlice - 1) / kSlice;
+  p.deal = deal(c.dv, c.H / c.Hk, kMaxWaves, keys_heads(c, slices));
   const int64_t side = linear_side_bytes(c, max_segments), per = padded((int64_t)p.deal.slices * max_segments * c.H * 4);
   p.forward = 0;
   p.reverse = side;
@@ -406,12 +507,10 @@ replayssm_linear_config config_of(const LinearArgs& a) {
 
 template <typename T, int DK, bool BACK>
 hipError_t start_keys(const LinearArgs& a, const KeysArgs& p, hipStream_t s) {
-  const int bytes = KeysLds<T, DK>::total(p.deal.waves);
-  static_assert(KeysLds<T, DK>::waves + kMaxWaves * KeysLds<T, DK>::kWave <= 160 * 1024, "the LDS of a compute unit");
   constexpr auto kernel = linear_keys_kernel<T, DK, BACK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(160 * 1024);
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * p.deal.chunks)), dim3(p.deal.waves * 64), bytes, s>>>(a, p);
+  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * p.deal.chunks)), dim3(p.deal.waves * 64), KeysLds<T, DK>::total(p.deal.waves, p.deal.heads), s>>>(a, p);
   return hipGetLastError();
 }
 

@@ -9,11 +9,6 @@ namespace {
 
 // ---- what each segment adds to the state --------------------------------------
 
-// Rows in LDS: bf16 in two buffers, of which the copies fill one while the other is computed with; types that change on their way
-// in one.
-template <typename T, int DK>
-constexpr int kBuffers = kCopied<T, DK> ? 2 : 1;
-
 template <typename T, int DK>
 struct StatesLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
@@ -47,7 +42,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_states_kernel(const 
   ValueFeed<T> zf(static_cast<const T*>(d.z) + (int64_t)at.head * a.dv + at.row0, d.z_stride, d.reverse, at.columns);
   ScalarFeed scalars(a, d, at.head, seg.end);
   Blocks blk(seg, d.reverse);
-  const auto bring = [&](char* to) {
+  const auto bring = [&](char* to) __attribute__((always_inline)) {
     yf.stage(Y(to), blk, wave, threads);
     zf.stage(Z(to), blk);
     scalars.load(blk);
@@ -128,15 +123,6 @@ struct OutLds {
   static_assert(total(kWaves<T>, kWaves<T> / 2) <= 160 * 1024, "heads of several slices fill the workgroup");
 };
 
-// The tiles of the scores, [c][rt] with 16 c <= 16 rt + 15 in pairs of c: which of the twelve.
-__device__ __forceinline__ constexpr int score_tile(int c, int rt) { return c < 2 ? 4 * c + rt : 8 + 2 * (c - 2) + rt - 2; }
-
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const f32x4& x) {
-  typedef T vec __attribute__((ext_vector_type(4)));
-  *reinterpret_cast<vec*>(p) = __builtin_convertvector(x, vec);
-}
-
 // Sequences without tokens, and the flag of those whose tables are bad.
 __device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d, const Deal& deal, int s, int hk, int chunk) {
   int b0;
@@ -188,7 +174,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   ValueFeed<T> zf(static_cast<const T*>(d.z) + head, d.z_stride, d.reverse, at.columns);
   ScalarFeed scalars(a, d, at.head, seg.end);
   Blocks blk(seg, d.reverse);
-  const auto bring = [&](char* to) {
+  const auto bring = [&](char* to) __attribute__((always_inline)) {
     xf.stage(X(to), blk, wave, threads);
     yf.stage(Y(to), blk, wave, threads);
     zf.stage(Z(to), blk);
@@ -207,20 +193,20 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
       state.zero();
   }
   const bool keep = closes && d.last != nullptr;
-  const int64_t out_row = (int64_t)a.H * a.dv, out_step = d.reverse ? -out_row : out_row, out_lane = n * out_step + 4 * g;
-  int diagonal = n - 8 * g;  // of the 16 rows of an even tile: the column e of a lane's eight that is its row's own
+  const int64_t out_row = (int64_t)a.H * a.dv;
+  const int out_step = d.reverse ? -(int)out_row : (int)out_row;  // (64 rows lie within 2^31 elements)
   while (true) {
     copies_landed();
     __syncthreads();
     const int live = blk.n;
-    T* to_rows = out + blk.token(0) * out_row + out_lane;
+    T* to_rows = out + blk.token(0) * out_row;
     blk.next();
     const bool more = blk.more();
     const ScalarFeed::Gates gates = scalars.gates;
     if (kBuffers<T, DK> == 2 && more) bring(other);
     if (makes) scalars.make(gates, rows);
     xr.at(X(now)), yr.at(Y(now)), zr.at(Z(now));
-    xr.rows(), yr.dealts(), yr.columns(), zr.columns(), fresh(diagonal);
+    xr.rows(), yr.dealts(), yr.columns(), zr.columns();
     // the scores of the key head, t[c][r] = y_c . x_r: the same for all wavefronts, which share the work
     for (int q = wave; q < 12; q += waves) {
       const int c = q < 8 ? q >> 2 : 2 + ((q - 8) >> 1), rt = q < 8 ? q & 3 : 2 + ((q - 8) & 1);
@@ -242,7 +228,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
       for (int rt = 0; rt < 4; ++rt) x[rt] = xr.row(rt, k);
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        const Split<low> s = split8<low>(join(state.S[2 * k][m], state.S[2 * k + 1][m]));
+        const Split<low> s = parts<low>(Eights{state.S[2 * k][m], state.S[2 * k + 1][m]});
         products<low, in>([&](int pi, int pj) {
 #pragma unroll
           for (int rt = 0; rt < 4; ++rt) acc[m][rt] = mfma(s.p[pi], x[rt].p[pj], acc[m][rt]);
@@ -253,6 +239,9 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
     __syncthreads();
     // what the block's own rows give, by P[r][c] = row_r col_c e^{G_r - G_c} t[c][r] with the skip weight on the diagonal
     const double end = rows->G[kRows - 1];
+    int lane_now = lane;
+    fresh(lane_now);
+    const int n_now = lane_now & 15, g_now = lane_now >> 4, diagonal = n_now - 8 * g_now;
     Raw8<T> z[kM][2];
 #pragma unroll
     for (int m = 0; m < kM; ++m)
@@ -260,30 +249,34 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
       for (int ks = 0; ks < 2; ++ks) z[m][ks] = zr.column(m, ks);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      const double Gr = rows->G[16 * rt + n];
-      const float row = rows->row[16 * rt + n], first = rows->first[16 * rt + n] * row;
+      const double Gr = rows->G[16 * rt + n_now];
+      const float row = rows->row[16 * rt + n_now], first = rows->first[16 * rt + n_now] * row;
 #pragma unroll
       for (int m = 0; m < kM; ++m) acc[m][rt] *= first;
 #pragma unroll
       for (int ks = 0; ks <= rt / 2; ++ks) {
-        const f32x8 t = join(ld4(scores + (score_tile(2 * ks, rt) * 64 + lane) * 4), ld4(scores + (score_tile(2 * ks + 1, rt) * 64 + lane) * 4));
-        f32x8 p = t * (pair_weights(rows, rt, ks, n, g) * (pair_scale(rows, Gr, rt, ks, n, g) * row));
+        const Eights t{ld4(scores + (score_tile(2 * ks, rt) * 64 + lane_now) * 4), ld4(scores + (score_tile(2 * ks + 1, rt) * 64 + lane_now) * 4)};
+        Eights p = t * (pair_weights(rows, rt, ks, n_now, g_now) * (pair_scale(rows, Gr, rt, ks, n_now, g_now) * row));
         if (ks == rt / 2 && skip != 0.f) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] += e == diagonal + 16 * (rt & 1) ? skip : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            p.lo[e] += e == diagonal + 16 * (rt & 1) ? skip : 0.f;
+            p.hi[e] += 4 + e == diagonal + 16 * (rt & 1) ? skip : 0.f;
+          }
         }
-        const Split<low> P = split8<low>(p);
+        const Split<low> P = parts<low>(p);
 #pragma unroll
-        for (int m = 0; m < kM; ++m) acc[m][rt] = mma(z[m][ks].split(), P, acc[m][rt]);
+        for (int m = 0; m < kM; ++m) acc[m][rt] = mma(parts_of(z[m][ks]), P, acc[m][rt]);
       }
       if (rt & 1) step_ends();
     }
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt)
-      if (at.live && 16 * rt + n < live) {
+      if (at.live && 16 * rt + n_now < live) {
+        T* to = to_rows + (16 * rt + n_now) * out_step + 4 * g_now;
 #pragma unroll
         for (int m = 0; m < kM; ++m)
-          if (16 * m < at.columns) store4(to_rows + 16 * rt * out_step + 16 * m, acc[m][rt]);
+          if (16 * m < at.columns) store4(to + 16 * m, acc[m][rt]);
       }
     // The state behind the block: in 24 bits where it is a result, in those of the outputs otherwise.
     const float whole = decay_of(end);
