@@ -33,10 +33,12 @@ namespace {
 
 constexpr int kRows = kBlock;
 
-// State rows (dv) that a wavefront holds, its slice of a head: two tiles of 16. (With four, which would share a block's scores among
-// twice the rows, the state and a block's results left the scheduler no registers at two wavefronts a SIMD, and it spilled.)
+// State rows (dv) that a wavefront holds, its slice of a head: M tiles of 16.
+template <int M>
+constexpr int kSlice = 16 * M;
+// States and outputs: two tiles. (With four, which would share a block's pairs among twice the rows, the state and a block's
+// results leave no registers for two wavefronts a SIMD; with one wavefront of 512 registers the outputs took a fifth longer.)
 constexpr int kTiles = 2;
-constexpr int kSlice = kTiles * 16;
 // Wavefronts of a workgroup, which share their key head's rows: all that fit LDS beside them.
 template <typename T>
 constexpr int kWaves = sizeof(T) == 4 ? 4 : 8;
@@ -455,50 +457,50 @@ struct RowFeed {
 };
 
 // A wavefront's own rows of z (a slice of a head's channels, `columns` of which exist) in their own type.
-template <typename T>
-using Values = ColumnTile<T, kSlice>;
+template <typename T, int M>
+using Values = ColumnTile<T, kSlice<M>>;
 
-template <typename T>
-__device__ __forceinline__ void put_value(const Values<T>& v, int row, int chunk, const Raw8<T>& x) {
+template <typename T, int M>
+__device__ __forceinline__ void put_value(const Values<T, M>& v, int row, int chunk, const Raw8<T>& x) {
   if constexpr (sizeof(T) == 2)
     *reinterpret_cast<bf16x8*>(v.tile.base + v.tile.at(row, chunk)) = __builtin_bit_cast(bf16x8, x.x);
   else
-    store8(v.base + row * Values<T>::kLdRow + chunk * 8, x.x);
+    store8(v.base + row * Values<T, M>::kLdRow + chunk * 8, x.x);
 }
 
 // Columns 32 ks + 8 g .. + 7 of a row.
-template <typename T>
-__device__ __forceinline__ Raw8<T> value_row(const Values<T>& v, int row, int ks, int g) {
+template <typename T, int M>
+__device__ __forceinline__ Raw8<T> value_row(const Values<T, M>& v, int row, int ks, int g) {
   Raw8<T> x;
   if constexpr (sizeof(T) == 2) {
     typedef T vec __attribute__((ext_vector_type(8)));
     x.x = __builtin_bit_cast(vec, *reinterpret_cast<const bf16x8*>(v.tile.base + v.tile.at(row, 4 * ks + g)));
   } else {
-    x.x = load8(v.base + row * Values<T>::kLdRow + 32 * ks + 8 * g);
+    x.x = load8(v.base + row * Values<T, M>::kLdRow + 32 * ks + 8 * g);
   }
   return x;
 }
 
-// Brings a wavefront's rows of z, `columns` of whose kSlice exist.
-template <typename T>
+// Brings a wavefront's rows of z, `columns` of whose kSlice<M> exist.
+template <typename T, int M>
 struct ValueFeed {
   const T* p;
   int64_t stride, step;
   int columns;
-  Copier<kSlice> copier;  // (bf16)
+  Copier<kSlice<M>> copier;  // (bf16)
   __device__ __forceinline__ ValueFeed(const T* rows, int64_t s, bool reverse, int c)
       : p(rows), stride(s), step(reverse ? -s : s), columns(c), copier(step) {}
-  __device__ __forceinline__ void stage(const Values<T>& tile, const Blocks& b) {
+  __device__ __forceinline__ void stage(const Values<T, M>& tile, const Blocks& b) {
     const T* base = p + b.token(0) * stride;
     if constexpr (kCopied<T, 32>) {
-      if (b.n == kRows && columns == kSlice) {
+      if (b.n == kRows && columns == kSlice<M>) {
         fresh(copier.chunk);
 #pragma unroll
-        for (int i = 0; i < Copier<kSlice>::kPieces; ++i) copier.copy(base, step, i, tile.tile.base);
+        for (int i = 0; i < Copier<kSlice<M>>::kPieces; ++i) copier.copy(base, step, i, tile.tile.base);
         return;
       }
     }
-    constexpr int kChunks = kSlice / 8, kUnits = kRows * kChunks, kBatch = kCopied<T, 32> ? 1 : 4;
+    constexpr int kChunks = kSlice<M> / 8, kUnits = kRows * kChunks, kBatch = kCopied<T, 32> ? 1 : 4;
     int u0 = threadIdx.x & 63;
     fresh(u0);
 #pragma unroll 1
@@ -513,28 +515,28 @@ struct ValueFeed {
           x[i].zero();
       }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) put_value<T>(tile, (u0 + i * 64) / kChunks, (u0 + i * 64) % kChunks, x[i]);
+      for (int i = 0; i < kBatch; ++i) put_value<T, M>(tile, (u0 + i * 64) / kChunks, (u0 + i * 64) % kChunks, x[i]);
     }
   }
 };
 
 // The same for a wavefront's rows of z: eight tokens 32 ks + 8 g .. of column 16 m + n (as ColumnTile::read<false>).
-template <typename T>
+template <typename T, int M>
 struct ValueReader {
   const char* base;
   int col_[2];
-  __device__ __forceinline__ ValueReader(const Values<T>& v, int lane) {
+  __device__ __forceinline__ ValueReader(const Values<T, M>& v, int lane) {
     if constexpr (sizeof(T) == 2) {
       base = v.tile.base;
       const int g = lane >> 4, e = (lane >> 2) & 3, c = lane & 3;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) col_[i] = Tile<kSlice, 1>::at(8 * g + e + 4 * i, c >> 1) + (c & 1) * 8;
+      for (int i = 0; i < 2; ++i) col_[i] = Tile<kSlice<M>, 1>::at(8 * g + e + 4 * i, c >> 1) + (c & 1) * 8;
     } else {
       base = reinterpret_cast<const char*>(v.base);
-      col_[0] = col_[1] = (8 * (lane >> 4) * Values<T>::kLdRow + (lane & 15)) * 4;
+      col_[0] = col_[1] = (8 * (lane >> 4) * Values<T, M>::kLdRow + (lane & 15)) * 4;
     }
   }
-  __device__ __forceinline__ void at(const Values<T>& v) {
+  __device__ __forceinline__ void at(const Values<T, M>& v) {
     if constexpr (sizeof(T) == 2)
       base = v.tile.base;
     else
@@ -546,14 +548,14 @@ struct ValueReader {
     if constexpr (sizeof(T) == 2) {
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
       typedef T vec __attribute__((ext_vector_type(8)));
-      constexpr int kRow = Tile<kSlice, 1>::kRowBytes;
+      constexpr int kRow = Tile<kSlice<M>, 1>::kRowBytes;
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(base + (col_[0] ^ (m << 5)) + ks * 32 * kRow));
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(base + (col_[1] ^ (m << 5)) + ks * 32 * kRow));
       r.x = __builtin_bit_cast(vec, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const float* c = reinterpret_cast<const float*>(base + col_[0]) + 32 * ks * Values<T>::kLdRow + 16 * m;
+      const float* c = reinterpret_cast<const float*>(base + col_[0]) + 32 * ks * Values<T, M>::kLdRow + 16 * m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r.x[e] = c[e * Values<T>::kLdRow];
+      for (int e = 0; e < 8; ++e) r.x[e] = c[e * Values<T, M>::kLdRow];
     }
     return r;
   }
@@ -565,9 +567,10 @@ struct Deal {
   int slices, heads, waves, parts, chunks;  // chunks: workgroups of a key head
 };
 
-inline Deal deal(int dv, int group, int most_waves, int most_heads) {
+// slice: state rows of a wavefront
+inline Deal deal(int dv, int slice, int group, int most_waves, int most_heads) {
   Deal d;
-  d.slices = (dv + kSlice - 1) / kSlice;
+  d.slices = (dv + slice - 1) / slice;
   d.parts = (d.slices + most_waves - 1) / most_waves;
   if (d.parts > 1) {
     d.heads = 1;
@@ -589,6 +592,7 @@ struct Place {
   bool live;              // (a wavefront without a slice computes with another's and writes nothing)
 };
 
+template <int M>
 __device__ __forceinline__ Place place_of(const LinearArgs& a, const Deal& d, int hk, int chunk, int wave) {
   const int group = a.H / a.Hk;
   Place p;
@@ -605,8 +609,8 @@ __device__ __forceinline__ Place place_of(const LinearArgs& a, const Deal& d, in
   p.live = head < group && slice < d.slices;
   p.slice = slice < d.slices ? slice : d.slices - 1;
   p.head = hk * group + (head < group ? head : group - 1);
-  p.row0 = p.slice * kSlice;
-  p.columns = a.dv - p.row0 < kSlice ? a.dv - p.row0 : kSlice;
+  p.row0 = p.slice * kSlice<M>;
+  p.columns = a.dv - p.row0 < kSlice<M> ? a.dv - p.row0 : kSlice<M>;
   return p;
 }
 

@@ -23,7 +23,13 @@ namespace rs {
 
 namespace {
 
-constexpr int kMaxWaves = 8;  // a head of 256 rows
+// Tiles of 16 state rows of a wavefront of linear_keys, and wavefronts of a workgroup (a head of 256 rows). bf16: four tiles and one
+// wavefront a SIMD with all its registers, so that a block's pairs serve twice the rows. Types of several parts hold operands
+// in too many registers for that: two tiles, two wavefronts.
+template <typename T>
+constexpr int kKeyTiles = sizeof(T) == 2 && Parts<T>::in == 1 ? 4 : 2;
+template <typename T>
+constexpr int kMaxWaves = 16 / kKeyTiles<T>;
 
 // What linear_keys leaves per token, head and slice: pairs with tokens in front of its block, and inside it.
 struct Pairs {
@@ -57,23 +63,23 @@ struct KeysLds {
   static constexpr int kTile = 4 * 64 * 16;  // 16 channels of 64 results
   static constexpr int kRing = 32 * 1024;    // the results of eight tiles; before them the scores, behind them the sums per row
   static constexpr int ring = 0, e = ring + kRing, y = e + (kHasE ? Rows::kBytes : 0);
-  static constexpr int kBuffer(int waves) { return Rows::kBytes + waves * Values<T>::kBytes; }
+  static constexpr int kBuffer(int waves) { return Rows::kBytes + waves * Values<T, kKeyTiles<T>>::kBytes; }
   static constexpr int scalars(int waves) { return y + kBuffers<T, DK> * kBuffer(waves); }
   static constexpr int total(int waves, int heads) { return scalars(waves) + heads * (int)sizeof(PairScalars); }
-  static_assert(DK / 16 * kTile <= kRing && 12 * 1024 <= kRing && kMaxWaves * 3 * kRows * 4 <= kRing, "what shares the ring's place");
+  static_assert(DK / 16 * kTile <= kRing && 12 * 1024 <= kRing && kMaxWaves<T> * 3 * kRows * 4 <= kRing, "what shares the ring's place");
   // value heads of a workgroup, if a head has `slices`: most that fit
   static constexpr int heads(int slices) {
-    int n = kMaxWaves / slices;
+    int n = kMaxWaves<T> / slices;
     while (n > 1 && total(n * slices, n) > 160 * 1024) --n;
     return n;
   }
-  static_assert(total(kMaxWaves, 1) <= 160 * 1024, "a head of eight slices");
+  static_assert(total(kMaxWaves<T>, 1) <= 160 * 1024, "a head of eight slices");
 };
 
 // States in registers as [dv][dk]: S[m][i] is the tile of rows dealt(m, .) by dk columns 16 i + n.
 template <typename T, int DK>
 struct ValueMajor {
-  static constexpr int kI = DK / 16, kM = kTiles;
+  static constexpr int kI = DK / 16, kM = kKeyTiles<T>;
   f32x4 S[kM][kI];
   __device__ __forceinline__ void load(const float* p, int columns) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -118,9 +124,9 @@ __device__ __forceinline__ void for_one(int which, const F& f) {
 // The results of 16 key channels are summed over the wavefronts in a ring: at every step each wavefront takes another tile of
 // channels, adds its own to what the ones before it left in LDS, and hands it on. A tile passes the wavefronts in a fixed order.
 template <typename T, int DK, bool BACK>
-__global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const LinearArgs a, const KeysArgs p) {
+__global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_keys_kernel(const LinearArgs a, const KeysArgs p) {
   constexpr int in = Parts<T>::in, low = Parts<T>::low;
-  constexpr int kK = kWide<DK> / 32, kI = DK / 16;
+  constexpr int kK = kWide<DK> / 32, kI = DK / 16, kM = kKeyTiles<T>, kV = kM / 2;
   constexpr int kWhole = 2 * in - 1 > kMid ? kMid : 2 * in - 1;  // products of inputs on the way to dg and dbeta: all (fp32: to 24 bits)
   using L = KeysLds<T, DK>;
   using State = ValueMajor<T, DK>;
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
   const int waves = p.deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Place at = place_of(a, p.deal, hk, part, wave);
+  const Place at = place_of<kM>(a, p.deal, hk, part, wave);
   const int slices = p.deal.slices, slice = at.slice;
   if (!seg.ok) {
     if (!BACK && p.skips && at.live && lane == 0) p.skips[((int64_t)slice * a.max_segments + b) * a.H + at.head] = 0.f;
@@ -142,7 +148,7 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
   char* now = lds + L::y;
   char* other = now + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
   const auto Y = [&](char* q) { return typename L::Rows(q); };
-  const auto W = [&](char* q) { return Values<T>(q + L::Rows::kBytes + wave * Values<T>::kBytes); };
+  const auto W = [&](char* q) { return Values<T, kKeyTiles<T>>(q + L::Rows::kBytes + wave * Values<T, kKeyTiles<T>>::kBytes); };
   PairScalars* rows = reinterpret_cast<PairScalars*>(lds + L::scalars(waves)) + at.slot;
   const bool makes = wave - at.slot * slices == at.slot * slices / 4 % slices;  // its head's tables (different heads' on different SIMDs)
   const int64_t head = (int64_t)at.head * a.dv + at.row0;
@@ -150,12 +156,12 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
   const T* u = static_cast<const T*>(p.u) + head;
   Reader<kWide<DK>, in> er(E, lane), yr(Y(now), lane);
   RowFeed<T, DK> ef(e, p.e_stride, BACK), yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, BACK);
-  ValueFeed<T> wf(static_cast<const T*>(p.w) + head, p.w_stride, BACK, at.columns);
+  ValueFeed<T, kM> wf(static_cast<const T*>(p.w) + head, p.w_stride, BACK, at.columns);
   ScalarFeed scalars(a, d, at.head, seg.end);
   Blocks blk(seg, BACK);
   const int64_t u_step = BACK ? -p.u_stride : p.u_stride, e_step = BACK ? -p.e_stride : p.e_stride, u_lane = n * u_step;
   // this wavefront's rows u of the block to come, as operands
-  Raw8<T> un[4];
+  Raw8<T> un[4][kV];
   const auto bring = [&](char* to) __attribute__((always_inline)) {
     yf.stage(Y(to), blk, wave, threads);
     wf.stage(W(to), blk);
@@ -165,10 +171,12 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
     const T* u0 = u + blk.token(0) * p.u_stride;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      if (16 * rt + n < blk.n && 8 * g < at.columns)
-        un[rt].load(u0 + 16 * rt * u_step + u_lane + 8 * g);
-      else
-        un[rt].zero();
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+        if (16 * rt + n < blk.n && 32 * k + 8 * g < at.columns)
+          un[rt][k].load(u0 + 16 * rt * u_step + u_lane + 32 * k + 8 * g);
+        else
+          un[rt][k].zero();
     }
   };
   bring(now);
@@ -193,14 +201,16 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
     blk.next();
     const bool more = blk.more();
     const ScalarFeed::Gates gates = scalars.gates;
-    Split<in> U[4];
+    Split<in> U[4][kV];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) U[rt] = parts_of(un[rt]);
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) U[rt][k] = parts_of(un[rt][k]);
     if (kBuffers<T, DK> == 2 && more) bring(other);
     if (makes) scalars.make(gates, rows);
     er.at(E), yr.at(Y(now));
     er.rows(), yr.dealts(), yr.plain_columns();
-    const Values<T> Wn = W(now);
+    const Values<T, kKeyTiles<T>> Wn = W(now);
     const T* e0 = e + cur.token(0) * p.e_stride;
     // the scores of the key head, t[c][r] = y_c . e_r: the same for all wavefronts, which share the work
     for (int q = wave; q < 12; q += waves) {
@@ -237,8 +247,12 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
       const double Gr = rows->G[16 * rt + n_now];
 #pragma unroll
       for (int ks = 0; ks <= rt / 2; ++ks) {
-        const Eights raw{mma_to<kWhole>(parts_of(value_row<T>(Wn, dealt(2 * ks, n_now), 0, g_now)), U[rt], f32x4{}),
-                               mma_to<kWhole>(parts_of(value_row<T>(Wn, dealt(2 * ks + 1, n_now), 0, g_now)), U[rt], f32x4{})};
+        Eights raw{};
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+          raw.lo = mma_to<kWhole>(parts_of(value_row<T, kM>(Wn, dealt(2 * ks, n_now), k, g_now)), U[rt][k], raw.lo);
+          raw.hi = mma_to<kWhole>(parts_of(value_row<T, kM>(Wn, dealt(2 * ks + 1, n_now), k, g_now)), U[rt][k], raw.hi);
+        }
         const Eights tt{ld4(ring + (score_tile(2 * ks, rt) * 64 + lane_now) * 4), ld4(ring + (score_tile(2 * ks + 1, rt) * 64 + lane_now) * 4)};
         const Eights x = raw * (pair_weights(rows, rt, ks, n_now, g_now) * pair_scale(rows, Gr, rt, ks, n_now, g_now));
         const Eights both = x * tt;
@@ -283,7 +297,6 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
       for_one<kI>(tile, [&](auto which) __attribute__((always_inline)) {
         constexpr int i = decltype(which)::value;
         f32x4 acc[4];
-        const Split<kMid> sp = parts<kMid>(Eights{state.S[0][i], state.S[1][i]});
         Split<in> ys[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -292,10 +305,14 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
         }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{};
-        products<kMid, in>([&](int x, int y) {
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) acc[rt] = mfma(sp.p[x], U[rt].p[y], acc[rt]);
-        });
+        for (int k = 0; k < kV; ++k) {
+          const Split<kMid> sp = parts<kMid>(Eights{state.S[2 * k][i], state.S[2 * k + 1][i]});
+          products<kMid, in>([&](int x, int y) {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) acc[rt] = mfma(sp.p[x], U[rt][k].p[y], acc[rt]);
+          });
+        }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           acc[rt] *= first[rt];
@@ -379,20 +396,20 @@ __global__ void __launch_bounds__(kMaxWaves * 64, 2) linear_keys_kernel(const Li
     if (!BACK || more) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        Split<kMid> z[kTiles];
+        Split<kMid> z[kM];
         const Eights weight = eights(rows->last + 32 * ks + 8 * (lane_now >> 4));
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) z[m] = parts<kMid>(widened(Wn.template read<true>(m, ks, lane_now)) * weight);
+        for (int m = 0; m < kM; ++m) z[m] = parts<kMid>(widened(Wn.template read<true>(m, ks, lane_now)) * weight);
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
           const Split<in> y = yr.plain_column(i, ks);
           if (ks == 0) {
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) state.S[m][i] *= whole;
+            for (int m = 0; m < kM; ++m) state.S[m][i] *= whole;
           }
           products<kMid, in>([&](int x, int v) {
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) state.S[m][i] = mfma(z[m].p[x], y.p[v], state.S[m][i]);
+            for (int m = 0; m < kM; ++m) state.S[m][i] = mfma(z[m].p[x], y.p[v], state.S[m][i]);
           });
           if (i & 1) step_ends();
         }
@@ -479,8 +496,10 @@ int keys_heads(const replayssm_linear_config& c, int slices) {
 
 KeysPlan keys_plan(const replayssm_linear_config& c, int max_segments) {
   KeysPlan p;
-  const int slices = (c.dv + kSlice - 1) / kSlice;
-  p.deal = deal(c.dv, c.H / c.Hk, kMaxWaves, keys_heads(c, slices));
+  const bool bf16 = c.dtype == REPLAYSSM_BF16;
+  const int slice = bf16 ? kSlice<kKeyTiles<__bf16>> : kSlice<kKeyTiles<float>>, most = bf16 ? kMaxWaves<__bf16> : kMaxWaves<float>;
+  static_assert(kKeyTiles<_Float16> == kKeyTiles<float>, "one shape for both");
+  p.deal = deal(c.dv, slice, c.H / c.Hk, most, keys_heads(c, (c.dv + slice - 1) / slice));
   const int64_t side = linear_side_bytes(c, max_segments), per = padded((int64_t)p.deal.slices * max_segments * c.H * 4);
   p.forward = 0;
   p.reverse = side;

@@ -12,7 +12,7 @@ namespace {
 template <typename T, int DK>
 struct StatesLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
-  static constexpr int kBuffer(int n) { return Rows::kBytes + n * Values<T>::kBytes; }
+  static constexpr int kBuffer(int n) { return Rows::kBytes + n * Values<T, kTiles>::kBytes; }
   static constexpr int scalars(int n) { return kBuffers<T, DK> * kBuffer(n); }
   static constexpr int total(int n) { return scalars(n) + n * (int)sizeof(RowScalars); }
   static_assert(total(kWaves<T>) <= 160 * 1024, "the LDS of a compute unit");
@@ -27,19 +27,19 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_states_kernel(const 
   if (!seg.ok || seg.index == (d.reverse ? 0 : seg.count - 1)) return;
   const int waves = deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place at = place_of(a, deal, hk, chunk, wave);
+  const Place at = place_of<kTiles>(a, deal, hk, chunk, wave);
   char* now = lds;
   char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
   const auto Y = [&](char* p) { return typename L::Rows(p); };
-  const auto Z = [&](char* p) { return Values<T>(p + L::Rows::kBytes + wave * Values<T>::kBytes); };
+  const auto Z = [&](char* p) { return Values<T, kTiles>(p + L::Rows::kBytes + wave * Values<T, kTiles>::kBytes); };
   RowScalars* rows = reinterpret_cast<RowScalars*>(lds + L::scalars(waves)) + wave;
   KeyMajor<T, DK> state;
   state.zero();
   double all = 0.0;
   Reader<kWide<DK>, Parts<T>::in> yr(Y(now), lane);
-  ValueReader<T> zr(Z(now), lane);
+  ValueReader<T, kTiles> zr(Z(now), lane);
   RowFeed<T, DK> yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, d.reverse);
-  ValueFeed<T> zf(static_cast<const T*>(d.z) + (int64_t)at.head * a.dv + at.row0, d.z_stride, d.reverse, at.columns);
+  ValueFeed<T, kTiles> zf(static_cast<const T*>(d.z) + (int64_t)at.head * a.dv + at.row0, d.z_stride, d.reverse, at.columns);
   ScalarFeed scalars(a, d, at.head, seg.end);
   Blocks blk(seg, d.reverse);
   const auto bring = [&](char* to) __attribute__((always_inline)) {
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
 template <typename T, int DK>
 struct OutLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
-  static constexpr int kBuffer(int n) { return 2 * Rows::kBytes + n * Values<T>::kBytes; }
+  static constexpr int kBuffer(int n) { return 2 * Rows::kBytes + n * Values<T, kTiles>::kBytes; }
   static constexpr int kScores = 12 * 1024;  // of the key head, fp32
   static constexpr int scores(int n) { return kBuffers<T, DK> * kBuffer(n); }
   static constexpr int scalars(int n) { return scores(n) + kScores; }
@@ -132,7 +132,7 @@ __device__ __forceinline__ void linear_empty(const LinearArgs& a, const Side& d,
     return;
   }
   if (seq.count != 0 || d.last == nullptr || d.last == d.first) return;
-  const Place at = place_of(a, deal, hk, chunk, threadIdx.x >> 6);
+  const Place at = place_of<kTiles>(a, deal, hk, chunk, threadIdx.x >> 6);
   if (!at.live) return;
   const int64_t base = (((int64_t)s * a.H + at.head) * a.dv + at.row0) * a.dk;
   for (int i = (threadIdx.x & 63) * 4; i < at.columns * a.dk; i += 256)
@@ -153,12 +153,12 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   const int waves = deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Place at = place_of(a, deal, hk, chunk, wave);
+  const Place at = place_of<kTiles>(a, deal, hk, chunk, wave);
   char* now = lds;
   char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
   const auto X = [&](char* p) { return typename L::Rows(p); };
   const auto Y = [&](char* p) { return typename L::Rows(p + L::Rows::kBytes); };
-  const auto Z = [&](char* p) { return Values<T>(p + 2 * L::Rows::kBytes + wave * Values<T>::kBytes); };
+  const auto Z = [&](char* p) { return Values<T, kTiles>(p + 2 * L::Rows::kBytes + wave * Values<T, kTiles>::kBytes); };
   float* scores = reinterpret_cast<float*>(lds + L::scores(waves));
   PairScalars* rows = reinterpret_cast<PairScalars*>(lds + L::scalars(waves)) + at.slot;
   // this wavefront makes its head's tables (those of a workgroup's heads on different SIMDs)
@@ -168,10 +168,10 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   const float skip = a.skip ? a.skip[at.head] : 0.f;
   const bool closes = seg.index == (d.reverse ? 0 : seg.count - 1);
   Reader<kWide<DK>, in> xr(X(now), lane), yr(Y(now), lane);
-  ValueReader<T> zr(Z(now), lane);
+  ValueReader<T, kTiles> zr(Z(now), lane);
   RowFeed<T, DK> xf(static_cast<const T*>(xs) + (int64_t)hk * DK, x_stride, d.reverse),
       yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, d.reverse);
-  ValueFeed<T> zf(static_cast<const T*>(d.z) + head, d.z_stride, d.reverse, at.columns);
+  ValueFeed<T, kTiles> zf(static_cast<const T*>(d.z) + head, d.z_stride, d.reverse, at.columns);
   ScalarFeed scalars(a, d, at.head, seg.end);
   Blocks blk(seg, d.reverse);
   const auto bring = [&](char* to) __attribute__((always_inline)) {
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
 template <typename T, int DK>
 hipError_t start_states(const LinearArgs& a, const Side& d, hipStream_t s) {
   using L = StatesLds<T, DK>;
-  const Deal way = deal(a.dv, a.H / a.Hk, kWaves<T>, kWaves<T>);
+  const Deal way = deal(a.dv, kSlice<kTiles>, a.H / a.Hk, kWaves<T>, kWaves<T>);
   constexpr auto kernel = linear_states_kernel<T, DK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(L::total(kWaves<T>));
   if (e != hipSuccess) return e;
@@ -315,7 +315,7 @@ hipError_t start_states(const LinearArgs& a, const Side& d, hipStream_t s) {
 template <typename T, int DK>
 hipError_t start_out(const LinearArgs& a, const Side& d, const void* x, int64_t x_stride, void* out, hipStream_t s) {
   using L = OutLds<T, DK>;
-  const Deal way = deal(a.dv, a.H / a.Hk, kWaves<T>, L::heads());
+  const Deal way = deal(a.dv, kSlice<kTiles>, a.H / a.Hk, kWaves<T>, L::heads());
   constexpr auto kernel = linear_out_kernel<T, DK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(160 * 1024);
   if (e != hipSuccess) return e;
@@ -360,7 +360,7 @@ hipError_t linear_out(const LinearArgs& a, const Side& d, const void* x, int64_t
 // Blocks of 64 tokens are dealt so that about two thousand wavefronts (two a SIMD) each walk one segment: shorter ones cost
 // memory for the states between them, longer ones leave compute units idle.
 int linear_segment_for(const replayssm_linear_config& c) {
-  const int64_t work = (c.n_tokens + kRows - 1) / kRows * c.H * ((c.dv + kSlice - 1) / kSlice);
+  const int64_t work = (c.n_tokens + kRows - 1) / kRows * c.H * ((c.dv + 31) / 32);
   int blocks = 4;
   while (blocks < 64 && work >= (int64_t)blocks * 2 * 2048) blocks *= 2;
   while (blocks < 1024 && c.H * (c.n_tokens / (blocks * kRows) + c.n_seqs) * ((c.dv + 31) / 32) > (int64_t)1 << 23) blocks *= 2;
