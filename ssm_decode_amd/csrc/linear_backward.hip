@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     }
     __syncthreads();
     const double end = rows->G[kRows - 1];
-    // D[r][c] = col_c e^{G_r - G_c} u_r . w_c, and its sums with the scores
+    // D[r][c] = row_r col_c e^{G_r - G_c} u_r . w_c, and its sums with the scores without row_r
     Split<low> D[6];
     float inner[4], diag[4], outer[4];
     int lane_now = lane;
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     for (int rt = 0; rt < 4; ++rt) {
       inner[rt] = diag[rt] = outer[rt] = 0.f;
       const double Gr = rows->G[16 * rt + n_now];
+      const float row = rows->row[16 * rt + n_now];
 #pragma unroll
       for (int ks = 0; ks <= rt / 2; ++ks) {
         Eights raw{};
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
             inner[rt] += both[i];
           }
         }
-        D[rt < 2 ? rt : 2 + 2 * (rt - 2) + ks] = parts<low>(x);
+        D[rt < 2 ? rt : 2 + 2 * (rt - 2) + ks] = parts<low>(x * row);
         done(inner[rt]), done(diag[rt]);
         if (!BACK) done(skips);
         step_ends();
@@ -275,12 +276,9 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     }
     __syncthreads();  // the scores have been read
     const float whole = decay_of(end);
-    float first[4], row[4];
+    float first[4];  // and the row's weight
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      first[rt] = rows->first[16 * rt + n];
-      row[rt] = rows->row[16 * rt + n];
-    }
+    for (int rt = 0; rt < 4; ++rt) first[rt] = rows->first[16 * rt + n] * rows->row[16 * rt + n];
     // the ring
     // (64 rows of keys lie within 2^31 elements)
     const int64_t to_block = (cur.token(0) * a.Hk + hk) * DK;
@@ -292,57 +290,66 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
       fresh(lane_row), fresh(lane_at);
       int tile = wave + s;
       if (tile >= turns) tile -= turns;
+      // the first and the last wavefront that a tile passes
       const bool opens = tile < waves ? wave == tile : wave == waves - 1;
       const bool closes = tile < waves - 1 ? wave == tile + 1 : wave == 0;
       for_one<kI>(tile, [&](auto which) __attribute__((always_inline)) {
         constexpr int i = decltype(which)::value;
-        f32x4 acc[4];
+        float* slot = ring + i * (L::kTile / 4) + lane_at;
+        f32x4 acc[4], before[4], el[4];
         Split<in> ys[2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          // column 16 i + n of rows 32 ks + 8 g ..
-          ys[ks] = yr.plain_column(i, ks);
-        }
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{};
-#pragma unroll
-        for (int k = 0; k < kV; ++k) {
-          const Split<kMid> sp = parts<kMid>(Eights{state.S[2 * k][i], state.S[2 * k + 1][i]});
-          products<kMid, in>([&](int x, int y) {
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) acc[rt] = mfma(sp.p[x], U[rt][k].p[y], acc[rt]);
-          });
-        }
+        for (int ks = 0; ks < 2; ++ks) ys[ks] = yr.plain_column(i, ks);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-          acc[rt] *= first[rt];
-          f32x4 el;
           if constexpr (L::kHasE)
-            el = er.four(rt, i);
+            el[rt] = er.four(rt, i);
           else
-            el = 16 * rt + lane_row < cur.n ? ld4(reinterpret_cast<const float*>(e0 + (16 * rt + lane_row) * e_step + 16 * i + 4 * g)) : f32x4{};
-          outer[rt] = fma4(acc[rt], el, outer[rt]);
+            el[rt] = 16 * rt + lane_row < cur.n ? ld4(reinterpret_cast<const float*>(e0 + (16 * rt + lane_row) * e_step + 16 * i + 4 * g)) : f32x4{};
+          acc[rt] = before[rt] = f32x4{};
         }
-        products<in, low>([&](int x, int y) {
+        if (!opens) {
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) before[rt] = ld4(slot + rt * 256);
+        }
+        if (at.live) {
+#pragma unroll
+          for (int k = 0; k < kV; ++k) {
+            const Split<kMid> sp = parts<kMid>(Eights{state.S[2 * k][i], state.S[2 * k + 1][i]});
+            products<kMid, in>([&](int x, int y) {
+#pragma unroll
+              for (int rt = 0; rt < 4; ++rt) acc[rt] = mfma(sp.p[x], U[rt][k].p[y], acc[rt]);
+            });
+          }
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            outer[rt] = fma4(acc[rt], el[rt], outer[rt]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[rt][e] = __builtin_fmaf(acc[rt][e], first[rt], before[rt][e]);
+          }
+          products<in, low>([&](int x, int y) {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+              for (int ks = 0; ks <= rt / 2; ++ks) acc[rt] = mfma(ys[ks].p[x], D[rt < 2 ? rt : 2 + 2 * (rt - 2) + ks].p[y], acc[rt]);
+          });
+        } else {
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) acc[rt] = before[rt];
+        }
+        if (!closes) {
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) st4(slot + rt * 256, acc[rt]);
+        } else {
 #pragma unroll
           for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int ks = 0; ks <= rt / 2; ++ks) acc[rt] = mfma(ys[ks].p[x], D[rt < 2 ? rt : 2 + 2 * (rt - 2) + ks].p[y], acc[rt]);
-        });
-        float* slot = ring + i * (L::kTile / 4) + lane_at;
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4 o = at.live ? acc[rt] * row[rt] : f32x4{};
-          if (!opens) o += ld4(slot + rt * 256);
-          if (!closes) {
-            st4(slot + rt * 256, o);
-          } else if (16 * rt + lane_row < cur.n) {
-            const int to = (16 * rt + lane_row) * key_step + 16 * i + 4 * g;
-            if (p.partial)
-              st4(partial + to_block + to, o);
-            else
-              store4(static_cast<T*>(p.out) + to_block + to, o);
-          }
+            if (16 * rt + lane_row < cur.n) {
+              const int to = (16 * rt + lane_row) * key_step + 16 * i + 4 * g;
+              if (partial)
+                st4(partial + to_block + to, acc[rt]);
+              else
+                store4(static_cast<T*>(p.out) + to_block + to, acc[rt]);
+            }
         }
       });
       __syncthreads();
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     float* red = ring + wave * 3 * kRows;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      const float o = sum_groups(outer[rt]), s = sum_groups(inner[rt]), q = sum_groups(diag[rt]);
+      const float o = sum_groups(outer[rt]) * rows->first[16 * rt + n], s = sum_groups(inner[rt]), q = sum_groups(diag[rt]);
       if (g == 0) {
         red[16 * rt + n] = o;
         red[kRows + 16 * rt + n] = s;
