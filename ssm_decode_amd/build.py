@@ -44,9 +44,14 @@ def common_flags():
     ]
 
 
+# The gradients' kernels have 512 registers a wavefront. Left to itself the compiler keeps all results of the matrix cores in the upper
+# half of them, where nothing else can use them, and moves every one down and back (394 us against 370, 16384 tokens, 64 heads).
+SOURCE_FLAGS = {"linear_backward.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc()] + common_flags() + ["-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc()] + common_flags() + SOURCE_FLAGS.get(src, []) + ["-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

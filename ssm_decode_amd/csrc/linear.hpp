@@ -117,6 +117,14 @@ struct Blocks {
 // x, of which the compiler forgets that it does not change: what is computed from it in a loop stays in the loop. (Of the hundred
 // addresses in LDS that a block takes, each one exclusive-or away from a lane's few, it would keep every one in a register.)
 __device__ __forceinline__ void fresh(int& x) { asm volatile("" : "+v"(x)); }
+// The lane, made anew (of no register): for what a loop does once a block, and would keep addresses for all the while.
+__device__ __forceinline__ int this_lane() {
+  int zero = 0;
+  fresh(zero);
+  return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+}
+// x, the same for all lanes, in a scalar register (what a division gives is not by itself).
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 // x is computed here, and not where it is used, with all that it is made of kept until then.
 __device__ __forceinline__ void done(float& x) { asm volatile("" : "+v"(x)); }
 
@@ -165,8 +173,10 @@ __device__ __forceinline__ double running_sum(double x) {
   x += row_shift<4>(x);
   x += row_shift<8>(x);
   const double a = lane_value(x, 15), b = a + lane_value(x, 31), c = b + lane_value(x, 47);
-  const int row = (threadIdx.x & 63) >> 4;
-  return x + (row == 0 ? 0.0 : row == 1 ? a : row == 2 ? b : c);
+  const int lane = this_lane();
+  double before = lane >= 16 ? a : 0.0;
+  before = lane >= 32 ? b : before;
+  return x + (lane >= 48 ? c : before);
 }
 
 // Makes them for one wavefront's head, lane r for row r: what they are made of is asked for a block ahead.
@@ -177,26 +187,32 @@ struct ScalarFeed {
   int end;  // the sequence's
   bool reverse;
   struct Gates {
-    float gate, col, row;
+    float gate, col, row;  // as read, by lanes behind the block's rows from its first
+    int n;
+    bool cut;  // row 0 has no decay: nothing was walked before it
   } gates;
   __device__ __forceinline__ ScalarFeed(const LinearArgs& a, const Side& d, int h, int seq_end)
       : g(a.g + h), col_from(d.beta ? d.beta + h : nullptr), row_from(d.row ? d.row + h : nullptr), step(a.H), col_weight(d.weight),
         row_weight(d.row_weight), end(seq_end), reverse(d.reverse) {}
-  __device__ __forceinline__ void load(const Blocks& b) {
-    const int lane = threadIdx.x & 63;
-    const bool live = lane < b.n;
-    const int64_t t = live ? b.token(lane) : b.t0;
+  __device__ __forceinline__ void load(const Blocks& b, int lane) {
+    const int row = lane < b.n ? lane : 0;
+    const int at = (reverse ? b.n - 1 - row : row) * (int)step;  // (64 rows lie within 2^31 elements)
+    const int64_t t0 = b.t0 * step;
+    gates.n = b.n;
     // backwards the decay between a token and the one walked before it is that one's own
-    const int64_t tg = reverse ? t + 1 : t;
-    gates.gate = live && tg < end ? g[tg * step] : 0.f;
-    gates.col = !live ? 0.f : col_from ? col_from[t * step] : col_weight;
-    gates.row = !live ? 0.f : row_from ? row_from[t * step] : row_weight;
+    gates.cut = reverse && b.t0 + b.n >= end;
+    gates.gate = g[t0 + (reverse && !(gates.cut && row == 0) ? at + (int)step : at)];
+    // (read from the gates where there are none: a load that may not be would hold its register from the block before)
+    gates.col = (col_from ? col_from : g)[t0 + at];
+    gates.row = (row_from ? row_from : g)[t0 + at];
   }
   // returns the block's whole exponent
   template <typename Scalars>
-  __device__ __forceinline__ static double make(const Gates& from, Scalars* out) {
-    const float gate = from.gate, col = from.col, row = from.row;
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ double make(const Gates& from, Scalars* out) const {
+    const int lane = this_lane();
+    const bool live = lane < from.n;
+    const float gate = live && !(from.cut && lane == 0) ? from.gate : 0.f, col = !live ? 0.f : col_from ? from.col : col_weight,
+                row = !live ? 0.f : row_from ? from.row : row_weight;
     const double sum = running_sum((double)closed_gate(gate) * kLog2e);
     const double whole = lane_value(sum, 63);
     out->G[lane] = sum;
@@ -357,15 +373,6 @@ struct Reader {
   }
 };
 
-// Of the two wavefronts on a SIMD one goes first, so that one's matrix instructions run while the other converts operands: with
-// equal priority they go through a block's phases together and wait for the same unit.
-__device__ __forceinline__ void take_turns(int wave) {
-  if (wave & 4)
-    __builtin_amdgcn_s_setprio(0);
-  else
-    __builtin_amdgcn_s_setprio(2);
-}
-
 // 16 bytes of every lane straight into LDS, to `to` (uniform) + 16 lane.
 __device__ __forceinline__ void copy16(const void* from, char* to) {
   typedef __attribute__((address_space(1))) const void* global_ptr;
@@ -401,8 +408,8 @@ struct Copier {
   static constexpr int kChunks = W / 8, kStep = 64 / kChunks, kPieces = kRows / kStep;
   int64_t offset;  // of the lane's row in the piece, in bytes
   int chunk;
-  __device__ __forceinline__ Copier(int64_t step) {
-    const int lane = threadIdx.x & 63, row = lane / kChunks;
+  __device__ __forceinline__ Copier(int64_t step, int lane) {
+    const int row = lane / kChunks;
     offset = row * step * 2;
     chunk = ((lane % kChunks) ^ Tile<W, 1>::key(row)) * 16;
   }
@@ -421,12 +428,12 @@ struct RowFeed {
   using Rows = Tile<W, Parts<T>::in>;
   const T* p;
   int64_t stride, step;
-  Copier<W> copier;
-  __device__ __forceinline__ RowFeed(const T* rows, int64_t s, bool reverse) : p(rows), stride(s), step(reverse ? -s : s), copier(step) {}
-  __device__ __forceinline__ void stage(const Rows& tile, const Blocks& b, int wave, int threads) {
+  __device__ __forceinline__ RowFeed(const T* rows, int64_t s, bool reverse) : p(rows), stride(s), step(reverse ? -s : s) {}
+  __device__ __forceinline__ void stage(const Rows& tile, const Blocks& b, int wave, int threads, int lane) {
     const T* base = p + b.token(0) * stride;
     if constexpr (kCopied<T, DK>) {
       if (b.n == kRows) {
+        Copier<W> copier(step, lane);
         fresh(copier.chunk);
         for (int i = wave; i < Copier<W>::kPieces; i += threads / 64) copier.copy(base, step, i, tile.base);
         return;
@@ -434,7 +441,7 @@ struct RowFeed {
     }
     // (a few at a time: in front of the copies' path registers are dear)
     constexpr int kChunks = W / 8, kUnits = kRows * kChunks, kBatch = kCopied<T, DK> ? 1 : 4;
-    int u0 = threadIdx.x;
+    int u0 = wave * 64 + lane;
     fresh(u0);
 #pragma unroll 1
     for (; u0 < kUnits; u0 += kBatch * threads) {
@@ -487,13 +494,13 @@ struct ValueFeed {
   const T* p;
   int64_t stride, step;
   int columns;
-  Copier<kSlice<M>> copier;  // (bf16)
   __device__ __forceinline__ ValueFeed(const T* rows, int64_t s, bool reverse, int c)
-      : p(rows), stride(s), step(reverse ? -s : s), columns(c), copier(step) {}
-  __device__ __forceinline__ void stage(const Values<T, M>& tile, const Blocks& b) {
+      : p(rows), stride(s), step(reverse ? -s : s), columns(c) {}
+  __device__ __forceinline__ void stage(const Values<T, M>& tile, const Blocks& b, int lane) {
     const T* base = p + b.token(0) * stride;
     if constexpr (kCopied<T, 32>) {
       if (b.n == kRows && columns == kSlice<M>) {
+        Copier<kSlice<M>> copier(step, lane);
         fresh(copier.chunk);
 #pragma unroll
         for (int i = 0; i < Copier<kSlice<M>>::kPieces; ++i) copier.copy(base, step, i, tile.tile.base);
@@ -501,7 +508,7 @@ struct ValueFeed {
       }
     }
     constexpr int kChunks = kSlice<M> / 8, kUnits = kRows * kChunks, kBatch = kCopied<T, 32> ? 1 : 4;
-    int u0 = threadIdx.x & 63;
+    int u0 = lane;
     fresh(u0);
 #pragma unroll 1
     for (; u0 < kUnits; u0 += kBatch * 64) {
@@ -565,6 +572,7 @@ struct ValueReader {
 // or, where a head has more slices than a workgroup wavefronts, one of `parts` parts of a head.
 struct Deal {
   int slices, heads, waves, parts, chunks;  // chunks: workgroups of a key head
+  int dies;                                 // that the workgroups' pairs are dealt to
 };
 
 // slice: state rows of a wavefront
@@ -584,6 +592,22 @@ inline Deal deal(int dv, int slice, int group, int most_waves, int most_heads) {
   d.heads = (group + d.chunks - 1) / d.chunks;  // (as even as they come)
   d.waves = d.heads * d.slices;
   return d;
+}
+
+// Which workgroup of `chunks` of one segment and key head this is, and which of those pairs it works for. Workgroups of a pair
+// read the same keys and queries: where there are pairs enough for every die they lie on one of them, and share its L2.
+struct Work {
+  int pair, chunk;
+  __device__ __forceinline__ explicit Work(const Deal& d) {
+    const int j = blockIdx.x / d.dies;
+    pair = uniform(j / d.chunks * d.dies + blockIdx.x % d.dies);
+    chunk = uniform(j % d.chunks);
+  }
+};
+// workgroups for `pairs` pairs
+inline unsigned grid_of(Deal& d, int64_t pairs) {
+  d.dies = d.chunks > 1 && pairs >= 64 ? 8 : 1;
+  return (unsigned)((pairs + d.dies - 1) / d.dies * d.dies * d.chunks);
 }
 
 struct Place {
@@ -607,8 +631,9 @@ __device__ __forceinline__ Place place_of(const LinearArgs& a, const Deal& d, in
     slice = wave % d.slices;
   }
   p.live = head < group && slice < d.slices;
-  p.slice = slice < d.slices ? slice : d.slices - 1;
-  p.head = hk * group + (head < group ? head : group - 1);
+  p.slot = uniform(p.slot);
+  p.slice = uniform(slice < d.slices ? slice : d.slices - 1);
+  p.head = uniform(hk * group + (head < group ? head : group - 1));
   p.row0 = p.slice * kSlice<M>;
   p.columns = a.dv - p.row0 < kSlice<M> ? a.dv - p.row0 : kSlice<M>;
   return p;

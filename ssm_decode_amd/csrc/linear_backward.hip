@@ -82,7 +82,7 @@ struct ValueMajor {
   static constexpr int kI = DK / 16, kM = kKeyTiles<T>;
   f32x4 S[kM][kI];
   __device__ __forceinline__ void load(const float* p, int columns) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int lane = this_lane(), n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int m = 0; m < kM; ++m)
 #pragma unroll
@@ -132,11 +132,11 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
   using State = ValueMajor<T, DK>;
   extern __shared__ __align__(16) char lds[];
   const Side& d = p.d;
-  const int part = blockIdx.x % p.deal.chunks, hk = blockIdx.x / p.deal.chunks % a.Hk, b = blockIdx.x / p.deal.chunks / a.Hk;
+  const Work work(p.deal);
+  const int part = work.chunk, hk = uniform(work.pair % a.Hk), b = uniform(work.pair / a.Hk);
   const Segment seg = linear_segment(a, b);
   const int waves = p.deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
   const Place at = place_of<kM>(a, p.deal, hk, part, wave);
   const int slices = p.deal.slices, slice = at.slice;
   if (!seg.ok) {
@@ -154,34 +154,34 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
   const int64_t head = (int64_t)at.head * a.dv + at.row0;
   const T* e = static_cast<const T*>(p.e) + (int64_t)hk * DK;
   const T* u = static_cast<const T*>(p.u) + head;
-  Reader<kWide<DK>, in> er(E, lane), yr(Y(now), lane);
   RowFeed<T, DK> ef(e, p.e_stride, BACK), yf(static_cast<const T*>(d.y) + (int64_t)hk * DK, d.y_stride, BACK);
   ValueFeed<T, kM> wf(static_cast<const T*>(p.w) + head, p.w_stride, BACK, at.columns);
   ScalarFeed scalars(a, d, at.head, seg.end);
   Blocks blk(seg, BACK);
-  const int64_t u_step = BACK ? -p.u_stride : p.u_stride, e_step = BACK ? -p.e_stride : p.e_stride, u_lane = n * u_step;
+  const int64_t u_step = BACK ? -p.u_stride : p.u_stride, e_step = BACK ? -p.e_stride : p.e_stride;
   // this wavefront's rows u of the block to come, as operands
   Raw8<T> un[4][kV];
   const auto bring = [&](char* to) __attribute__((always_inline)) {
-    yf.stage(Y(to), blk, wave, threads);
-    wf.stage(W(to), blk);
-    scalars.load(blk);
+    yf.stage(Y(to), blk, wave, threads, this_lane());
+    wf.stage(W(to), blk, this_lane());
+    scalars.load(blk, this_lane());
   };
   const auto bring_u = [&]() __attribute__((always_inline)) {
-    const T* u0 = u + blk.token(0) * p.u_stride;
+    const int lane = this_lane(), n = lane & 15, g = lane >> 4;
+    const T* u0 = u + blk.token(0) * p.u_stride + n * u_step + 8 * g;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
 #pragma unroll
       for (int k = 0; k < kV; ++k)
         if (16 * rt + n < blk.n && 32 * k + 8 * g < at.columns)
-          un[rt][k].load(u0 + 16 * rt * u_step + u_lane + 32 * k + 8 * g);
+          un[rt][k].load(u0 + 16 * rt * u_step + 32 * k);
         else
           un[rt][k].zero();
     }
   };
   bring(now);
   bring_u();
-  if (L::kHasE) ef.stage(E, blk, wave, threads);
+  if (L::kHasE) ef.stage(E, blk, wave, threads, this_lane());
   const int64_t one = (int64_t)a.H * a.dv * DK, off = head * DK;
   State state;
   state.load(seg.count > 1 ? d.starts + b * one + off : d.first ? d.first + seg.s * one + off : nullptr, at.columns);
@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
       for (int k = 0; k < kV; ++k) U[rt][k] = parts_of(un[rt][k]);
     if (kBuffers<T, DK> == 2 && more) bring(other);
     if (makes) scalars.make(gates, rows);
-    er.at(E), yr.at(Y(now));
-    er.rows(), yr.dealts(), yr.plain_columns();
+    int lane_now = this_lane();
+    int n_now = lane_now & 15, g_now = lane_now >> 4;
+    Reader<kWide<DK>, in> er(E, lane_now), yr(Y(now), lane_now);
     const Values<T, kKeyTiles<T>> Wn = W(now);
     const T* e0 = e + cur.token(0) * p.e_stride;
     // the scores of the key head, t[c][r] = y_c . e_r: the same for all wavefronts, which share the work
@@ -223,24 +224,24 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
           x = er.row(rt, k);
         } else {
           Raw8<T> raw;
-          if (16 * rt + n < cur.n && 32 * k + 8 * g < DK)
-            raw.load(e0 + (16 * rt + n) * e_step + 32 * k + 8 * g);
+          if (16 * rt + n_now < cur.n && 32 * k + 8 * g_now < DK)
+            raw.load(e0 + (16 * rt + n_now) * e_step + 32 * k + 8 * g_now);
           else
             raw.zero();
           x = parts_of(raw);
         }
         t = mma_to<kWhole>(yr.dealt_row(c, k), x, t);
       }
-      st4(ring + (q * 64 + lane) * 4, t);
+      st4(ring + (q * 64 + lane_now) * 4, t);
     }
     __syncthreads();
     const double end = rows->G[kRows - 1];
     // D[r][c] = row_r col_c e^{G_r - G_c} u_r . w_c, and its sums with the scores without row_r
     Split<low> D[6];
     float inner[4], diag[4], outer[4];
-    int lane_now = lane;
     fresh(lane_now);
-    const int n_now = lane_now & 15, g_now = lane_now >> 4, diagonal = n_now - 8 * g_now;
+    n_now = lane_now & 15, g_now = lane_now >> 4;
+    const int diagonal = n_now - 8 * g_now;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       inner[rt] = diag[rt] = outer[rt] = 0.f;
@@ -276,9 +277,13 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     }
     __syncthreads();  // the scores have been read
     const float whole = decay_of(end);
+    fresh(lane_now);
+    n_now = lane_now & 15, g_now = lane_now >> 4;
+    er = yr = Reader<kWide<DK>, in>(E, lane_now);
+    yr.at(Y(now));
     float first[4];  // and the row's weight
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) first[rt] = rows->first[16 * rt + n] * rows->row[16 * rt + n];
+    for (int rt = 0; rt < 4; ++rt) first[rt] = rows->first[16 * rt + n_now] * rows->row[16 * rt + n_now];
     // the ring
     // (64 rows of keys lie within 2^31 elements)
     const int64_t to_block = (cur.token(0) * a.Hk + hk) * DK;
@@ -286,8 +291,8 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
 #pragma unroll 1
     for (int s = 0; s < turns; ++s) {
       er.fours(), yr.plain_columns();
-      int lane_row = n, lane_at = lane * 4;
-      fresh(lane_row), fresh(lane_at);
+      int lane_row = n_now, lane_at = lane_now * 4, lane_four = 4 * g_now;
+      fresh(lane_row), fresh(lane_at), fresh(lane_four);
       int tile = wave + s;
       if (tile >= turns) tile -= turns;
       // the first and the last wavefront that a tile passes
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
           if constexpr (L::kHasE)
             el[rt] = er.four(rt, i);
           else
-            el[rt] = 16 * rt + lane_row < cur.n ? ld4(reinterpret_cast<const float*>(e0 + (16 * rt + lane_row) * e_step + 16 * i + 4 * g)) : f32x4{};
+            el[rt] = 16 * rt + lane_row < cur.n ? ld4(reinterpret_cast<const float*>(e0 + (16 * rt + lane_row) * e_step + 16 * i + lane_four)) : f32x4{};
           acc[rt] = before[rt] = f32x4{};
         }
         if (!opens) {
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
 #pragma unroll
           for (int rt = 0; rt < 4; ++rt)
             if (16 * rt + lane_row < cur.n) {
-              const int to = (16 * rt + lane_row) * key_step + 16 * i + 4 * g;
+              const int to = (16 * rt + lane_row) * key_step + 16 * i + lane_four;
               if (partial)
                 st4(partial + to_block + to, acc[rt]);
               else
@@ -355,42 +360,44 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
       __syncthreads();
     }
     if (kBuffers<T, DK> == 2 && more) {
-      if (L::kHasE) ef.stage(E, blk, wave, threads);
+      if (L::kHasE) ef.stage(E, blk, wave, threads, this_lane());
       bring_u();
     }
     // sums per row, over this head's slices
+    fresh(lane_now);
+    n_now = lane_now & 15, g_now = lane_now >> 4;
     float* red = ring + wave * 3 * kRows;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      const float o = sum_groups(outer[rt]) * rows->first[16 * rt + n], s = sum_groups(inner[rt]), q = sum_groups(diag[rt]);
-      if (g == 0) {
-        red[16 * rt + n] = o;
-        red[kRows + 16 * rt + n] = s;
-        red[2 * kRows + 16 * rt + n] = q;
+      const float o = sum_groups(outer[rt]) * rows->first[16 * rt + n_now], s = sum_groups(inner[rt]), q = sum_groups(diag[rt]);
+      if (g_now == 0) {
+        red[16 * rt + n_now] = o;
+        red[kRows + 16 * rt + n_now] = s;
+        red[2 * kRows + 16 * rt + n_now] = q;
       }
     }
     __syncthreads();
     if (!BACK) {
-      if (at.live && lane < cur.n)
-        p.pairs[((int64_t)slice * a.n_tokens + cur.token(lane)) * a.H + at.head] =
-            Pairs{red[lane] * rows->row[lane], red[kRows + lane] * rows->row[lane]};
+      if (at.live && lane_now < cur.n)
+        p.pairs[((int64_t)slice * a.n_tokens + cur.token(lane_now)) * a.H + at.head] =
+            Pairs{red[lane_now] * rows->row[lane_now], red[kRows + lane_now] * rows->row[lane_now]};
     } else if (slice == 0) {
       float o = 0.f, s = 0.f, q = 0.f;
       double x = 0.0, within = 0.0;
-      const bool here = lane < cur.n;
-      const int64_t to = (here ? cur.token(lane) : cur.t0) * a.H + at.head;
+      const bool here = lane_now < cur.n;
+      const int64_t to = (here ? cur.token(lane_now) : cur.t0) * a.H + at.head;
       for (int k = 0; k < slices; ++k) {
         const float* r = ring + (wave + k) * 3 * kRows;
-        o += r[lane];
-        s += r[kRows + lane];
-        q += r[2 * kRows + lane];
+        o += r[lane_now];
+        s += r[kRows + lane_now];
+        q += r[2 * kRows + lane_now];
         if (here) {
           const Pairs f = p.pairs[k * (a.n_tokens * a.H) + to];
           x += (double)f.outer;
           within += (double)f.inner;
         }
       }
-      const double weight = rows->row[lane], z = weight * o;
+      const double weight = rows->row[lane_now], z = weight * o;
       const double sum = running_sum(here ? x + within - z - weight * s : 0.0), span = running_sum(here ? x - z : 0.0);
       if (here && at.live) {
         p.dg[to] = (float)(rho + sum);
@@ -400,6 +407,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     }
     // the state behind the block
     fresh(lane_now);
+    yr = Reader<kWide<DK>, in>(Y(now), lane_now);
     if (!BACK || more) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
       __syncthreads();
       bring(now);
       bring_u();
-      if (L::kHasE) ef.stage(E, blk, wave, threads);
+      if (L::kHasE) ef.stage(E, blk, wave, threads, this_lane());
     } else {
       char* t = now;
       now = other;
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
     if (seg.t1 < seg.end) product *= expf(closed_gate(a.g[seg.t1 * a.H + at.head]));
   }
   skips = sum_width<64>(skips);
-  if (lane == 0 && at.live) {
+  if (this_lane() == 0 && at.live) {
     p.rho[to] = product;
     if (p.skips) p.skips[to] = skips;
   }
@@ -536,7 +544,9 @@ hipError_t start_keys(const LinearArgs& a, const KeysArgs& p, hipStream_t s) {
   constexpr auto kernel = linear_keys_kernel<T, DK, BACK>;
   const hipError_t e = allow_lds<decltype(kernel), kernel>(160 * 1024);
   if (e != hipSuccess) return e;
-  kernel<<<dim3((unsigned)(a.max_segments * a.Hk * p.deal.chunks)), dim3(p.deal.waves * 64), KeysLds<T, DK>::total(p.deal.waves, p.deal.heads), s>>>(a, p);
+  KeysArgs dealt = p;
+  const unsigned grid = grid_of(dealt.deal, (int64_t)a.max_segments * a.Hk);
+  kernel<<<dim3(grid), dim3(p.deal.waves * 64), KeysLds<T, DK>::total(p.deal.waves, p.deal.heads), s>>>(a, dealt);
   return hipGetLastError();
 }
 
