@@ -17,7 +17,9 @@ namespace rs {
 
 namespace {
 
-constexpr int kAhead = 8;        // tokens asked for at a time
+// Tokens asked for at a time. The gradients, with two rows a token, have registers for two wavefronts a SIMD with four, for one with
+// eight (332 us against 237 on 16384 tokens of 10240 channels in bf16).
+constexpr int kAhead = 8, kAheadBack = 4;
 constexpr int kConvWaves = 4;    // of a workgroup, each with a run of its own
 constexpr int kConvThreads = kConvWaves * 64;
 
@@ -109,17 +111,19 @@ __device__ __forceinline__ void conv_window(const ConvPromptArgs& a, int s, int 
   }
 }
 
-// Grid: x over runs of kConvWaves wavefronts (then over sequences, for the windows), y over 512 channels.
+// Grid: 512 channels, inside runs of kConvWaves wavefronts (then sequences, for the windows): workgroups that follow each other read
+// along a row (with a column's runs first: 237 us against 228 on 20011 tokens of 10240 channels in bf16).
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPromptArgs a, int run, int run_groups) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int unit = blockIdx.y * 64 + (threadIdx.x & 63);
-  if ((int)blockIdx.x >= run_groups) {
-    const int s = ((int)blockIdx.x - run_groups) * kConvWaves + wave;
+  const int columns = (a.D + 511) / 512, column = blockIdx.x % columns, group = blockIdx.x / columns;
+  const int unit = column * 64 + (threadIdx.x & 63);
+  if (group >= run_groups) {
+    const int s = (group - run_groups) * kConvWaves + wave;
     if (s < a.n_seqs) conv_window<T, W>(a, s, unit);
     return;
   }
-  const int64_t t0 = ((int64_t)blockIdx.x * kConvWaves + wave) * run;
+  const int64_t t0 = ((int64_t)group * kConvWaves + wave) * run;
   const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
   if (t0 >= t1) return;
   const bool live = 8 * unit < a.D;
@@ -204,9 +208,10 @@ template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(const ConvPromptArgs a, int run, int run_groups) {
   __shared__ __align__(16) float sums[kConvWaves][64 * 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int unit = blockIdx.y * 64 + lane;
-  if ((int)blockIdx.x >= run_groups) {
-    const int s = ((int)blockIdx.x - run_groups) * kConvWaves + wave;
+  const int columns = (a.D + 511) / 512, column = blockIdx.x % columns, group = blockIdx.x / columns;
+  const int unit = column * 64 + lane;
+  if (group >= run_groups) {
+    const int s = (group - run_groups) * kConvWaves + wave;
     if (s < a.n_seqs) conv_dfirst<T, W, SILU>(a, s, unit);
     return;
   }
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
 #pragma unroll
   for (int j = 0; j < W; ++j) dw[j] = f32x8{};
   // runs of this wavefront
-  for (int64_t t0 = ((int64_t)blockIdx.x * kConvWaves + wave) * run; t0 < a.n_tokens; t0 += (int64_t)run_groups * kConvWaves * run) {
+  for (int64_t t0 = ((int64_t)group * kConvWaves + wave) * run; t0 < a.n_tokens; t0 += (int64_t)run_groups * kConvWaves * run) {
     const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
     int64_t at = t0;
     while (at < t1) {
@@ -233,10 +238,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
       th.history(q, (int)(at - q.begin), h);
 #pragma unroll
       for (int j = 0; j < W; ++j) e[j] = f32x8{};
-      Eight<T> xn[kAhead], dn[kAhead];
+      Eight<T> xn[kAheadBack], dn[kAheadBack];
       const auto fetch = [&](int64_t t) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kAheadBack; ++i) {
           const int64_t r = t + i < a.n_tokens ? t + i : a.n_tokens - 1;
           xn[i] = raw8(th.x + r * a.x_stride);
           dn[i] = raw8(dy + r * a.D);
@@ -244,16 +249,16 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
       };
       fetch(at);
       const int64_t stop = to + W - 1;
-      for (int64_t t = at; t < stop; t += kAhead) {
-        Eight<T> xs[kAhead], ds[kAhead];
+      for (int64_t t = at; t < stop; t += kAheadBack) {
+        Eight<T> xs[kAheadBack], ds[kAheadBack];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kAheadBack; ++i) {
           xs[i] = xn[i];
           ds[i] = dn[i];
         }
-        if (t + kAhead < stop) fetch(t + kAhead);
+        if (t + kAheadBack < stop) fetch(t + kAheadBack);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kAheadBack; ++i) {
           if (t + i < stop) {
             f32x8 g{};
             if (t + i < q.end) {
@@ -293,13 +298,13 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
     }
   }
   if (a.partial == nullptr) return;
-  float* part = a.partial + (int64_t)blockIdx.x * (W + 1) * a.D;
+  float* part = a.partial + (int64_t)group * (W + 1) * a.D;
 #pragma unroll
   for (int j = 0; j <= W; ++j) {
     store8(&sums[wave][lane * 8], j < W ? dw[j < W ? j : 0] : db);
     __syncthreads();
     for (int c = threadIdx.x; c < 512; c += kConvThreads) {
-      const int channel = blockIdx.y * 512 + c;
+      const int channel = column * 512 + c;
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < kConvWaves; ++v) s += sums[v][c];
@@ -342,6 +347,7 @@ ConvPlan conv_plan(int64_t n_tokens, int D) {
   const int64_t columns = (D + 511) / 512;
   ConvPlan p;
   p.run = n_tokens / 32 * columns >= 4096 ? 32 : kAhead;
+  while (n_tokens / (p.run * kConvWaves) * columns >= 1 << 23) p.run *= 2;  // (threads of a grid are fewer than 2^32)
   p.groups = (int)((n_tokens + p.run * kConvWaves - 1) / (p.run * kConvWaves));
   return p;
 }
@@ -361,7 +367,7 @@ ConvPlan conv_backward_plan(int64_t n_tokens, int D) {
 template <typename T, int W, bool SILU>
 hipError_t conv_start(const ConvPromptArgs& a, bool backward, hipStream_t s) {
   const ConvPlan p = backward ? conv_backward_plan(a.n_tokens, a.D) : conv_plan(a.n_tokens, a.D);
-  const dim3 grid((unsigned)(p.groups + (a.n_seqs + kConvWaves - 1) / kConvWaves), (unsigned)((a.D + 511) / 512));
+  const dim3 grid((unsigned)((p.groups + (a.n_seqs + kConvWaves - 1) / kConvWaves) * ((a.D + 511) / 512)));
   if (!backward) {
     conv_prompt_kernel<T, W, SILU><<<grid, dim3(kConvThreads), 0, s>>>(a, p.run, p.groups);
     return hipGetLastError();
