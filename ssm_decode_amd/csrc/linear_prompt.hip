@@ -115,7 +115,10 @@ struct OutLds {
   using Rows = Tile<kWide<DK>, Parts<T>::in>;
   static constexpr int kBuffer(int n) { return 2 * Rows::kBytes + n * Values<T, kTiles>::kBytes; }
   static constexpr int kScores = 12 * 1024;  // of the key head, fp32
-  static constexpr int scores(int n) { return kBuffers<T, DK> * kBuffer(n); }
+  // Rows that are copied have two buffers where a workgroup fills the compute unit, one where two workgroups of four wavefronts or fewer
+  // share it: each then computes while the other waits.
+  static constexpr int buffers(int n) { return n > kWaves<T> / 2 ? kBuffers<T, DK> : 1; }
+  static constexpr int scores(int n) { return buffers(n) * kBuffer(n); }
   static constexpr int scalars(int n) { return scores(n) + kScores; }
   static constexpr int total(int n, int heads) { return scalars(n) + heads * (int)sizeof(PairScalars); }
   // value heads of a workgroup: most that fit
@@ -161,7 +164,8 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   const int n = lane & 15, g = lane >> 4;
   const Place at = place_of<kTiles>(a, deal, hk, chunk, wave);
   char* now = lds;
-  char* other = lds + (kBuffers<T, DK> - 1) * L::kBuffer(waves);
+  const bool ahead = L::buffers(waves) == 2;
+  char* other = ahead ? lds + L::kBuffer(waves) : lds;
   const auto X = [&](char* p) { return typename L::Rows(p); };
   const auto Y = [&](char* p) { return typename L::Rows(p + L::Rows::kBytes); };
   const auto Z = [&](char* p) { return Values<T, kTiles>(p + 2 * L::Rows::kBytes + wave * Values<T, kTiles>::kBytes); };
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
     blk.next();
     const bool more = blk.more();
     const ScalarFeed::Gates gates = scalars.gates;
-    if (kBuffers<T, DK> == 2 && more) bring(other);
+    if (ahead && more) bring(other);
     if (makes) scalars.make(gates, rows);
     xr.at(X(now)), yr.at(Y(now)), zr.at(Z(now));
     xr.rows(), yr.dealts(), yr.columns(), zr.columns();
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
     else if (more)
       state.template update<low>(whole, yr, z, rows->last);
     if (!more) break;
-    if (kBuffers<T, DK> == 1) {
+    if (!ahead) {
       __syncthreads();
       bring(now);
     } else {
