@@ -10,7 +10,8 @@
 // which gives a 128 x 128 head four workgroups: one sequence of 32 heads then still
 // covers 128 compute units. Measured at 256 sequences of 32 heads of 128 x 128: 196 us, 5.5 TB/s of
 // state read and written; with 64 or 128 rows per workgroup 206 and 209 us; with non-temporal stores,
-// which give up the write-back cache's merging, 294 us. One sequence: 4.5 us.
+// which give up the write-back cache's merging, 294 us. One sequence: 4.5 us. Linear attention at 256
+// sequences of 128 heads of 64 x 128: 368 us, 5.9 TB/s.
 #include "element.hpp"
 #include "prompt.hpp"
 
