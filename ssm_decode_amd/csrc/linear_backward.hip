@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
   const Side& d = p.d;
   const Work work(p.deal);
   const int part = work.chunk, hk = uniform(work.pair % a.Hk), b = uniform(work.pair / a.Hk);
+  if (b >= a.max_segments) return;  // (pairs are dealt to whole rounds of the dies)
   const Segment seg = linear_segment(a, b);
   const int waves = p.deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -465,17 +466,20 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
   }
 }
 
-// dst = sum of the parts, in the type of the gradients, for the tokens of a segment. (Rows of no sequence are left as they were.)
+// dst = sum of the parts, in the type of the gradients, for the tokens of the segments (a grid is at most 65535 high). (Rows of no sequence are left as they were.)
 template <typename T>
 __global__ void __launch_bounds__(256) linear_sum_kernel(const LinearArgs a, const float* partial, int parts, T* dst) {
-  const Segment seg = linear_segment(a, blockIdx.y);
-  if (!seg.ok) return;
   const int row = a.Hk * a.dk;
-  const int64_t size = a.n_tokens * row, end = seg.t1 * row;
-  for (int64_t at = seg.t0 * row + ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < end; at += (int64_t)gridDim.x * 2048) {
-    f32x8 s = load8(partial + at);
-    for (int p = 1; p < parts; ++p) s += load8(partial + p * size + at);
-    store8(dst + at, s);
+  const int64_t size = a.n_tokens * row;
+  for (int b = blockIdx.y; b < a.max_segments; b += gridDim.y) {
+    const Segment seg = linear_segment(a, b);
+    if (!seg.ok) continue;
+    const int64_t end = seg.t1 * row;
+    for (int64_t at = seg.t0 * row + ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < end; at += (int64_t)gridDim.x * 2048) {
+      f32x8 s = load8(partial + at);
+      for (int p = 1; p < parts; ++p) s += load8(partial + p * size + at);
+      store8(dst + at, s);
+    }
   }
 }
 
@@ -568,7 +572,7 @@ hipError_t keys(const LinearArgs& a, const KeysArgs& p, hipStream_t s) {
   }
   if (e != hipSuccess || p.partial == nullptr) return e;
   const int64_t units = ((int64_t)a.segment * a.Hk * a.dk + 2047) / 2048;
-  linear_sum_kernel<T><<<dim3((unsigned)(units < 1024 ? units : 1024), (unsigned)a.max_segments), dim3(256), 0, s>>>(a, p.partial, p.deal.chunks,
+  linear_sum_kernel<T><<<dim3((unsigned)(units < 1024 ? units : 1024), (unsigned)(a.max_segments < 32768 ? a.max_segments : 32768)), dim3(256), 0, s>>>(a, p.partial, p.deal.chunks,
                                                                                                                   static_cast<T*>(p.out));
   return hipGetLastError();
 }

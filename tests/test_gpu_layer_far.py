@@ -93,3 +93,31 @@ def test_states_of_segments_past_2_31():
     rs.linear_prompt(cfg, m.struct, *(put(x) for x in (a.q, a.k, a.v, a.g, a.beta)), None, None, out, last, ws, a.err)
     assert int(a.err[0]) == 0 and torch.equal(out[big:], want[0]) and torch.equal(last[1], want[1][0])
     assert not out[:big].any() and not last[0].any()
+
+
+def test_more_segments_than_a_grid_is_high():
+    """16384 sequences in 66000 segments, several workgroups a key head: the last sequence comes out as it does alone."""
+    kw = dict(H=5, Hk=1, dk=16, dv=16, dtype="bf16", wide=False, s0=False)
+    a = Linear([197], **kw)
+    out, last = a.forward()
+    grads = a.backward(want=("dbeta", "dskip"))
+    N, n = 16384, 197
+    T = N * n
+    assert T // 64 + N > 65536
+    cfg = rs.make_linear_config(N, T, 5, 1, 16, 16, dtype="bf16", scale=a.scale, segment=64)
+    m = rs.RaggedMaps(rs.make_ragged_config(N, T, 64))
+    rs.ragged_maps(m.cfg, m.struct, torch.full((N,), n, dtype=torch.int32, device="cuda"))
+    big = T - n
+    put = lambda x: torch.cat([torch.zeros((big,) + x.shape[1:], dtype=x.dtype, device="cuda"), x])  # noqa: E731
+    args = [put(x) for x in (a.q, a.k, a.v, a.g, a.beta)]
+    o, S = torch.empty((T, 5, 16), dtype=torch.bfloat16, device="cuda"), torch.empty((N, 5, 16, 16), device="cuda")
+    sizes = rs.linear_sizes(cfg)
+    rs.linear_prompt(cfg, m.struct, *args, a.skip, None, o, S, torch.empty(sizes[0], dtype=torch.uint8, device="cuda"), a.err)
+    assert torch.equal(o[big:], out) and torch.equal(S[-1], last[0]) and not o[:big].any()
+    new = lambda x: torch.full((T,) + x.shape[1:], 7.0, dtype=x.dtype, device="cuda")  # noqa: E731
+    r = {x: new(grads[x]) for x in ("dq", "dk", "dv", "dg", "dbeta")} | {"dskip": torch.empty_like(grads["dskip"])}
+    rs.linear_prompt_backward(cfg, m.struct, *args, a.skip, None, put(a.do), None, *r.values(), None,
+                              torch.empty(sizes[1], dtype=torch.uint8, device="cuda"), a.err)
+    assert int(a.err[0]) == 0 and torch.equal(r["dskip"], grads["dskip"])
+    for x in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(r[x][big:], grads[x]) and not r[x][:big].any(), x

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import ssm_decode_amd as rs
-from layer_harness import Linear
+from layer_harness import BAR32, Linear, f64, near
 
 pytestmark = pytest.mark.gpu
 
@@ -13,7 +13,7 @@ LENS = [300, 0, 257, 1, 320, 64, 0, 299]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("H,Hk,dk,dv", [(32, 2, 32, 64), (12, 4, 64, 256)])
+@pytest.mark.parametrize("H,Hk,dk,dv", [(32, 2, 32, 64), (12, 4, 64, 256), (15, 5, 16, 256)])
 def test_many_segments_of_shared_keys(dtype, H, Hk, dk, dv):
     b = Linear(LENS, H=H, Hk=Hk, dk=dk, dv=dv, dtype=dtype, seed=30, room=9)
     assert (b.T // 64 + b.N) * Hk >= 40
@@ -25,6 +25,9 @@ def test_many_segments_of_shared_keys(dtype, H, Hk, dk, dv):
     assert (out[b.used:] == 7.0).all()
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert (r[n][b.used:] == 7.0).all() and torch.isfinite(r[n][:b.used].float()).all(), n
+    # the skip weights' gradient: every sequence's, exactly once (fp32 sums of at most T dv terms)
+    terms = f64(b.do[:b.used]) * f64(b.v[:b.used])
+    near(r["dskip"], terms.sum((0, 2)), np.abs(terms).sum((0, 2)), "f32", BAR32)
     # alone, with the tables' room of its own, each sequence's gradients are the same bits
     starts = np.cumsum([0] + LENS)
     for s in (0, 4):
