@@ -606,7 +606,7 @@ struct Work {
     chunk = uniform(j % d.chunks);
   }
 };
-// Workgroups for `pairs` pairs: of whole rounds of the dies, so that the last ones may find no pair.
+// Workgroups for `pairs` pairs: a whole number of turns of the dies, so that the last ones may find no pair.
 inline unsigned grid_of(Deal& d, int64_t pairs) {
   d.dies = d.chunks > 1 && pairs >= 64 ? 8 : 1;
   return (unsigned)((pairs + d.dies - 1) / d.dies * d.dies * d.chunks);

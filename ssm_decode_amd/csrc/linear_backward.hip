@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kMaxWaves<T> * 64, kMaxWaves<T> / 4) linear_ke
   const Side& d = p.d;
   const Work work(p.deal);
   const int part = work.chunk, hk = uniform(work.pair % a.Hk), b = uniform(work.pair / a.Hk);
-  if (b >= a.max_segments) return;  // (pairs are dealt to whole rounds of the dies)
+  if (b >= a.max_segments) return;  // (a grid is a whole number of turns of the dies)
   const Segment seg = linear_segment(a, b);
   const int waves = p.deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
