@@ -30,9 +30,10 @@ namespace rs {
 namespace {
 
 // Tiles of 16 state rows of a wavefront of linear_keys, and wavefronts of a workgroup (a head of 256 rows). bf16: four tiles and one
-// wavefront a SIMD with all its registers, so that a block's pairs serve twice the rows. Types of several parts hold operands
-// in too many registers for that: two tiles, two wavefronts. (bf16 with two: 1759 us against
-// 1442 for all of a training batch's gradients, before the steps that brought them to 1034.)
+// wavefront a SIMD with all its registers, so that a block's pairs serve twice the rows (with two tiles 1759 us against
+// 1442 for all of a training batch's gradients, before the steps that brought them to 1034). Types of several parts: two tiles and two
+// wavefronts. (fp16 with four, which at 128 key channels has 260 bytes a lane in memory: the training batch 706 + 663 us against 755 +
+// 786 with two, the two directions of 1501 tokens in seven sequences, which wait for their few wavefronts, 38 + 23 against 27 + 19.)
 template <typename T>
 constexpr int kKeyTiles = sizeof(T) == 2 && Parts<T>::in == 1 ? 4 : 2;
 template <typename T>
