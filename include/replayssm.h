@@ -617,7 +617,8 @@ typedef struct replayssm_conv_prompt_config {
   int64_t x_stride;
 } replayssm_conv_prompt_config;
 
-/* Bytes of the backward call's workspace. Host only. */
+/* Bytes of the backward call's workspace (at most 20 MiB): never fewer for more tokens, so that one workspace made for the
+ * largest batch serves the smaller ones. Host only. */
 int replayssm_conv_prompt_sizes(const replayssm_conv_prompt_config* cfg, int64_t* backward_bytes);
 
 /* y [n_tokens][D] from x [n_tokens][D], w [D][W], bias [D] (NULL: 0) and the windows `first` in front of the sequences

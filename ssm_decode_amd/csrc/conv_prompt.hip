@@ -354,14 +354,18 @@ ConvPlan conv_plan(int64_t n_tokens, int D) {
 }
 
 // Backward: at most two thousand workgroups in all, each of which writes one row of weights' gradients per channel.
+int conv_backward_groups(int64_t n_tokens, int D, int run) {
+  const int64_t columns = (D + 511) / 512;
+  const int64_t all = (n_tokens + run * kConvWaves - 1) / (run * kConvWaves);
+  int64_t most = 2048 / columns;
+  if (most < 1) most = 1;
+  return (int)(all < most ? all : most);
+}
 ConvPlan conv_backward_plan(int64_t n_tokens, int D) {
   const int64_t columns = (D + 511) / 512;
   ConvPlan p;
   p.run = n_tokens / 64 * columns >= 2048 ? 64 : n_tokens / 32 * columns >= 2048 ? 32 : kAhead;
-  const int64_t all = (n_tokens + p.run * kConvWaves - 1) / (p.run * kConvWaves);
-  int64_t most = 2048 / columns;
-  if (most < 1) most = 1;
-  p.groups = (int)(all < most ? all : most);
+  p.groups = conv_backward_groups(n_tokens, D, p.run);
   return p;
 }
 
@@ -421,8 +425,10 @@ __global__ void __launch_bounds__(256) conv_restore_kernel(const ConvRestoreArgs
 
 }  // namespace
 
+// Room for the shortest runs, whatever the plan takes: a batch of fewer tokens, whose shorter runs are more workgroups, has
+// room in the workspace of a larger one (20 MiB at most).
 int64_t conv_prompt_backward_bytes(const replayssm_conv_prompt_config& c) {
-  return (int64_t)conv_backward_plan(c.n_tokens, c.D).groups * (c.W + 1) * c.D * 4;
+  return (int64_t)conv_backward_groups(c.n_tokens, c.D, kAhead) * (c.W + 1) * c.D * 4;
 }
 
 hipError_t launch_conv_prompt(const ConvPromptArgs& a, hipStream_t s) { return conv_prompt(a, false, s); }
