@@ -624,9 +624,9 @@ int replayssm_conv_prompt_sizes(const replayssm_conv_prompt_config* cfg, int64_t
 /* y [n_tokens][D] from x [n_tokens][D], w [D][W], bias [D] (NULL: 0) and the windows `first` in front of the sequences
  * (NULL: 0); `last` (NULL: not wanted) receives the inputs that the next tokens need: the sequence's last W - 1, those of
  * `first` among them where it has fewer tokens. maps: the tables of this batch, of any block size, with max_tokens <= n_tokens
- * (read: cu_tokens, token_seq). A sequence whose offsets fall or leave 0..n_tokens, and a token that the tables give to a
- * sequence that does not hold it, are skipped (their rows left as they were) and set REPLAYSSM_DEVERR_RANGE. Rows of tokens that
- * no sequence holds are left as they were. */
+ * (read: cu_tokens, and token_seq below the smaller of n_tokens and cu_tokens[n_seqs]). A sequence whose offsets fall or leave
+ * 0..n_tokens or pass cu_tokens[n_seqs], and a token that the tables give to a sequence that does not hold it, are skipped (their
+ * rows left as they were) and set REPLAYSSM_DEVERR_RANGE. Rows of tokens that no sequence holds are left as they were. */
 int replayssm_conv_prompt(const replayssm_conv_prompt_config* cfg, const replayssm_ragged* maps, const void* x,
                           const float* w, const float* bias, const float* first, void* y, float* last, int32_t* err,
                           void* stream);

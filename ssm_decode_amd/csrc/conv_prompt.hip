@@ -29,15 +29,22 @@ struct ConvSeq {
   int s, begin, end;
 };
 
+// Tokens that the tables hold: token_seq has no entries behind them where the tables have room for fewer than n_tokens.
+__device__ __forceinline__ int64_t conv_tokens(const ConvPromptArgs& a) {
+  const int held = a.cu_tokens[a.n_seqs];
+  return held < a.n_tokens ? (held > 0 ? held : 0) : a.n_tokens;
+}
+
 // (t is uniform over the wavefront, and so is everything read here.)
-__device__ __forceinline__ bool conv_seq(const ConvPromptArgs& a, int64_t t, ConvSeq& q) {
+__device__ __forceinline__ bool conv_seq(const ConvPromptArgs& a, int64_t held, int64_t t, ConvSeq& q) {
+  if (t >= held) return false;
   q.s = a.token_seq[t];
   if (q.s < 0) return false;
   bool ok = q.s < a.n_seqs;
   if (ok) {
     q.begin = a.cu_tokens[q.s];
     q.end = a.cu_tokens[q.s + 1];
-    ok = q.begin >= 0 && (int64_t)q.begin <= t && t < (int64_t)q.end && (int64_t)q.end <= a.n_tokens;
+    ok = q.begin >= 0 && (int64_t)q.begin <= t && t < (int64_t)q.end && (int64_t)q.end <= held;
   }
   if (!ok && (threadIdx.x & 63) == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
   return ok;
@@ -95,7 +102,7 @@ struct ConvThread {
 template <typename T, int W>
 __device__ __forceinline__ void conv_window(const ConvPromptArgs& a, int s, int unit) {
   ConvSeq q{s, a.cu_tokens[s], a.cu_tokens[s + 1]};
-  if (q.begin < 0 || q.end < q.begin || (int64_t)q.end > a.n_tokens) {
+  if (q.begin < 0 || q.end < q.begin || (int64_t)q.end > conv_tokens(a)) {
     if (unit == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
     return;
   }
@@ -132,7 +139,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPro
   T* y = static_cast<T*>(a.y) + th.c;
   f32x8 h[W];
   ConvSeq q;
-  bool ok = conv_seq(a, t0, q);
+  const int64_t held = conv_tokens(a);
+  bool ok = conv_seq(a, held, t0, q);
   if (ok) th.history(q, (int)(t0 - q.begin), h);
   Eight<T> next[kAhead];
   const auto fetch = [&](int64_t t) {
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPro
     for (int i = 0; i < kAhead; ++i) {
       if (t + i < t1) {
         if (t + i > t0 && (!ok || t + i >= q.end)) {
-          ok = conv_seq(a, t + i, q);
+          ok = conv_seq(a, held, t + i, q);
           if (ok) th.history(q, (int)(t + i - q.begin), h);
         }
         if (ok) {
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPro
 template <typename T, int W, bool SILU>
 __device__ __forceinline__ void conv_dfirst(const ConvPromptArgs& a, int s, int unit) {
   const ConvSeq q{s, a.cu_tokens[s], a.cu_tokens[s + 1]};
-  if (q.begin < 0 || q.end < q.begin || (int64_t)q.end > a.n_tokens) {
+  if (q.begin < 0 || q.end < q.begin || (int64_t)q.end > conv_tokens(a)) {
     if (unit == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
     return;
   }
@@ -223,13 +231,14 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
   f32x8 dw[W], db{};
 #pragma unroll
   for (int j = 0; j < W; ++j) dw[j] = f32x8{};
+  const int64_t held = conv_tokens(a);
   // runs of this wavefront
   for (int64_t t0 = ((int64_t)group * kConvWaves + wave) * run; t0 < a.n_tokens; t0 += (int64_t)run_groups * kConvWaves * run) {
     const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
     int64_t at = t0;
     while (at < t1) {
       ConvSeq q;
-      if (!conv_seq(a, at, q)) {
+      if (!conv_seq(a, held, at, q)) {
         ++at;
         continue;
       }

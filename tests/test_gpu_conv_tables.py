@@ -28,3 +28,46 @@ def test_gradients_with_less_room_stay_in_their_workspace():
     want = e.backward()
     for n in want:
         assert torch.equal(r[n][:room] if n == "dx" else r[n], want[n]), n
+
+
+def _tables(c, room):
+    """Tables of room for `room` tokens as a C caller has them, in front of entries that are none of theirs."""
+    m = rs.RaggedMaps(rs.make_ragged_config(c.N, room, 64))
+    rs.ragged_maps(m.cfg, m.struct, torch.tensor(c.lens, dtype=torch.int32, device="cuda"))
+    m.wide = torch.zeros(c.T, dtype=torch.int32, device="cuda")
+    m.wide[:room] = m.token_seq
+    return m, rs.Ragged(m.cu_tokens.data_ptr(), m.cu_blocks.data_ptr(), m.wide.data_ptr(), m.token_pos.data_ptr(), m.block_seq.data_ptr(),
+                        m.err.data_ptr())
+
+
+class _Struct:
+    def __init__(self, struct):
+        self.struct = struct
+
+
+@pytest.mark.parametrize("lens,room", [([20, 20], 40), ([20, 5], 40), ([0, 0], 1), ([900, 64], 1000)])
+def test_entries_behind_the_tables_are_not_read(lens, room):
+    """What lies behind token_seq's max_tokens entries names a sequence, which would be flagged."""
+    T = room + 100
+    c = Conv(lens, D=64, dtype="bf16", seed=21, room=T - sum(lens))
+    keep, struct = _tables(c, room)
+    y, last = c.forward(maps=_Struct(struct))
+    r = c.backward(maps=_Struct(struct))
+    assert c.err[0] == 0 and (y[c.used:] == 7.0).all() and (r["dx"][c.used:] == 7.0).all()
+    c.check_forward(y, last)
+    c.check_backward(r)
+
+
+def test_a_total_that_falls_takes_the_sequences_behind_it():
+    c = Conv([20, 30, 10], D=64, dtype="bf16", seed=22)
+    y, last = c.forward()
+    dx = c.backward()["dx"]
+    e = Conv([20, 30, 10], D=64, dtype="bf16", seed=22)
+    m = e.maps()
+    m.cu_tokens[3] = 45
+    z, end = e.forward(maps=m)
+    r = e.backward(maps=m, want=("dfirst",))
+    assert e.err[0] == rs.DEVERR_RANGE
+    assert torch.equal(z[:20], y[:20]) and (z[20:] == 7.0).all()
+    assert torch.equal(r["dx"][:20], dx[:20]) and (r["dx"][20:] == 7.0).all()
+    assert torch.equal(end[0], last[0]) and (end[1:] == 7.0).all() and (r["dfirst"][1:] == 7.0).all()
