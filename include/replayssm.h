@@ -626,7 +626,8 @@ int replayssm_conv_prompt_sizes(const replayssm_conv_prompt_config* cfg, int64_t
  * `first` among them where it has fewer tokens. maps: the tables of this batch, of any block size, with max_tokens <= n_tokens
  * (read: cu_tokens, and token_seq below the smaller of n_tokens and cu_tokens[n_seqs]). A sequence whose offsets fall or leave
  * 0..n_tokens or pass cu_tokens[n_seqs], and a token that the tables give to a sequence that does not hold it, are skipped (their
- * rows left as they were) and set REPLAYSSM_DEVERR_RANGE. Rows of tokens that no sequence holds are left as they were. */
+ * rows left as they were; the other tokens' rows and the windows see its input as before) and set REPLAYSSM_DEVERR_RANGE. Rows of tokens
+ * that no sequence holds, or whose entry of token_seq is negative, are left as they were. */
 int replayssm_conv_prompt(const replayssm_conv_prompt_config* cfg, const replayssm_ragged* maps, const void* x,
                           const float* w, const float* bias, const float* first, void* y, float* last, int32_t* err,
                           void* stream);
@@ -634,7 +635,7 @@ int replayssm_conv_prompt(const replayssm_conv_prompt_config* cfg, const replays
 /* Gradients: from dy [n_tokens][D] and dlast (of `last`; NULL: 0) to dx [n_tokens][D] in `dtype`, dw [D][W], dbias [D] and
  * dfirst (of `first`), fp32; dw, dbias and dfirst may be NULL: not wanted. x, w, bias and `first` are those of the forward
  * call. workspace: replayssm_conv_prompt_sizes bytes, used when dw or dbias is wanted. Sums have a fixed order: equal calls give
- * equal bits. Rows and sequences are skipped as in the forward call. */
+ * equal bits. Rows and sequences are skipped as in the forward call: a skipped row's dy takes no part. */
 int replayssm_conv_prompt_backward(const replayssm_conv_prompt_config* cfg, const replayssm_ragged* maps, const void* x,
                                    const float* w, const float* bias, const float* first, const void* dy, const float* dlast,
                                    void* dx, float* dw, float* dbias, float* dfirst, void* workspace, int32_t* err,

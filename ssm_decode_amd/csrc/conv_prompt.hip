@@ -8,7 +8,8 @@
 // a run of tokens with the last W - 1 inputs in registers, the rows of the next kAhead tokens already asked for; a wavefront
 // covers 512 channels, so each of its loads is one KiB. A run reads the W - 1 rows in front of it again (and, backward, the W - 1
 // behind it). Runs are cut from the packed batch, whatever the sequences' lengths; where a run passes from one sequence to the
-// next its history is loaded anew, a branch that a whole wavefront takes. SiLU and its slope are computed again in the
+// next its history is loaded anew, a branch that a whole wavefront takes. Its lanes read the tokens' sequences together, 64 at a
+// time, so that every token's entry is looked at. SiLU and its slope are computed again in the
 // backward pass from x, which costs less than storing s. Weights' gradients are summed over a run in registers, over a
 // workgroup's wavefronts in LDS and over workgroups by a second kernel, in a fixed order.
 #include "act.hpp"
@@ -24,9 +25,10 @@ constexpr int kAhead = 8, kAheadBack = 4;
 constexpr int kConvWaves = 4;    // of a workgroup, each with a run of its own
 constexpr int kConvThreads = kConvWaves * 64;
 
-// A sequence of the packed batch that holds token t, as the tables have it.
+// Sequence s of the packed batch; it holds no token where the tables are wrong.
 struct ConvSeq {
   int s, begin, end;
+  __device__ __forceinline__ bool holds(int64_t t) const { return begin <= t && t < end; }
 };
 
 // Tokens that the tables hold: token_seq has no entries behind them where the tables have room for fewer than n_tokens.
@@ -35,19 +37,18 @@ __device__ __forceinline__ int64_t conv_tokens(const ConvPromptArgs& a) {
   return held < a.n_tokens ? (held > 0 ? held : 0) : a.n_tokens;
 }
 
-// (t is uniform over the wavefront, and so is everything read here.)
-__device__ __forceinline__ bool conv_seq(const ConvPromptArgs& a, int64_t held, int64_t t, ConvSeq& q) {
-  if (t >= held) return false;
-  q.s = a.token_seq[t];
-  if (q.s < 0) return false;
-  bool ok = q.s < a.n_seqs;
-  if (ok) {
-    q.begin = a.cu_tokens[q.s];
-    q.end = a.cu_tokens[q.s + 1];
-    ok = q.begin >= 0 && (int64_t)q.begin <= t && t < (int64_t)q.end && (int64_t)q.end <= held;
-  }
-  if (!ok && (threadIdx.x & 63) == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
-  return ok;
+// (s is uniform over the wavefront, and so is everything read here.)
+__device__ __forceinline__ ConvSeq conv_seq(const ConvPromptArgs& a, int64_t held, int s) {
+  ConvSeq q{s, 0, 0};
+  if (s < 0 || s >= a.n_seqs) return q;
+  const int begin = a.cu_tokens[s], end = a.cu_tokens[s + 1];
+  if (begin >= 0 && (int64_t)end <= held) q.begin = begin, q.end = end;
+  return q;
+}
+
+// A token that the tables give to sequence s, which does not hold it.
+__device__ __forceinline__ void conv_flag(const ConvPromptArgs& a, int s) {
+  if (s >= 0 && (threadIdx.x & 63) == 0) atomicOr(a.err, REPLAYSSM_DEVERR_RANGE);
 }
 
 template <typename T, int W>
@@ -131,17 +132,16 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPro
     if (s < a.n_seqs) conv_window<T, W>(a, s, unit);
     return;
   }
-  const int64_t t0 = ((int64_t)group * kConvWaves + wave) * run;
-  const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
+  const int64_t held = conv_tokens(a), t0 = ((int64_t)group * kConvWaves + wave) * run;
+  const int64_t t1 = t0 + run < held ? t0 + run : held;
   if (t0 >= t1) return;
   const bool live = 8 * unit < a.D;
   const ConvThread<T, W> th(a, live ? 8 * unit : a.D - 8);
   T* y = static_cast<T*>(a.y) + th.c;
   f32x8 h[W];
-  ConvSeq q;
-  const int64_t held = conv_tokens(a);
-  bool ok = conv_seq(a, held, t0, q);
-  if (ok) th.history(q, (int)(t0 - q.begin), h);
+  ConvSeq q{-1, 0, 0};
+  bool walks = false;  // h holds the inputs in front of the next token
+  int owner = -1;      // lane i: of the i-th of 64 tokens
   Eight<T> next[kAhead];
   const auto fetch = [&](int64_t t) {
 #pragma unroll
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPro
   };
   fetch(t0);
   for (int64_t t = t0; t < t1; t += kAhead) {
+    if (((t - t0) & 63) == 0) owner = t + (threadIdx.x & 63) < t1 ? a.token_seq[t + (threadIdx.x & 63)] : -1;
     Eight<T> now[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) now[i] = next[i];
@@ -156,18 +157,24 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_kernel(const ConvPro
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (t + i < t1) {
-        if (t + i > t0 && (!ok || t + i >= q.end)) {
-          ok = conv_seq(a, held, t + i, q);
-          if (ok) th.history(q, (int)(t + i - q.begin), h);
+        const int s = __builtin_amdgcn_readlane(owner, (int)(t - t0 + i) & 63);
+        if (s != q.s) {
+          q = conv_seq(a, held, s);
+          walks = false;
         }
-        if (ok) {
+        if (!q.holds(t + i)) {
+          conv_flag(a, s);
+          walks = false;
+        } else {
+          if (!walks) th.history(q, (int)(t + i - q.begin), h);
+          walks = true;
           h[W - 1] = wide(now[i]);
-          f32x8 s = th.mix(h);
+          f32x8 z = th.mix(h);
           if (SILU) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] *= sigmoid<sizeof(T) == 4>(s[e]);
+            for (int e = 0; e < 8; ++e) z[e] *= sigmoid<sizeof(T) == 4>(z[e]);
           }
-          if (live) store8(y + (t + i) * a.D, s);
+          if (live) store8(y + (t + i) * a.D, z);
           th.shift(h);
         }
       }
@@ -195,11 +202,14 @@ __device__ __forceinline__ void conv_dfirst(const ConvPromptArgs& a, int s, int 
   for (int p = 0; p < W - 1; ++p) {
     if (p < n) {
       h[W - 1] = th.input(q, p);
-      f32x8 e = wide(raw8(dy + ((int64_t)q.begin + p) * a.D));
-      if (SILU) {
-        const f32x8 z = th.mix(h);
+      f32x8 e{};
+      if (a.token_seq[q.begin + p] == s) {
+        e = wide(raw8(dy + ((int64_t)q.begin + p) * a.D));
+        if (SILU) {
+          const f32x8 z = th.mix(h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] *= silu<sizeof(T) == 4>(z[i]).slope;
+          for (int i = 0; i < 8; ++i) e[i] *= silu<sizeof(T) == 4>(z[i]).slope;
+        }
       }
       th.shift(h);
 #pragma unroll
@@ -234,16 +244,23 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
   const int64_t held = conv_tokens(a);
   // runs of this wavefront
   for (int64_t t0 = ((int64_t)group * kConvWaves + wave) * run; t0 < a.n_tokens; t0 += (int64_t)run_groups * kConvWaves * run) {
-    const int64_t t1 = t0 + run < a.n_tokens ? t0 + run : a.n_tokens;
+    const int64_t t1 = t0 + run < held ? t0 + run : held;
     int64_t at = t0;
     while (at < t1) {
-      ConvSeq q;
-      if (!conv_seq(a, held, at, q)) {
+      const int s = a.token_seq[at];
+      const ConvSeq q = conv_seq(a, held, s);
+      if (!q.holds(at)) {
+        conv_flag(a, s);
         ++at;
         continue;
       }
-      // tokens at .. to - 1 of sequence q: their dx, and their part of the weights' gradients
-      const int64_t to = t1 < q.end ? t1 : q.end;
+      // the tokens from here on, the run's and W - 1 more, that both tables give to sequence q (bit j: token at + j)
+      const uint64_t own = __builtin_amdgcn_ballot_w64(at + lane < q.end && a.token_seq[at + lane < q.end ? at + lane : at] == s);
+      const uint64_t more = __builtin_amdgcn_ballot_w64(lane < W - 1 && at + 64 + lane < q.end && a.token_seq[at + 64 + lane < q.end ? at + 64 + lane : at] == s);
+      // at .. to - 1: their dx, and their part of the weights' gradients; behind: of the W - 1 tokens that follow, whose dy reaches them
+      const int ones = own + 1 ? __builtin_ctzll(~own) : 64, n = (int)(t1 - at) < ones ? (int)(t1 - at) : ones;
+      const int64_t to = at + n;
+      const uint64_t behind = n < 64 ? own >> n | more << (64 - n) : more;
       f32x8 h[W], e[W];  // e[W - 1]: of the newest token
       th.history(q, (int)(at - q.begin), h);
 #pragma unroll
@@ -285,6 +302,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
                 for (int j = 0; j < W; ++j)
 #pragma unroll
                   for (int c = 0; c < 8; ++c) dw[j][c] = __builtin_fmaf(g[c], h[j][c], dw[j][c]);
+              } else if (!(behind >> (t + i - to) & 1)) {
+                g = f32x8{};
               }
               th.shift(h);
             }

@@ -71,3 +71,54 @@ def test_a_total_that_falls_takes_the_sequences_behind_it():
     assert torch.equal(z[:20], y[:20]) and (z[20:] == 7.0).all()
     assert torch.equal(r["dx"][:20], dx[:20]) and (r["dx"][20:] == 7.0).all()
     assert torch.equal(end[0], last[0]) and (end[1:] == 7.0).all() and (r["dfirst"][1:] == 7.0).all()
+
+
+def _one_entry(c, entries):
+    """The batch's tables with some tokens given to other sequences; what both calls give must be what good tables give where those
+    rows' dy is zero, but for the rows, which stay as they were."""
+    owners = c.maps().token_seq.tolist()
+    wrong = {t: s for t, s in entries.items() if s != owners[t]}  # (the others say what the tables said)
+    rows = torch.tensor(sorted(wrong), dtype=torch.int64, device="cuda")
+    y, last = c.forward()
+    kept, c.dy = c.dy, c.dy.clone()
+    c.dy[rows] = 0
+    want = c.backward()
+    c.dy = kept
+    m = c.maps()
+    for t, s in entries.items():
+        m.token_seq[t] = s
+    assert c.err[0] == 0
+    z, end = c.forward(maps=m)
+    flag = rs.DEVERR_RANGE if any(s >= 0 for s in wrong.values()) else 0
+    assert c.err[0] == flag, entries
+    c.err.zero_()
+    r = c.backward(maps=m)
+    assert c.err[0] == flag, entries
+    y[rows] = 7.0
+    want["dx"][rows] = 7.0
+    assert torch.equal(z, y) and torch.equal(end, last), entries
+    for n in want:
+        assert torch.equal(r[n], want[n]), (entries, n)
+
+
+# (runs of eight tokens, of which the first token of one, one inside, one at its end; the first and the last of a sequence)
+@pytest.mark.parametrize("entries", [{8: 1}, {11: 0}, {15: 9}, {0: 1}, {1: -1}, {99: 0}, {100: 0}, {102: -1}, {129: 0}, {12: 1, 13: 1, 14: 2}, {64: 2 ** 31 - 1},
+                                     {20: -2 ** 31}, {t: 2 for t in range(30, 101)}])
+@pytest.mark.parametrize("dtype,W", [("bf16", 4), ("f32", 2), ("f16", 3)])
+def test_single_entries_of_other_sequences(entries, dtype, W):
+    _one_entry(Conv([100, 30, 0, 7], D=72, W=W, dtype=dtype, seed=23), entries)
+
+
+def test_single_entries_in_the_longest_runs():
+    """Runs of 64 tokens backwards, 32 forwards; entries at their ends, and among the tokens that the run in front looks ahead to."""
+    for entries in ({63: 1}, {64: 0, 66: -1, 67: 0}, {62: 1, 64: 1, 65: -1}, {127: 5, 131: 0}, {600: 1, 601: 0}, {1024: 0}):
+        _one_entry(Conv([601, 1, 700], D=131072, dtype="bf16", seed=24, lead=0), entries)
+
+
+def test_an_entry_inside_a_run_keeps_non_finite_rows_to_themselves():
+    c = Conv([100, 30], D=64, dtype="f32", seed=25)
+    m = c.maps()
+    m.token_seq[50] = -1
+    c.dy[50] = float("nan")
+    r = c.backward(maps=m)
+    assert torch.isfinite(r["dx"]).all() and torch.isfinite(r["dw"]).all() and torch.isfinite(r["dfirst"]).all()
