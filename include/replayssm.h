@@ -698,7 +698,7 @@ int replayssm_linear_sizes(const replayssm_linear_config* cfg, int64_t* forward_
  * not wanted; may be S0). workspace: forward_bytes of replayssm_linear_sizes (may be NULL if that is 0), free again when the call's
  * work is done. A sequence whose tables contradict each other or leave the arrays is skipped (out and S_out are left as they
  * were) and REPLAYSSM_DEVERR_RANGE set in err, as by replayssm_delta_prompt. For one configuration results do not depend on
- * what else is in the batch, to the bit. */
+ * what else is in the batch, nor on which of them are wanted, to the bit. */
 int replayssm_linear_prompt(const replayssm_linear_config* cfg, const replayssm_ragged* maps, const void* q, const void* k,
                             const void* v, const float* g, const float* beta, const float* skip, const float* S0, void* out,
                             float* S_out, void* workspace, int32_t* err, void* stream);

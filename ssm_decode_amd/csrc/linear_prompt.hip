@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
   if (!seg.ok) return;
   const int waves = deal.waves, threads = waves * 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
   const Place at = place_of<kTiles>(a, deal, hk, chunk, wave);
   char* now = lds;
   const bool ahead = L::buffers(waves) == 2;
@@ -296,12 +295,8 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
         for (int m = 0; m < kM; ++m)
           if (16 * m < at.columns) store4(to + 16 * m, acc[m][rt]);
       }
-    // The state behind the block: in 24 bits where it is a result, in those of the outputs otherwise.
-    const float whole = decay_of(end);
-    if (keep)
-      state.template update<kMid>(whole, yr, z, rows->last);
-    else if (more)
-      state.template update<low>(whole, yr, z, rows->last);
+    // The state behind the block, in 24 bits whether or not it is asked for: what is wanted changes no other result.
+    if (keep || more) state.template update<kMid>(decay_of(end), yr, z, rows->last);
     if (!more) break;
     if (!ahead) {
       __syncthreads();
