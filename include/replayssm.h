@@ -660,8 +660,8 @@ int replayssm_conv_restore(const replayssm_conv_config* cfg, const replayssm_con
  * `segment` (prompt calls): sequences are cut into segments of so many tokens, which are computed in parallel from states
  * that a first pass finds; a multiple of REPLAYSSM_DELTA_BLOCK up to 65536. replayssm_linear_segment gives one that suits the
  * sizes. H * (n_tokens / segment + n_seqs) * ceil(dv / 32) <= 2^23.
- * Sums and states are fp32. In the prompt calls the operands of products are held in 24 bits on the way to states and fp32
- * gradients, and with fp32 inputs to all results; what goes into 16-bit results alone is held in 17 bits before it is summed.
+ * Sums and states are fp32. In the prompt calls the operands of products are held in 24 bits, but for two that go into 16-bit
+ * results alone and are held in 17 bits before they are summed: the state where out and dv multiply it, and the pairs of dq and dk.
  * Rows of out of tokens that no sequence holds are left as they were. A non-finite input may reach every later token of its
  * sequence, and in the prompt calls the earlier tokens of its block of 64 too; other sequences are not touched. */
 typedef struct replayssm_linear_config {

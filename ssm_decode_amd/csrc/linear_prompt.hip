@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
                                                                        void* outs, const Deal deal) {
   constexpr int in = Parts<T>::in, low = Parts<T>::low;
   constexpr int kK = kWide<DK> / 32, kM = kTiles;
+  constexpr int kWhole = 2 * in - 1 > kMid ? kMid : 2 * in - 1;  // products of inputs: all (fp32: to 24 bits)
   using L = OutLds<T, DK>;
   extern __shared__ __align__(16) char lds[];
   const Work work(deal);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
       const int c = q < 8 ? q >> 2 : 2 + ((q - 8) >> 1), rt = q < 8 ? q & 3 : 2 + ((q - 8) & 1);
       f32x4 t{};
 #pragma unroll
-      for (int k = 0; k < kK; ++k) t = mma(yr.dealt_row(c, k), xr.row(rt, k), t);
+      for (int k = 0; k < kK; ++k) t = mma_to<kWhole>(yr.dealt_row(c, k), xr.row(rt, k), t);
       st4(scores + (q * 64 + lane) * 4, t);
     }
     // what the state gives
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kWaves<T> * 64, 2) linear_out_kernel(const Lin
             p.hi[e] += 4 + e == diagonal + 16 * (rt & 1) ? skip : 0.f;
           }
         }
-        const Split<low> P = parts<low>(p);
+        const Split<kMid> P = parts<kMid>(p);
 #pragma unroll
         for (int m = 0; m < kM; ++m) acc[m][rt] = mma(parts_of(z[m][ks]), P, acc[m][rt]);
       }
