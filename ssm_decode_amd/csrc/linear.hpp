@@ -80,7 +80,7 @@ __device__ __forceinline__ Segment linear_sequence(const LinearArgs& a, int s, i
   return r;
 }
 
-// Segment b of the batch. (linear_join, which looks at every sequence, flags what is bad.)
+// Segment b of the batch. (linear_out's last workgroups, which look at every sequence, flag what is bad: linear_empty.)
 __device__ __forceinline__ Segment linear_segment(const LinearArgs& a, int b) {
   Segment r{};
   if (b >= linear_segments(a)) return r;
@@ -111,7 +111,6 @@ struct Blocks {
     t0 += reverse ? -kRows : kRows;
     size();
   }
-  __device__ __forceinline__ bool final() const { return reverse ? t0 == lo : t0 + kRows >= hi; }
   // token of a row
   __device__ __forceinline__ int64_t token(int r) const { return reverse ? t0 + n - 1 - r : t0 + r; }
 };
