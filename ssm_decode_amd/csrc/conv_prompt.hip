@@ -4,7 +4,7 @@
 //     e_t = dy_t act'(s_t),  dx_t = sum_n e_{t+n} w[W-1-n] (tokens of the sequence),  dw[j] = sum_t e_t x_{t-W+1+j}
 //
 // Bound by memory: x is read once and y written once (216 us and 3.8 TB/s on 24 ragged prompts of 20011 tokens, 10240 channels, bf16;
-// gradients on 16384 tokens 229 us and 4.4 TB/s, where a large copy reaches 4.8). A thread owns eight channels (16 bytes of a 16-bit row) and walks
+// gradients on 16384 tokens 232 us and 4.3 TB/s, where a large copy reaches 4.8). A thread owns eight channels (16 bytes of a 16-bit row) and walks
 // a run of tokens with the last W - 1 inputs in registers, the rows of the next kAhead tokens already asked for; a wavefront
 // covers 512 channels, so each of its loads is one KiB. A run reads the W - 1 rows in front of it again (and, backward, the W - 1
 // behind it). Runs are cut from the packed batch, whatever the sequences' lengths; where a run passes from one sequence to the

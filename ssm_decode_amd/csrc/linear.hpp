@@ -17,9 +17,12 @@
 // The kernels therefore take a `Side`: which arrays are walked, in which direction. A row of a block is a place in walking
 // order: row r is token t0 + r, or t0 + rows - 1 - r backwards (blocks and segments are cut the same way for both).
 //
-// Precision is that of the delta rule's kernels (chunk.hpp): operands of products on the way to states and fp32
-// gradients in 24 bits, those of 16-bit results in 17; decay exponents are summed in fp64, since e^{G_r - G_c} takes
-// differences of long sums.
+// Precision: operands of products are held in 24 bits (three bf16 parts, see chunk.hpp), but for two that go into 16-bit results alone
+// and have 17: the state where out and dv multiply it, and the pairs of dq and dk. The pairs of out and dv have 24: the skip weight lies
+// on their diagonal, and cut to 17 bits it moves all outputs of its head alike (a long prompt's outputs 1.0e-4 off those of fp32
+// products in place of 3.5e-5, for 812 us in place of 845). Three parts of the state too would be 1.7e-5 off and cost 895 us; of the pairs
+// of dq and dk, 8e-5 off now, 50 us of a training batch's 1044, with registers in memory at 128 key channels. Decay exponents are
+// summed in fp64, since e^{G_r - G_c} takes differences of long sums.
 #pragma once
 
 #include <type_traits>
@@ -38,10 +41,11 @@ template <int M>
 constexpr int kSlice = 16 * M;
 // States and outputs: two tiles. (With four, which would share a block's pairs among twice the rows, the state and a block's
 // results leave no registers for two wavefronts a SIMD; with one wavefront of 512 registers the outputs took a fifth longer, 750 us
-// against 617 on 32768 tokens of 128 heads of 64 by 128 in bf16.)
+// against 617 on 32768 tokens of 128 heads of 64 by 128 in bf16, when pairs had two parts.)
 constexpr int kTiles = 2;
 // Wavefronts of a workgroup, which share their key head's rows and scores: all that fit LDS beside them. (Four for the outputs of the
-// same batch: 780 us against 720, rows and scores twice.)
+// same batch, with two buffers each, of which one workgroup fills a compute unit: 780 us against 720, rows and scores twice, when pairs
+// had two parts.)
 template <typename T>
 constexpr int kWaves = sizeof(T) == 4 ? 4 : 8;
 

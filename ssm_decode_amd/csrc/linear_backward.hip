@@ -17,8 +17,9 @@
 // rho - sum x' + sum x. It starts at a segment's end as e^{g} <S, dS> of the states there, so that rounding does not pile up over a
 // long sequence.
 //
-// linear_keys is bound by the issue of vector instructions too: per block and wavefront 504 matrix instructions (8000 cycles) and 4500
-// others. Everything that a lane needs once a block (addresses above all) is made again from the lane's number: kept over the
+// linear_keys waits: its one wavefront a SIMD has a vector instruction under way for 36 to 40 % of the time (504 to 516 matrix instructions
+// of 16 cycles and about 4000 others for a block of 48000 cycles) and waits for 33 to 39 %, at the ring's barriers and for operands from
+// LDS, with no second wavefront to go on. Everything that a lane needs once a block (addresses above all) is made again from the lane's number: kept over the
 // loop it passed the 512 registers, and a register read back from memory waits for the copies in flight as well (507 us
 // against 394 for one direction, 16384 tokens of 64 heads of 64 by 128 in bf16; 346 forwards and 317 back with results in the
 // lower registers). Sums over value heads go through LDS in a ring, in a fixed order, without atomics.
@@ -31,7 +32,7 @@ namespace {
 
 // Tiles of 16 state rows of a wavefront of linear_keys, and wavefronts of a workgroup (a head of 256 rows). bf16: four tiles and one
 // wavefront a SIMD with all its registers, so that a block's pairs serve twice the rows (with two tiles 1759 us against
-// 1442 for all of a training batch's gradients, before the steps that brought them to 1034). Types of several parts: two tiles and two
+// 1442 for all of a training batch's gradients, before the steps that brought them to 1034 and 24 bits of dv's pairs, which cost 10 of them). Types of several parts: two tiles and two
 // wavefronts. (fp16 with four, which at 128 key channels has 260 bytes a lane in memory: the training batch 706 + 663 us against 755 +
 // 786 with two, the two directions of 1501 tokens in seven sequences, which wait for their few wavefronts, 38 + 23 against 27 + 19.)
 template <typename T>

@@ -3,11 +3,12 @@
 //
 // A wavefront holds 32 rows of a head's state and walks its segment's blocks; a workgroup's wavefronts (several value heads of one
 // key head, or the slices of a wide one) share the key head's rows in LDS and its scores, of which each makes a part, and a
-// head's wavefronts its decay tables, which one of them makes. What bounds them is the issue of vector instructions: a block of 64
-// rows is 252 matrix instructions (4000 cycles of a SIMD) and about 2500 others for each of a SIMD's two wavefronts, most of them
-// taking states, weighted values and pairs apart into bf16 parts. Measured on 32768 tokens of 128 heads of 64 by 128 (8 key
-// heads) in bf16: states 252 to 294 us, outputs 596 to 645, 1.25 GB that have to pass memory in 260; 24 ragged prompts of 20011 tokens,
-// 32 heads of 128 by 128: states 67, outputs 280.
+// head's wavefronts its decay tables, which one of them makes. No part of the hardware is full: for a block of 64 rows the
+// outputs take 200 matrix instructions (16 cycles each) and about 1390 others of each of a SIMD's two wavefronts, most of them taking
+// states, weighted values and pairs apart into bf16 parts, the states 96 and 480. That is 61 and 50 % of a SIMD's time with a vector
+// instruction under way and 31 and 34 % with a matrix instruction; a third of the time a wavefront waits, at barriers and for LDS.
+// Measured on 32768 tokens of 128 heads of 64 by 128 (8 key heads) in bf16: states 251 to 276 us, outputs 644 to 707, 1.25 GB that
+// have to pass memory in 260; 24 ragged prompts of 20011 tokens, 32 heads of 128 by 128: states 64 to 66, outputs 294 to 300.
 #include "launch.hpp"
 #include "linear.hpp"
 
@@ -18,7 +19,7 @@ namespace {
 // ---- what each segment adds to the state --------------------------------------
 
 // Wavefronts of a workgroup: with four, two workgroups that wait at barriers of their own share a compute unit (262 us against 322
-// with eight, on 32768 tokens of 64 heads of 64 by 128 in bf16), at the price of a second copy of the key head's rows.
+// with eight, on 32768 tokens of 128 heads of 64 by 128 in bf16), at the price of a second copy of the key head's rows.
 constexpr int kStateWaves = 4;
 
 template <typename T, int DK>
@@ -125,7 +126,7 @@ struct OutLds {
   static constexpr int kScores = 12 * 1024;  // of the key head, fp32
   // Rows that are copied have two buffers where a workgroup fills the compute unit, one where two workgroups of four wavefronts or fewer
   // share it: each then computes while the other waits (24 ragged prompts, a key head for each of 32 heads: 340 us with two, 280 with
-  // one; with eight wavefronts both take as long).
+  // one, before the pairs had three parts; with eight wavefronts both take as long).
   static constexpr int buffers(int n) { return n > kWaves<T> / 2 ? kBuffers<T, DK> : 1; }
   static constexpr int scores(int n) { return buffers(n) * kBuffer(n); }
   static constexpr int scalars(int n) { return scores(n) + kScores; }

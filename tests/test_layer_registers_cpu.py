@@ -11,3 +11,8 @@ from test_kernel_registers_cpu import scratch  # noqa: F401
 def test_no_scratch(scratch, kernel):  # noqa: F811
     named = {k: b for k, b in scratch.items() if kernel in k}
     assert named and not {k: b for k, b in named.items() if b}
+
+
+def test_outputs_of_every_type(scratch):  # noqa: F811
+    named = {k: b for k, b in scratch.items() if "linear_out_kernel" in k}
+    assert len(named) == 12 and not {k: b for k, b in named.items() if b}
