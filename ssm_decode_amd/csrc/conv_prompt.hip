@@ -247,16 +247,18 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt_backward_kernel(cons
     const int64_t t1 = t0 + run < held ? t0 + run : held;
     int64_t at = t0;
     while (at < t1) {
-      const int s = a.token_seq[at];
+      // the sequences of the tokens from here on, the run's and W - 1 more
+      const int64_t next = at + lane;
+      const int owner = next < held ? a.token_seq[next] : -1, owner_behind = lane < W - 1 && next + 64 < held ? a.token_seq[next + 64] : -1;
+      const int s = __builtin_amdgcn_readfirstlane(owner);
       const ConvSeq q = conv_seq(a, held, s);
       if (!q.holds(at)) {
         conv_flag(a, s);
         ++at;
         continue;
       }
-      // the tokens from here on, the run's and W - 1 more, that both tables give to sequence q (bit j: token at + j)
-      const uint64_t own = __builtin_amdgcn_ballot_w64(at + lane < q.end && a.token_seq[at + lane < q.end ? at + lane : at] == s);
-      const uint64_t more = __builtin_amdgcn_ballot_w64(lane < W - 1 && at + 64 + lane < q.end && a.token_seq[at + 64 + lane < q.end ? at + 64 + lane : at] == s);
+      // those that both tables give to sequence q (bit j: token at + j)
+      const uint64_t own = __builtin_amdgcn_ballot_w64(next < q.end && owner == s), more = __builtin_amdgcn_ballot_w64(next + 64 < q.end && owner_behind == s);
       // at .. to - 1: their dx, and their part of the weights' gradients; behind: of the W - 1 tokens that follow, whose dy reaches them
       const int ones = own + 1 ? __builtin_ctzll(~own) : 64, n = (int)(t1 - at) < ones ? (int)(t1 - at) : ones;
       const int64_t to = at + n;
